@@ -11,6 +11,8 @@ Tensor conventions (all contiguous, on the current CUDA/HIP device):
   bf16 values      torch.bfloat16 (or int16/uint16 holding the bits)
   fp8 e4m3 codes   torch.uint8 (or torch.float8_e4m3fn)
   scales, weights  torch.float32;  expert ids torch.int32
+  4-bit weights    torch.uint8, two codes to a byte; their scales torch.bfloat16
+                   (int4) or torch.uint8 (mxfp4), their zero points torch.uint8
 """
 from __future__ import annotations
 
@@ -21,7 +23,7 @@ from ctypes import POINTER, c_char_p, c_int, c_int64, c_size_t, c_void_p
 
 import torch
 
-ABI_VERSION = 8
+ABI_VERSION = 9
 ENGINE_AUTO, ENGINE_SKINNY, ENGINE_TILED, ENGINE_SPLITK = 0, 1, 2, 3
 TILE_AUTO, TILE_256X256, TILE_256X128, TILE_128X64, TILE_256X64 = 0, 1, 2, 3, 4
 
@@ -76,6 +78,22 @@ def lib() -> ctypes.CDLL:
         L.r9k_gemm_fp8_block_bf16a_packed.argtypes = L.r9k_gemm_fp8_block_bf16a.argtypes
         L.r9k_gemm_fp8_block_qa_noalloc.argtypes = [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_int64,
                                                     c_void_p, c_int, c_void_p]
+        L.r9k_quant_weight_w4.argtypes = [c_void_p, c_int64, c_int64, c_int, c_int] + [c_void_p] * 4
+        L.r9k_pack_weight_w4.argtypes = [c_void_p] * 3 + [c_int64, c_int64, c_int, c_int] + [c_void_p] * 4
+        L.r9k_gemm_w4_workspace.argtypes = [c_int64, c_int64, c_int64, POINTER(c_size_t)]
+        L.r9k_gemm_w4.argtypes = [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64,
+                                  c_void_p, c_void_p, c_size_t, c_void_p]
+        L.r9k_moe_gemm_w4.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64,
+                                      c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64, c_int, c_void_p, c_void_p]
+        L.r9k_moe_permute_workspace.argtypes = [c_int64, c_int64, c_int64, POINTER(c_size_t)]
+        L.r9k_moe_permute.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int64, c_int64, c_void_p,
+                                      c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]
+        L.r9k_moe_permute_backward.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int64, c_void_p,
+                                               c_void_p]
+        L.r9k_moe_unpermute.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p, c_int64, c_void_p,
+                                        c_void_p]
+        L.r9k_moe_unpermute_backward.argtypes = [c_void_p, c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p,
+                                                 c_int64, c_void_p, c_void_p, c_void_p]
         v = L.r9k_abi_version()
         if v != ABI_VERSION:
             raise ImportError(f"libr9k.so has ABI version {v}, this binding needs {ABI_VERSION}")
@@ -412,3 +430,262 @@ def moe_fp8_decode(x, topk_ids, topk_w, w13, w13_s, w2, w2_s, out=None, workspac
               _ptr(out, BF16, "out"), _ptr(wsb, FP8, "workspace"), wsb.numel(), 1 if fused else 0, _stream(stream)),
            "r9k_moe_fp8_decode_packed" if packed else "r9k_moe_fp8_decode")
     return out
+
+
+# ------------------------------------------------------ 4-bit weights ----
+
+W4_INT, W4_MXFP4 = 0, 1
+ACT_NONE, ACT_SILU_MUL = 0, 1
+U8 = (torch.uint8,)
+_ROWS = {torch.bfloat16: 0, torch.float32: 1}  # R9K_BF16, R9K_F32
+
+
+def _dev(t: torch.Tensor, name: str) -> int:
+    """The current device's index; the call's first tensor has to be there."""
+    cur = torch.cuda.current_device() if t.is_cuda else -1
+    if t.get_device() != cur or cur < 0:
+        raise ValueError(f"{name} must be a tensor of the current device")
+    return cur
+
+
+def _addr(t: torch.Tensor, dtypes, name: str, dev: int, shape=None) -> int:
+    """Device address of a contiguous tensor of device `dev`, checked (0 for an empty one)."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor of the current device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, needs {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _raw(stream, dev: int) -> int:
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _new(shape, dtype, dev: int, stream) -> torch.Tensor:
+    """A fresh tensor for a call on `stream`, owned by that stream in torch's allocator."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _scratch(ws: torch.Tensor | None, nbytes: int, dev: int, stream):
+    """(address, bytes, tensor) of a call's workspace: the caller's, or a fresh one, which torch keeps for
+    this stream (or the graph being captured) until the call's work is done."""
+    if ws is None:
+        if nbytes == 0:
+            return None, 0, None
+        ws = _new((nbytes,), torch.uint8, dev, stream)
+    return _addr(ws, U8, "workspace", dev) or None, ws.numel(), ws
+
+
+def _w4_format(wp, sp, zp, dev: int, wname="w", sname="s", zname="z"):
+    """Addresses, format and group of a 4-bit weight [..., N, K/2] with its scales and zeros [..., N, K/group]."""
+    if wp.dim() < 2 or sp.dim() != wp.dim() or sp.shape[:-1] != wp.shape[:-1] or not sp.shape[-1]:
+        raise ValueError(f"{sname}: shape {tuple(sp.shape)} does not go with {wname} {tuple(wp.shape)}")
+    K = 2 * wp.shape[-1]
+    if K % sp.shape[-1]:
+        raise ValueError(f"{sname}: {sp.shape[-1]} groups do not divide K = {K}")
+    fmt = W4_INT if sp.dtype == torch.bfloat16 else W4_MXFP4
+    return (_addr(wp, U8, wname, dev), _addr(sp, (torch.bfloat16, torch.uint8), sname, dev),
+            None if zp is None else _addr(zp, U8, zname, dev, sp.shape), fmt, K // sp.shape[-1])
+
+
+def quant_weight_w4(w: torch.Tensor, group: int = 128, fmt: int = W4_INT, zeros: bool = False, stream=None):
+    """4-bit group quant: w [..., N, K] bf16 -> (codes [..., N, K/2] u8, scales [..., N, K/group], zeros or None).
+    W4_INT: scales bf16, zero points u8 when `zeros` (else 8 is meant); W4_MXFP4: group 32, scales u8 (e8m0)."""
+    dev = _dev(w, "w")
+    K, rows = w.shape[-1], w.numel() // max(w.shape[-1], 1)
+    if group <= 0 or K % group:
+        raise ValueError(f"K = {K} is not whole groups of {group}")
+    lead = w.shape[:-1]
+    wq = _new((*lead, K // 2), torch.uint8, dev, stream)
+    s = _new((*lead, K // group), torch.bfloat16 if fmt == W4_INT else torch.uint8, dev, stream)
+    z = _new((*lead, K // group), torch.uint8, dev, stream) if zeros else None
+    _check(lib().r9k_quant_weight_w4(_addr(w, BF16, "w", dev), rows, K, fmt, group, wq.data_ptr(), s.data_ptr(),
+                                     None if z is None else z.data_ptr(), _raw(stream, dev)), "r9k_quant_weight_w4")
+    return wq, s, z
+
+
+def pack_weight_w4(wq, s, z=None, stream=None):
+    """The packed copy that the products read (r9k_pack_weight_w4): codes [..., N, K/2], scales [..., N, K/group],
+    zeros or None -> the same shapes.  Experts' weights [E, N, K/2] pack as one.  Once, at load time."""
+    dev = _dev(wq, "wq")
+    a, b, c, fmt, group = _w4_format(wq, s, z, dev, "wq")
+    wp, sp = _new(wq.shape, torch.uint8, dev, stream), _new(s.shape, s.dtype, dev, stream)
+    zp = None if z is None else _new(z.shape, torch.uint8, dev, stream)
+    K = 2 * wq.shape[-1]
+    if wq.shape[-2] % 16:
+        raise ValueError(f"wq: {wq.shape[-2]} rows are not a multiple of 16")
+    _check(lib().r9k_pack_weight_w4(a, b, c, wq.numel() // wq.shape[-1], K, fmt, group, wp.data_ptr(), sp.data_ptr(),
+                                    None if zp is None else zp.data_ptr(), _raw(stream, dev)), "r9k_pack_weight_w4")
+    return wp, sp, zp
+
+
+@functools.lru_cache(maxsize=4096)
+def gemm_w4_workspace(M: int, K: int, N: int) -> int:
+    """Workspace bytes for gemm_w4 of this shape (r9k_gemm_w4_workspace); 0 for many shapes."""
+    b = c_size_t(0)
+    _check(lib().r9k_gemm_w4_workspace(M, K, N, ctypes.byref(b)), "r9k_gemm_w4_workspace")
+    return b.value
+
+
+def gemm_w4(a, wp, sp, zp=None, c=None, workspace=None, stream=None) -> torch.Tensor:
+    """Product with a packed 4-bit weight (r9k_gemm_w4): a [M,K] bf16, (wp, sp, zp) from pack_weight_w4 -> C [M,N]
+    bf16.  The format and the group follow from sp's type and shape."""
+    dev = _dev(a, "a")
+    M, K = a.shape
+    w, s, z, fmt, group = _w4_format(wp, sp, zp, dev, "wp", "sp", "zp")
+    if wp.dim() != 2 or 2 * wp.shape[1] != K:
+        raise ValueError(f"wp: shape {tuple(wp.shape)} does not go with a {tuple(a.shape)}")
+    N = wp.shape[0]
+    pa = _addr(a, BF16, "a", dev)
+    if c is None:
+        c = _new((M, N), torch.bfloat16, dev, stream)
+    pc = _addr(c, BF16, "c", dev, (M, N))
+    if M == 0:  # an empty batch: nothing to compute (an empty tensor has no device address to pass)
+        return c
+    pw, nb, _keep = _scratch(workspace, gemm_w4_workspace(M, K, N), dev, stream)
+    _check(lib().r9k_gemm_w4(pa, M, K, w, s, z, fmt, group, N, pc, pw, nb, _raw(stream, dev)), "r9k_gemm_w4")
+    return c
+
+
+_ACTS = {"none": ACT_NONE, "silu_mul": ACT_SILU_MUL}
+
+
+def moe_gemm_w4(x, offsets, wp, sp, zp=None, src=None, topk: int = 1, act: str = "none", c=None,
+                stream=None) -> torch.Tensor:
+    """The experts' products on sorted rows (r9k_moe_gemm_w4): offsets [E+1] and src [R] from moe_permute, (wp, sp,
+    zp) the packed weights [E,N,K/2] -> [R,N] bf16, or with act="silu_mul" [R,N/2].  Without src, x [R,K] holds the
+    sorted rows; with it, x [T,K] the tokens' rows and row r reads x[src[r] // topk].  Rows from offsets[E] on are
+    not written."""
+    dev = _dev(x, "x")
+    rows, K = x.shape
+    w, s, z, fmt, group = _w4_format(wp, sp, zp, dev, "wp", "sp", "zp")
+    if wp.dim() != 3 or 2 * wp.shape[2] != K:
+        raise ValueError(f"wp: shape {tuple(wp.shape)} does not go with x {tuple(x.shape)}")
+    if act not in _ACTS:
+        raise ValueError(f"act {act!r} not in {tuple(_ACTS)}")
+    E, N = wp.shape[0], wp.shape[1]
+    R = rows if src is None else src.numel()
+    out = (R, N if act == "none" else N // 2)
+    px = _addr(x, BF16, "x", dev)
+    po = _addr(offsets, I32, "offsets", dev, (E + 1,))
+    ps = None if src is None else _addr(src, I32, "src", dev)
+    if c is None:
+        c = _new(out, torch.bfloat16, dev, stream)
+    pc = _addr(c, BF16, "c", dev, out)
+    if R == 0:
+        return c
+    _check(lib().r9k_moe_gemm_w4(px, rows, ps, topk, po, E, R, K, w, s, z, fmt, group, N, _ACTS[act], pc,
+                                 _raw(stream, dev)), "r9k_moe_gemm_w4")
+    return c
+
+
+# ------------------------------------------- rows sorted by expert ----
+
+@functools.lru_cache(maxsize=1024)
+def moe_permute_workspace(T: int, E: int, topk: int) -> int:
+    b = c_size_t(0)
+    _check(lib().r9k_moe_permute_workspace(T, E, topk, ctypes.byref(b)), "r9k_moe_permute_workspace")
+    return b.value
+
+
+def moe_permute(x, topk_ids, E: int, xs=None, src=None, pos=None, offsets=None, workspace=None, stream=None):
+    """Token rows sorted by expert (r9k_moe_permute): x [T,H] bf16 or fp32, ids [T,topk] int32 -> (xs [T*topk,H],
+    src [T*topk], pos [T,topk], offsets [E+1]).  x None: the sort alone, and xs is None.  Rows of xs from
+    offsets[E] on (slots whose id lies outside [0,E)) are not written."""
+    dev = _dev(topk_ids, "topk_ids")
+    T, topk = topk_ids.shape
+    R = T * topk
+    pi = _addr(topk_ids, I32, "topk_ids", dev)
+    px = pxs = None
+    H = dt = 0
+    if x is not None:
+        px = _addr(x, _ROWS, "x", dev)
+        if x.dim() != 2 or x.shape[0] != T:
+            raise ValueError(f"x: shape {tuple(x.shape)} does not go with {T} tokens")
+        H, dt = x.shape[1], _ROWS[x.dtype]
+        if xs is None:
+            xs = _new((R, H), x.dtype, dev, stream)
+        pxs = _addr(xs, (x.dtype,), "xs", dev, (R, H))
+    elif xs is not None:
+        raise ValueError("xs without x")
+    if src is None:
+        src = _new((R,), torch.int32, dev, stream)
+    if pos is None:
+        pos = _new((T, topk), torch.int32, dev, stream)
+    if offsets is None:
+        offsets = _new((E + 1,), torch.int32, dev, stream)
+    psrc, ppos = _addr(src, I32, "src", dev, (R,)), _addr(pos, I32, "pos", dev, (T, topk))
+    poff = _addr(offsets, I32, "offsets", dev, (E + 1,))
+    if T == 0:  # no slots (empty tensors have no device address to pass): the call sees only the offsets
+        px = pxs = None
+        pi = psrc = ppos = poff
+    pw, nb, _keep = _scratch(workspace, moe_permute_workspace(T, E, topk), dev, stream)
+    _check(lib().r9k_moe_permute(px, dt, T, H, pi, topk, E, pxs, psrc, ppos, poff, pw, nb, _raw(stream, dev)),
+           "r9k_moe_permute")
+    return xs, src, pos, offsets
+
+
+def _sorted_rows(y, pos, dev: int, name: str):
+    T, topk = pos.shape
+    ppos = _addr(pos, I32, "pos", dev)
+    py = _addr(y, _ROWS, name, dev)
+    if y.dim() != 2 or y.shape[0] != T * topk:
+        raise ValueError(f"{name}: shape {tuple(y.shape)} does not go with {T} x {topk} slots")
+    return T, topk, y.shape[1], ppos, py
+
+
+def moe_permute_backward(gxs, pos, gx=None, stream=None) -> torch.Tensor:
+    """Gradient of moe_permute: gxs [T*topk,H], pos [T,topk] -> gx [T,H], the sum over a token's kept slots."""
+    dev = _dev(gxs, "gxs")
+    T, topk, H, ppos, pg = _sorted_rows(gxs, pos, dev, "gxs")
+    if gx is None:
+        gx = _new((T, H), gxs.dtype, dev, stream)
+    po = _addr(gx, (gxs.dtype,), "gx", dev, (T, H))
+    if T:
+        _check(lib().r9k_moe_permute_backward(pg, _ROWS[gxs.dtype], T, H, ppos, topk, po, _raw(stream, dev)),
+               "r9k_moe_permute_backward")
+    return gx
+
+
+def moe_unpermute(y, pos, w=None, out=None, stream=None) -> torch.Tensor:
+    """Sorted rows back to their tokens (r9k_moe_unpermute): y [T*topk,H], pos [T,topk], weights w [T,topk] fp32 (None: 1)
+    -> out [T,H] = sum_j w[t,j] * y[pos[t,j]]."""
+    dev = _dev(y, "y")
+    T, topk, H, ppos, py = _sorted_rows(y, pos, dev, "y")
+    pw = None if w is None else _addr(w, F32, "w", dev, (T, topk))
+    if out is None:
+        out = _new((T, H), y.dtype, dev, stream)
+    po = _addr(out, (y.dtype,), "out", dev, (T, H))
+    if T:
+        _check(lib().r9k_moe_unpermute(py, _ROWS[y.dtype], T, H, ppos, pw, topk, po, _raw(stream, dev)),
+               "r9k_moe_unpermute")
+    return out
+
+
+def moe_unpermute_backward(gout, y, pos, w, gy=None, gw=None, stream=None):
+    """Gradient of moe_unpermute: gout [T,H], y [T*topk,H], pos and w [T,topk] -> (gy [T*topk,H], gw [T,topk] fp32).
+    Rows of gy that no slot fills are not written."""
+    dev = _dev(y, "y")
+    T, topk, H, ppos, py = _sorted_rows(y, pos, dev, "y")
+    pg = _addr(gout, (y.dtype,), "gout", dev, (T, H))
+    pw = _addr(w, F32, "w", dev, (T, topk))
+    if gy is None:
+        gy = _new(y.shape, y.dtype, dev, stream)
+    if gw is None:
+        gw = _new((T, topk), torch.float32, dev, stream)
+    pgy, pgw = _addr(gy, (y.dtype,), "gy", dev, y.shape), _addr(gw, F32, "gw", dev, (T, topk))
+    if T:
+        _check(lib().r9k_moe_unpermute_backward(pg, py, _ROWS[y.dtype], T, H, ppos, pw, topk, pgy, pgw,
+                                                _raw(stream, dev)), "r9k_moe_unpermute_backward")
+    return gy, gw

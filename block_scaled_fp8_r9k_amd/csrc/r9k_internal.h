@@ -202,6 +202,49 @@ hipError_t launch_moe_decode(const MoeArgs &args, bool fused, hipStream_t s);
 hipError_t launch_moe_route(const float *logits, int64_t T, int64_t E, int topk, int32_t *ids, float *w,
                             hipStream_t s);
 
+// ---- 4-bit weights (w4_weight.hip, gemm_w4.hip) ----
+// fmt: W4_INT or W4_MXFP4; grp: values a scale covers; the packed layout is in w4_device.h
+hipError_t launch_quant_weight_w4(const uint16_t *w, int64_t N, int64_t K, int fmt, int grp, uint8_t *wq, void *s,
+                                  uint8_t *z, hipStream_t st);
+hipError_t launch_pack_weight_w4(const uint8_t *wq, const void *s, const uint8_t *z, int64_t N, int64_t K, int fmt,
+                                 int grp, uint8_t *wp, void *sp, uint8_t *zp, hipStream_t st);
+struct W4Args {
+    const uint16_t *a;       // activations [arows][K] bf16
+    const uint8_t *wp;       // packed codes [E][N*K/2]
+    const void *sp;          // packed scales
+    const uint8_t *zp;       // packed zeros, or NULL
+    uint16_t *c;             // [M][N] bf16, or [M][N/2] with silu
+    int64_t M, K, N;         // M: rows of c (expert products: the most that offsets cover)
+    const int32_t *offsets;  // expert products: [E + 1] first rows; NULL for a dense product
+    const int32_t *src;      // expert products: row r reads activation row src[r] / topk; NULL: row r
+    int64_t E, topk, arows;
+    int silu;                // 1: columns [0, N/2) gate, [N/2, N) up, c = silu(gate) * up
+    int nblk;                // (launcher) column blocks of the grid
+};
+struct W4Cfg {
+    int mt;  // row tiles of 16 a CTA
+    int nt;  // column tiles a wave
+    int nw;  // waves a CTA, consecutive K slices
+};
+W4Cfg w4_config(const W4Args &a);
+hipError_t launch_gemm_w4(const W4Args &a, int fmt, int grp, hipStream_t s);
+
+// ---- rows sorted by expert (moe_sort.hip) ----
+struct SortArgs {
+    const int32_t *ids;  // [T][topk]
+    const void *x;       // [T] rows, or NULL: the sort alone
+    void *xs;            // [T*topk] rows
+    int32_t *src, *pos, *offsets, *count;
+    int64_t T, topk, E, row_bytes;
+};
+size_t moe_sort_workspace(int64_t R, int64_t E);
+hipError_t launch_moe_permute(const SortArgs &a, hipStream_t s);
+hipError_t launch_moe_unpermute(const void *y, bool f32, int64_t row_bytes, int64_t T, int64_t topk,
+                                const int32_t *pos, const float *w, void *out, hipStream_t s);
+hipError_t launch_moe_unpermute_backward(const void *g, const void *y, bool f32, int64_t row_bytes, int64_t T,
+                                         int64_t topk, const int32_t *pos, const float *w, void *gy, float *gw,
+                                         hipStream_t s);
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace r9k

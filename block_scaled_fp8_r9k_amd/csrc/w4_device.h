@@ -1,0 +1,110 @@
+// Device helpers of the 4-bit weight kernels: formats, layout, decoding.
+//
+// Two formats of group-scaled 4-bit weights:
+//   int4   codes q = 0..15, value (q - z) * s: s bf16 per group of 32, 64 or 128
+//          along K, z a zero point 0..15 per group (8 where none are given);
+//   mxfp4  codes e2m1 (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives), value
+//          v * 2^(e - 127), e a byte per group of 32.
+// Packed layout (r9k_pack_weight_w4), for 16-row tile t = n / 16 and chunk
+// c = k / 128 (C = K / 128 chunks): the 1 KiB block at (t * C + c) * 1024 holds
+// at 16 * l the 16 bytes that MFMA lane l (row l % 16, quarter q = l / 16)
+// feeds to the chunk's four v_mfma_f32_16x16x32_bf16: word j holds k = 128 c +
+// 32 j + 8 q + 0..7.  int4: byte b of a word holds k + b in its low half and
+// k + b + 4 in its high half, so that a mask and a shift leave four codes in
+// four bytes; mxfp4: byte b holds k + 2 b and k + 2 b + 1, as the converter
+// takes them.
+// int4 scales and zeros, ng = 128 / group: element (((t * C + c) * 4 + q) * ng + i) * 4 + r
+// is row 16 t + 4 q + r, group i of the chunk: the rows whose sums lane l holds
+// after an MFMA.  mxfp4 scales: byte ((t * C + c) * 16 + r) * 4 + i is row 16 t + r,
+// group i: the row whose codes lane l % 16 = r converts.
+#pragma once
+
+#include "r9k_device.h"
+
+namespace r9k {
+
+typedef __bf16 w4_v8bf __attribute__((ext_vector_type(8)));
+typedef __bf16 w4_v2bf __attribute__((ext_vector_type(2)));
+typedef unsigned int w4_v4u __attribute__((ext_vector_type(4)));
+
+enum { W4_INT = 0, W4_MXFP4 = 1 };
+
+// Eight int4 codes (one packed word) -> eight bf16 of the values 0..15, exact.
+// A code in the low half of a byte is the e4m3 number q * 2^-9 (subnormal up to
+// 7, and the first binade continues with the same step up to 15), so the
+// fp8 converter with scale 2^9 gives q: seven instructions for eight codes.
+__device__ __forceinline__ w4_v8bf w4_int_frag(uint32_t x) {
+    const int lo = (int)(x & 0x0F0F0F0Fu), hi = (int)((x >> 4) & 0x0F0F0F0Fu);
+    const w4_v4u u = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true))};
+    return __builtin_bit_cast(w4_v8bf, u);
+}
+
+// Eight e2m1 codes (one packed word) times the group's scale -> eight bf16.
+// Two significant bits times a power of two: exact in bf16.
+__device__ __forceinline__ w4_v8bf w4_fp4_frag(uint32_t x, float scale) {
+    const w4_v4u u = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 0)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 1)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 2)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 3))};
+    return __builtin_bit_cast(w4_v8bf, u);
+}
+
+__device__ __forceinline__ w4_v8bf w4_frag(uint4 v) { return __builtin_bit_cast(w4_v8bf, w4_v4u{v.x, v.y, v.z, v.w}); }
+
+__device__ __forceinline__ w4_v8bf w4_ones() {
+    return __builtin_bit_cast(w4_v8bf, w4_v4u{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+}
+
+__device__ __forceinline__ v4f w4_mfma(w4_v8bf w, w4_v8bf a, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, a, c, 0, 0, 0);
+}
+
+// Four fp32 -> four bf16, round to nearest even (hardware converter; infinities
+// and NaN stay what they are).
+__device__ __forceinline__ uint2 w4_bf16x4(v4f x) {
+    const w4_v2bf lo = {(__bf16)x[0], (__bf16)x[1]}, hi = {(__bf16)x[2], (__bf16)x[3]};
+    return make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+}
+
+// silu(g) * u in fp32
+__device__ __forceinline__ float w4_silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// Row block `item` of the experts' row ranges [offsets[e], offsets[e+1]), RB
+// rows to a block, blocks counted expert by expert.  Every wave finds it by
+// itself (64 experts a step): false if there are fewer blocks.  Offsets are held to
+// [0, R], so that wrong ones cannot lead out of the rows.
+__device__ __forceinline__ bool w4_find_block(const int32_t *offsets, int E, int R, int RB, int item, int &e_out,
+                                              int &r0, int &r1) {
+    const int lane = threadIdx.x & 63;
+    int base = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        const int e = e0 + lane;
+        int o0 = e < E ? offsets[e] : 0, o1 = e < E ? offsets[e + 1] : 0;
+        o0 = min(max(o0, 0), R);
+        o1 = min(max(o1, o0), R);
+        const int nb = (o1 - o0 + RB - 1) / RB;
+        int incl = nb;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(incl, d, 64);
+            if (lane >= d) incl += v;
+        }
+        const int total = __builtin_amdgcn_readlane(incl, 63);
+        if (item < base + total) {
+            const unsigned long long m = __ballot(base + incl > item);
+            const int l = __builtin_ctzll(m);
+            const int first = base + __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(nb, l);
+            e_out = e0 + l;
+            r0 = __builtin_amdgcn_readlane(o0, l) + (item - first) * RB;
+            r1 = __builtin_amdgcn_readlane(o1, l);
+            return true;
+        }
+        base += total;
+    }
+    return false;
+}
+
+}  // namespace r9k

@@ -60,7 +60,7 @@ extern "C" {
 #pragma GCC visibility push(default)
 #endif
 
-#define R9K_ABI_VERSION 8
+#define R9K_ABI_VERSION 9
 
 /* Return codes: 0 or negative, as the pages' kernels return them (release
  * v0.3.0, its validation record: a test failing "with the kernel's -7").
@@ -77,7 +77,7 @@ extern "C" {
 /* The ABI version this library implements (R9K_ABI_VERSION; 4 added the MoE
  * routing and the shared-expert fold, 5 the bf16-activation variant, 6 the
  * mid-width kernel in the plan query, 7 the allocation-free GEMM entry point, 8 the tiled-plan
- * control and R9K_ENGINE_SPLITK).  Callers refuse
+ * control and R9K_ENGINE_SPLITK, 9 the 4-bit weights and the rows sorted by expert).  Callers refuse
  * a library whose version differs from the header they were built against:
  * the convention of the pages' plugin, which refuses an older libr9k.so
  * (release v0.2.2, "Upgrading").  Host only; cannot fail. */
@@ -386,6 +386,146 @@ int r9k_moe_route(const float *logits, int64_t T, int64_t E, int64_t topk, int32
  * 4 hs [P][I/128] fp32 (P = T*topk; gu, hq and hs are written by the
  * three-launch path only).  Host only.  Errors: NULLPTR; SHAPE; ARG. */
 int r9k_moe_ws_offset(int64_t T, int64_t H, int64_t E, int64_t I, int64_t topk, int which, size_t *offset);
+
+/* ------------------------------------------------------------------------ */
+/* 4-bit weights with group scales                                           */
+/* ------------------------------------------------------------------------ */
+
+/* Two formats, two codes to a byte (element k = 2i in the low half of byte i):
+ *   R9K_W4_INT    codes q = 0..15; value (q - z) * s.  s: bf16, one per `group`
+ *                 = 32, 64 or 128 values along K.  z: a zero point 0..15 per group
+ *                 (uint8_t), or none, which means 8.
+ *   R9K_W4_MXFP4  codes e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 the sign); value
+ *                 v * 2^(s - 127).  s: uint8_t, one per 32 values, 1..254; no zeros.
+ * Row-major: wq [N][K/2], s [N][K/group], z [N][K/group].  K is a multiple of
+ * 128, N of 16.  The products read a packed copy (r9k_pack_weight_w4), in which
+ * the codes, scales and zeros keep their sizes and values. */
+#define R9K_W4_INT 0
+#define R9K_W4_MXFP4 1
+
+/* Group quantisation of bf16 weights at load time, in fp32, ties to even:
+ *   R9K_W4_INT, z NULL:  s = bf16(max(amax, 1e-10f) / 7), q = clamp(rint(w / s) + 8, 0, 15);
+ *   R9K_W4_INT, z given: lo = min(0, min w), hi = max(0, max w),
+ *                        s = bf16(max(hi - lo, 1e-10f) / 15), z = clamp(rint(-lo / s), 0, 15),
+ *                        q = clamp(rint(w / s) + z, 0, 15);
+ *   R9K_W4_MXFP4:        s = clamp(exponent field of amax - 2, 1, 254),
+ *                        q = e2m1(w / 2^(s - 127)), ties to the even code, saturating.
+ *   w [N][K] bf16 -> wq, s, z as above.
+ * Errors: NULLPTR; SHAPE if N is not a positive multiple of 16 or K of 128; ARG for
+ * an unknown format, a group the format does not have, or zeros with R9K_W4_MXFP4;
+ * ALIGN; DEVICE; LAUNCH. */
+int r9k_quant_weight_w4(const uint16_t *w, int64_t N, int64_t K, int format, int group, uint8_t *wq, void *s,
+                        uint8_t *z, void *stream);
+
+/* The packed copy that the products read: wp, sp and zp have the sizes of wq, s
+ * and z (zp NULL exactly when z is).  For tile t = n / 16 and chunk c = k / 128
+ * (C = K / 128) the 1 KiB at (t * C + c) * 1024 holds at 16 * l + 4 * j (l = 0..63,
+ * j = 0..3) the codes of row 16 t + l % 16, k = 128 c + 32 j + 8 (l / 16) + 0..7;
+ * the byte order inside and that of sp and zp are the library's own.  Experts'
+ * weights [E][N][K/2] are packed as one weight of E * N rows.
+ * Errors: as r9k_quant_weight_w4; ARG also if an output overlaps its input, or
+ * zp is given without z or z without zp. */
+int r9k_pack_weight_w4(const uint8_t *wq, const void *s, const uint8_t *z, int64_t N, int64_t K, int format,
+                       int group, uint8_t *wp, void *sp, uint8_t *zp, void *stream);
+
+/* Workspace bytes of r9k_gemm_w4 for this shape, in any format (host only; 0 for
+ * many shapes, and then the workspace may be NULL).  Needs no initialisation;
+ * calls sharing one must not overlap in time.
+ * Errors: NULLPTR (bytes); SHAPE as for the call. */
+int r9k_gemm_w4_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes);
+
+/* Product of bf16 activations with a packed 4-bit weight, one output rounding:
+ *   c[m][n] = bf16( sum_k a[m][k] * value(n, k) ),
+ * any number of rows.  The activations are used as given and the weight's values
+ * exactly: products, group sums and their scaling are fp32.
+ *   a [M][K] bf16 -> c [M][N] bf16 (not overlapping an input).
+ * Errors: NULLPTR (a, wp, sp, c, or a workspace where one is needed); SHAPE if
+ * M < 0, K is not a positive multiple of 128 or N of 16; ARG for an unknown
+ * format, a group the format does not have, or zeros with R9K_W4_MXFP4; ALIGN;
+ * WORKSPACE; DEVICE; LAUNCH.  M = 0 launches nothing. */
+int r9k_gemm_w4(const uint16_t *a, int64_t M, int64_t K, const uint8_t *wp, const void *sp, const uint8_t *zp,
+                int format, int group, int64_t N, uint16_t *c, void *workspace, size_t ws_bytes, void *stream);
+
+/* The experts' products on rows sorted by expert (r9k_moe_permute): rows
+ * [offsets[e], offsets[e+1]) of c are the product with expert e's weight, as
+ * r9k_gemm_w4 computes it.  act:
+ *   R9K_ACT_NONE      c [R][N];
+ *   R9K_ACT_SILU_MUL  columns [0, N/2) of the product are gate, [N/2, N) up, and
+ *                     c [R][N/2] = bf16( silu(gate) * up ), fp32 between.
+ * Activation row of row r: r itself (src NULL), or src[r] / topk, with src as
+ * r9k_moe_permute writes it: the token rows are then read in place and no sorted
+ * copy is needed.  arows: the rows of a.  Rows of c from offsets[E] on are left as
+ * they were.
+ *   a [arows][K] bf16, src [R] int32, offsets [E+1] int32 (device, ascending, at
+ *   most R); wp, sp, zp: E weights of N rows packed as one -> c.
+ * offsets and src are device data the host cannot check: offsets are held to
+ * [0, R], and an index outside a reads row 0.
+ * Errors: NULLPTR (a, offsets, wp, sp, c); SHAPE if R < 0, arows < 1 (with R > 0), E
+ * < 1 or > 2048, topk < 1, K not a positive multiple of 128, N of 16 (of 32 with
+ * silu), or without src arows < R; ARG for an unknown format, group or act, or zeros with
+ * R9K_W4_MXFP4; ALIGN; DEVICE; LAUNCH.  R = 0 launches nothing. */
+#define R9K_ACT_NONE 0
+#define R9K_ACT_SILU_MUL 1
+int r9k_moe_gemm_w4(const uint16_t *a, int64_t arows, const int32_t *src, int64_t topk, const int32_t *offsets,
+                    int64_t E, int64_t R, int64_t K, const uint8_t *wp, const void *sp, const uint8_t *zp,
+                    int format, int group, int64_t N, int act, uint16_t *c, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rows sorted by expert, and back                                           */
+/* ------------------------------------------------------------------------ */
+
+/* Element type of the rows moved. */
+#define R9K_BF16 0
+#define R9K_F32 1
+
+/* Workspace bytes of r9k_moe_permute (host only).  Needs no initialisation;
+ * calls sharing one must not overlap in time.
+ * Errors: NULLPTR (bytes); SHAPE as for the call. */
+int r9k_moe_permute_workspace(int64_t T, int64_t E, int64_t topk, size_t *bytes);
+
+/* Sort the slots p = t * topk + j by expert topk_ids[t][j], stable, and copy
+ * each token's row to the rows of its slots:
+ *   offsets[e] = slots with an expert below e (offsets[E]: all kept slots);
+ *   pos[t][j]  = the slot's row, -1 where the id lies outside [0, E);
+ *   src[r]     = the slot of row r, -1 from offsets[E] on;
+ *   xs[pos[t][j]] = x[t]; rows from offsets[E] on are left as they were.
+ * x and xs may both be NULL: the sort alone (for r9k_moe_gemm_w4's src), and
+ * dtype and H are then not looked at.
+ *   x [T][H], xs [T*topk][H] (dtype); topk_ids [T][topk]; src [T*topk], pos
+ *   [T][topk], offsets [E+1] int32.
+ * Errors: NULLPTR (one of x and xs alone included); SHAPE if T < 0 or > 2^24, topk < 1 or > 64, E < 1
+ * or > 2048, or a row is not a positive multiple of 16 bytes; ARG for an unknown
+ * dtype or xs overlapping x; ALIGN; WORKSPACE; DEVICE; LAUNCH.  T = 0 writes the
+ * offsets (zeros) and nothing else. */
+int r9k_moe_permute(const void *x, int dtype, int64_t T, int64_t H, const int32_t *topk_ids, int64_t topk, int64_t E,
+                    void *xs, int32_t *src, int32_t *pos, int32_t *offsets, void *workspace, size_t ws_bytes,
+                    void *stream);
+
+/* The gradient of r9k_moe_permute: gx[t] = sum_j gxs[pos[t][j]] over the kept
+ * slots, j ascending in fp32, rounded once; 0 for a token with none.
+ *   gxs [T*topk][H], pos [T][topk] -> gx [T][H].
+ * Errors: as r9k_moe_unpermute. */
+int r9k_moe_permute_backward(const void *gxs, int dtype, int64_t T, int64_t H, const int32_t *pos, int64_t topk,
+                             void *gx, void *stream);
+
+/* Sorted rows back to their tokens, weights applied:
+ *   out[t] = sum_j w[t][j] * y[pos[t][j]] over the kept slots, j ascending in
+ * fp32, rounded once; 0 for a token with none.  w NULL: weights 1.
+ *   y [T*topk][H], pos [T][topk] int32, w [T][topk] fp32 -> out [T][H].
+ * A position outside [0, T*topk) counts as a dropped slot.
+ * Errors: NULLPTR; SHAPE as r9k_moe_permute; ARG for an unknown dtype or out
+ * overlapping y; ALIGN; DEVICE; LAUNCH.  T = 0 launches nothing. */
+int r9k_moe_unpermute(const void *y, int dtype, int64_t T, int64_t H, const int32_t *pos, const float *w,
+                      int64_t topk, void *out, void *stream);
+
+/* The gradient of r9k_moe_unpermute:
+ *   gy[pos[t][j]] = w[t][j] * gout[t]  (one rounding; rows that no slot fills are left
+ *   as they were), gw[t][j] = sum_h gout[t][h] * y[pos[t][j]][h] in fp32, 0 for a
+ *   dropped slot.
+ *   gout [T][H], y [T*topk][H], pos, w as above -> gy [T*topk][H], gw [T][topk] fp32.
+ * Errors: as r9k_moe_unpermute, ARG for gy overlapping gout or y. */
+int r9k_moe_unpermute_backward(const void *gout, const void *y, int dtype, int64_t T, int64_t H, const int32_t *pos,
+                               const float *w, int64_t topk, void *gy, float *gw, void *stream);
 
 #if defined(__GNUC__) || defined(__clang__)
 #pragma GCC visibility pop

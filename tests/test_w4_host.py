@@ -1,0 +1,216 @@
+"""The 4-bit weight and row-sorting calls on the host: every check of arguments, before any device is touched."""
+import ctypes
+from ctypes import c_size_t, c_void_p
+
+import pytest
+
+from tests.test_abi import _gpu_present
+
+A, B, C, D, E16 = (c_void_p(0x100000000 * i) for i in range(1, 6))  # aligned, far apart, never dereferenced
+ODD, NUL, S = c_void_p(0x100000008), c_void_p(None), c_void_p(None)
+INT, MX = 0, 1
+
+
+@pytest.fixture(scope="module")
+def L():
+    import block_scaled_fp8_r9k_amd as r9k
+    return r9k.lib()
+
+
+def test_constants():
+    import block_scaled_fp8_r9k_amd as r9k
+    from tests.test_abi import _defines
+    d = _defines()
+    assert (r9k.W4_INT, r9k.W4_MXFP4) == (d["R9K_W4_INT"], d["R9K_W4_MXFP4"]) == (INT, MX)
+    assert (r9k.ACT_NONE, r9k.ACT_SILU_MUL) == (d["R9K_ACT_NONE"], d["R9K_ACT_SILU_MUL"])
+    assert sorted(r9k._ROWS.values()) == [d["R9K_BF16"], d["R9K_F32"]]
+
+
+def test_quant_checks(L):
+    f = L.r9k_quant_weight_w4
+    ok = [A, 16, 128, INT, 128, B, C, NUL, S]
+
+    def with_(i, v):
+        x = list(ok)
+        x[i] = v
+        return f(*x)
+    for i in (0, 5, 6):
+        assert with_(i, NUL) == -1
+    for N in (0, -16, 8, 100):
+        assert with_(1, N) == -2
+    for K in (0, 64, 130, -128):
+        assert with_(2, K) == -2
+    assert with_(3, 2) == -7 and with_(3, -1) == -7
+    for g in (0, 16, 48, 256):
+        assert with_(4, g) == -7
+    assert f(A, 16, 128, MX, 128, B, C, NUL, S) == -7        # mxfp4 has one group size
+    assert f(A, 16, 128, MX, 32, B, C, D, S) == -7           # and no zeros
+    for i in (0, 5, 6, 7):
+        assert with_(i, ODD) == -3
+
+
+def test_pack_checks(L):
+    f = L.r9k_pack_weight_w4
+    ok = [A, B, NUL, 16, 128, INT, 128, C, D, NUL, S]
+
+    def with_(**kw):
+        x = list(ok)
+        for k, v in kw.items():
+            x[int(k[1:])] = v
+        return f(*x)
+    for i in (0, 1, 7, 8):
+        assert with_(**{f"_{i}": NUL}) == -1
+    assert with_(_3=24) == -2 and with_(_4=64) == -2
+    assert with_(_5=3) == -7 and with_(_6=96) == -7 and with_(_5=MX) == -7
+    assert with_(_2=E16) == -7 and with_(_9=E16) == -7       # zeros in without out, and out without in
+    assert with_(_7=A) == -7 and with_(_8=B) == -7           # in place
+    for i in (0, 1, 7, 8):
+        assert with_(**{f"_{i}": ODD}) == -3
+
+
+def _ws(fn, *shape):
+    b = c_size_t(1 << 40)
+    return fn(*shape, ctypes.byref(b)), b.value
+
+
+def test_gemm_checks(L):
+    f = L.r9k_gemm_w4
+    big = 1 << 40
+    ok = [A, 3, 256, B, C, NUL, INT, 64, 48, D, E16, big, S]
+
+    def with_(**kw):
+        x = list(ok)
+        for k, v in kw.items():
+            x[int(k[1:])] = v
+        return f(*x)
+    for i in (0, 3, 4, 9):
+        assert with_(**{f"_{i}": NUL}) == -1
+    assert with_(_1=-1) == -2 and with_(_1=1 << 25) == -2
+    assert with_(_2=64) == -2 and with_(_2=0) == -2 and with_(_8=8) == -2 and with_(_8=0) == -2
+    assert with_(_6=5) == -7 and with_(_7=100) == -7 and with_(_6=MX) == -7
+    assert with_(_6=MX, _7=32, _5=E16) == -7
+    for i in (0, 3, 4, 5, 9, 10):
+        assert with_(**{f"_{i}": ODD}) == -3
+    assert with_(_1=0) == 0
+    assert L.r9k_gemm_w4_workspace(1, 128, 16, None) == -1
+    assert _ws(L.r9k_gemm_w4_workspace, -1, 128, 16)[0] == -2
+    assert _ws(L.r9k_gemm_w4_workspace, 1, 100, 16)[0] == -2
+    assert _ws(L.r9k_gemm_w4_workspace, 1, 128, 20)[0] == -2
+    assert _ws(L.r9k_gemm_w4_workspace, 0, 128, 16) == (0, 0)
+    for M in (1, 5, 64, 300, 4096):       # a workspace smaller than the query's is refused, and NULL where one is needed
+        rc, need = _ws(L.r9k_gemm_w4_workspace, M, 4096, 4096)
+        assert rc == 0 and need % 256 == 0
+        if need:
+            x = dict(_1=M, _2=4096, _8=4096)
+            assert with_(_11=need - 1, **x) == -6 and with_(_10=NUL, **x) == -1
+
+
+def test_moe_gemm_checks(L):
+    f = L.r9k_moe_gemm_w4
+    ok = [A, 8, B, 2, C, 4, 16, 256, D, E16, NUL, INT, 128, 64, 1, c_void_p(6 << 32), S]
+
+    def with_(**kw):
+        x = list(ok)
+        for k, v in kw.items():
+            x[int(k[1:])] = v
+        return f(*x)
+    for i in (0, 4, 8, 9, 15):
+        assert with_(**{f"_{i}": NUL}) == -1
+    assert with_(_1=0) == -2 and with_(_1=-1) == -2
+    assert with_(_2=NUL) == -2                               # 16 rows from 8 without an index
+    assert with_(_3=0) == -2
+    assert with_(_5=0) == -2 and with_(_5=2049) == -2
+    assert with_(_6=-1) == -2
+    assert with_(_7=100) == -2 and with_(_13=16) == -2       # silu needs whole tiles in either half
+    assert with_(_13=24, _14=0) == -2
+    assert with_(_11=2) == -7 and with_(_12=16) == -7 and with_(_14=2) == -7
+    for i in (0, 2, 4, 8, 9, 10, 15):
+        assert with_(**{f"_{i}": ODD}) == -3
+    assert with_(_6=0) == 0
+
+
+def test_permute_checks(L):
+    f = L.r9k_moe_permute
+    F = c_void_p(6 << 32)
+    G = c_void_p(7 << 32)
+    ok = [A, 0, 4, 64, B, 2, 8, C, D, E16, F, G, 1 << 30, S]
+
+    def with_(**kw):
+        x = list(ok)
+        for k, v in kw.items():
+            x[int(k[1:])] = v
+        return f(*x)
+    for i in (0, 4, 7, 8, 9, 10, 11):
+        assert with_(**{f"_{i}": NUL}) == -1
+    assert with_(_1=2) == -7
+    assert with_(_2=-1) == -2 and with_(_2=1 << 25) == -2
+    assert with_(_3=0) == -2 and with_(_3=4) == -2 and with_(_3=63) == -2
+    assert with_(_3=2, _1=1) == -2                           # 8 bytes of fp32
+    assert with_(_5=0) == -2 and with_(_5=65) == -2
+    assert with_(_6=0) == -2 and with_(_6=2049) == -2
+    assert with_(_7=A) == -7                                 # rows on top of their source
+    assert with_(_12=0) == -6
+    for i in (0, 4, 7, 8, 9, 10, 11):
+        assert with_(**{f"_{i}": ODD}) == -3
+    assert L.r9k_moe_permute_workspace(4, 8, 2, None) == -1
+    assert _ws(L.r9k_moe_permute_workspace, 4, 0, 2)[0] == -2
+    assert _ws(L.r9k_moe_permute_workspace, 4, 8, 0)[0] == -2
+    assert _ws(L.r9k_moe_permute_workspace, -4, 8, 2)[0] == -2
+    rc, need = _ws(L.r9k_moe_permute_workspace, 4, 8, 2)
+    assert rc == 0 and need % 256 == 0
+
+
+def test_unpermute_checks(L):
+    for f, ok, ptrs, out in (
+            (L.r9k_moe_unpermute, [A, 0, 4, 64, B, C, 2, D, S], (0, 4, 7), 7),
+            (L.r9k_moe_permute_backward, [A, 0, 4, 64, B, 2, D, S], (0, 4, 6), 6)):
+        def with_(i, v):
+            x = list(ok)
+            x[i] = v
+            return f(*x)
+        for i in ptrs:
+            assert with_(i, NUL) == -1 and with_(i, ODD) == -3
+        assert with_(1, 3) == -7 and with_(out, A) == -7
+        assert with_(2, -1) == -2 and with_(3, 20) == -2 and with_(3, 0) == -2
+        assert with_(2, 0) == 0
+    f = L.r9k_moe_unpermute_backward
+    ok = [A, B, 1, 4, 64, C, D, 2, E16, c_void_p(6 << 32), S]
+
+    def with_(i, v):
+        x = list(ok)
+        x[i] = v
+        return f(*x)
+    for i in (0, 1, 5, 6, 8, 9):
+        assert with_(i, NUL) == -1 and with_(i, ODD) == -3
+    assert with_(8, A) == -7 and with_(8, B) == -7
+    assert with_(2, 2) == -7 and with_(3, -1) == -2 and with_(4, 2) == -2 and with_(7, 0) == -2
+    assert with_(3, 0) == 0
+
+
+@pytest.mark.skipif(_gpu_present(), reason="valid arguments would reach a real device")
+def test_no_device_is_reported(L):
+    big, F, G = 1 << 40, c_void_p(6 << 32), c_void_p(7 << 32)
+    assert L.r9k_quant_weight_w4(A, 16, 128, INT, 32, B, C, D, S) == -4
+    assert L.r9k_pack_weight_w4(A, B, NUL, 16, 128, MX, 32, C, D, NUL, S) == -4
+    assert L.r9k_gemm_w4(A, 1, 128, B, C, NUL, INT, 128, 16, D, E16, big, S) == -4
+    assert L.r9k_moe_gemm_w4(A, 8, B, 2, C, 4, 16, 256, D, E16, NUL, INT, 128, 64, 1, F, S) == -4
+    assert L.r9k_moe_permute(A, 0, 4, 64, B, 2, 8, C, D, E16, F, G, big, S) == -4
+    assert L.r9k_moe_unpermute(A, 0, 4, 64, B, C, 2, D, S) == -4
+    assert L.r9k_moe_permute_backward(A, 0, 4, 64, B, 2, D, S) == -4
+    assert L.r9k_moe_unpermute_backward(A, B, 1, 4, 64, C, D, 2, E16, F, S) == -4
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+    import block_scaled_fp8_r9k_amd as r9k
+    bf, u8, i32 = torch.bfloat16, torch.uint8, torch.int32
+    with pytest.raises(ValueError):
+        r9k.quant_weight_w4(torch.zeros((16, 128), dtype=bf))
+    with pytest.raises(ValueError):
+        r9k.pack_weight_w4(torch.zeros((16, 64), dtype=u8), torch.zeros((16, 1), dtype=bf))
+    with pytest.raises(ValueError):
+        r9k.gemm_w4(torch.zeros((1, 128), dtype=bf), torch.zeros((16, 64), dtype=u8), torch.zeros((16, 1), dtype=bf))
+    with pytest.raises(ValueError):
+        r9k.moe_permute(None, torch.zeros((2, 2), dtype=i32), 4)
+    with pytest.raises(ValueError):
+        r9k.moe_unpermute(torch.zeros((4, 64)), torch.zeros((2, 2), dtype=i32))
