@@ -84,7 +84,9 @@ def lib() -> ctypes.CDLL:
         L.r9k_gemm_w4.argtypes = [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64,
                                   c_void_p, c_void_p, c_size_t, c_void_p]
         L.r9k_moe_gemm_w4.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64,
-                                      c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64, c_int, c_void_p, c_void_p]
+                                      c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64, c_int, c_void_p, c_void_p,
+                                      c_size_t, c_void_p]
+        L.r9k_moe_gemm_w4_workspace.argtypes = [c_int64] * 5 + [c_int, POINTER(c_size_t)]
         L.r9k_moe_permute_workspace.argtypes = [c_int64, c_int64, c_int64, POINTER(c_size_t)]
         L.r9k_moe_permute.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int64, c_int64, c_void_p,
                                       c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]
@@ -440,25 +442,31 @@ U8 = (torch.uint8,)
 _ROWS = {torch.bfloat16: 0, torch.float32: 1}  # R9K_BF16, R9K_F32
 
 
+# the current device's index without torch.cuda's lazy-initialisation check (a device
+# tensor is in hand when these are called)
+_cur_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _dev(t: torch.Tensor, name: str) -> int:
     """The current device's index; the call's first tensor has to be there."""
-    cur = torch.cuda.current_device() if t.is_cuda else -1
-    if t.get_device() != cur or cur < 0:
-        raise ValueError(f"{name} must be a tensor of the current device")
-    return cur
+    if t.is_cuda:
+        cur = _cur_device()
+        if t.get_device() == cur:
+            return cur
+    raise ValueError(f"{name} must be a tensor of the current device")
 
 
 def _addr(t: torch.Tensor, dtypes, name: str, dev: int, shape=None) -> int:
     """Device address of a contiguous tensor of device `dev`, checked (0 for an empty one)."""
+    if t.dtype in dtypes and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a tensor of the current device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, needs {tuple(shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, needs {tuple(shape)}")
 
 
 def _raw(stream, dev: int) -> int:
@@ -487,16 +495,22 @@ def _scratch(ws: torch.Tensor | None, nbytes: int, dev: int, stream):
     return _addr(ws, U8, "workspace", dev) or None, ws.numel(), ws
 
 
-def _w4_format(wp, sp, zp, dev: int, wname="w", sname="s", zname="z"):
-    """Addresses, format and group of a 4-bit weight [..., N, K/2] with its scales and zeros [..., N, K/group]."""
-    if wp.dim() < 2 or sp.dim() != wp.dim() or sp.shape[:-1] != wp.shape[:-1] or not sp.shape[-1]:
-        raise ValueError(f"{sname}: shape {tuple(sp.shape)} does not go with {wname} {tuple(wp.shape)}")
-    K = 2 * wp.shape[-1]
-    if K % sp.shape[-1]:
-        raise ValueError(f"{sname}: {sp.shape[-1]} groups do not divide K = {K}")
-    fmt = W4_INT if sp.dtype == torch.bfloat16 else W4_MXFP4
-    return (_addr(wp, U8, wname, dev), _addr(sp, (torch.bfloat16, torch.uint8), sname, dev),
-            None if zp is None else _addr(zp, U8, zname, dev, sp.shape), fmt, K // sp.shape[-1])
+_W4_SCALES = {torch.bfloat16: W4_INT, torch.uint8: W4_MXFP4}
+
+
+def _w4_format(wp, sp, zp, dev: int, dims: int = 0):
+    """Addresses, format, rows (all leading sizes), K and group of a 4-bit weight [..., N, K/2] with its scales and
+    zeros [..., N, K/group] (`dims`: the number of sizes it must have)."""
+    ws, ss = wp.shape, sp.shape
+    nd = len(ws)
+    if nd < 2 or (dims and nd != dims) or len(ss) != nd or ss[-2] != ws[-2] or (nd > 2 and ss[:-2] != ws[:-2]):
+        raise ValueError(f"scales {tuple(ss)} do not go with 4-bit codes {tuple(ws)}"
+                         + (f" of {dims} sizes" if dims else ""))
+    K, groups = 2 * ws[-1], ss[-1]
+    if not groups or K % groups:
+        raise ValueError(f"{groups} scales a row do not divide K = {K}")
+    return (_addr(wp, U8, "codes", dev), _addr(sp, _W4_SCALES, "scales", dev),
+            None if zp is None else _addr(zp, U8, "zeros", dev, ss), _W4_SCALES[sp.dtype], K, K // groups)
 
 
 def quant_weight_w4(w: torch.Tensor, group: int = 128, fmt: int = W4_INT, zeros: bool = False, stream=None):
@@ -519,13 +533,12 @@ def pack_weight_w4(wq, s, z=None, stream=None):
     """The packed copy that the products read (r9k_pack_weight_w4): codes [..., N, K/2], scales [..., N, K/group],
     zeros or None -> the same shapes.  Experts' weights [E, N, K/2] pack as one.  Once, at load time."""
     dev = _dev(wq, "wq")
-    a, b, c, fmt, group = _w4_format(wq, s, z, dev, "wq")
+    a, b, c, fmt, K, group = _w4_format(wq, s, z, dev)
     wp, sp = _new(wq.shape, torch.uint8, dev, stream), _new(s.shape, s.dtype, dev, stream)
     zp = None if z is None else _new(z.shape, torch.uint8, dev, stream)
-    K = 2 * wq.shape[-1]
     if wq.shape[-2] % 16:
         raise ValueError(f"wq: {wq.shape[-2]} rows are not a multiple of 16")
-    _check(lib().r9k_pack_weight_w4(a, b, c, wq.numel() // wq.shape[-1], K, fmt, group, wp.data_ptr(), sp.data_ptr(),
+    _check(lib().r9k_pack_weight_w4(a, b, c, 2 * wq.numel() // K, K, fmt, group, wp.data_ptr(), sp.data_ptr(),
                                     None if zp is None else zp.data_ptr(), _raw(stream, dev)), "r9k_pack_weight_w4")
     return wp, sp, zp
 
@@ -542,42 +555,47 @@ def gemm_w4(a, wp, sp, zp=None, c=None, workspace=None, stream=None) -> torch.Te
     """Product with a packed 4-bit weight (r9k_gemm_w4): a [M,K] bf16, (wp, sp, zp) from pack_weight_w4 -> C [M,N]
     bf16.  The format and the group follow from sp's type and shape."""
     dev = _dev(a, "a")
-    M, K = a.shape
-    w, s, z, fmt, group = _w4_format(wp, sp, zp, dev, "wp", "sp", "zp")
-    if wp.dim() != 2 or 2 * wp.shape[1] != K:
-        raise ValueError(f"wp: shape {tuple(wp.shape)} does not go with a {tuple(a.shape)}")
-    N = wp.shape[0]
-    pa = _addr(a, BF16, "a", dev)
+    w, s, z, fmt, K, group = _w4_format(wp, sp, zp, dev, 2)
+    M, N = a.shape[0], wp.shape[0]
+    pa = _addr(a, BF16, "a", dev, (M, K))
     if c is None:
         c = _new((M, N), torch.bfloat16, dev, stream)
     pc = _addr(c, BF16, "c", dev, (M, N))
     if M == 0:  # an empty batch: nothing to compute (an empty tensor has no device address to pass)
         return c
     pw, nb, _keep = _scratch(workspace, gemm_w4_workspace(M, K, N), dev, stream)
-    _check(lib().r9k_gemm_w4(pa, M, K, w, s, z, fmt, group, N, pc, pw, nb, _raw(stream, dev)), "r9k_gemm_w4")
+    rc = lib().r9k_gemm_w4(pa, M, K, w, s, z, fmt, group, N, pc, pw, nb, _raw(stream, dev))
+    if rc:
+        _check(rc, "r9k_gemm_w4")
     return c
 
 
 _ACTS = {"none": ACT_NONE, "silu_mul": ACT_SILU_MUL}
 
 
-def moe_gemm_w4(x, offsets, wp, sp, zp=None, src=None, topk: int = 1, act: str = "none", c=None,
+@functools.lru_cache(maxsize=4096)
+def moe_gemm_w4_workspace(rows: int, E: int, R: int, K: int, N: int, act: str = "none") -> int:
+    """Workspace bytes for moe_gemm_w4 of these sizes (r9k_moe_gemm_w4_workspace); 0 for many."""
+    b = c_size_t(0)
+    _check(lib().r9k_moe_gemm_w4_workspace(rows, E, R, K, N, _ACTS[act], ctypes.byref(b)),
+           "r9k_moe_gemm_w4_workspace")
+    return b.value
+
+
+def moe_gemm_w4(x, offsets, wp, sp, zp=None, src=None, topk: int = 1, act: str = "none", c=None, workspace=None,
                 stream=None) -> torch.Tensor:
     """The experts' products on sorted rows (r9k_moe_gemm_w4): offsets [E+1] and src [R] from moe_permute, (wp, sp,
     zp) the packed weights [E,N,K/2] -> [R,N] bf16, or with act="silu_mul" [R,N/2].  Without src, x [R,K] holds the
     sorted rows; with it, x [T,K] the tokens' rows and row r reads x[src[r] // topk].  Rows from offsets[E] on are
     not written."""
     dev = _dev(x, "x")
-    rows, K = x.shape
-    w, s, z, fmt, group = _w4_format(wp, sp, zp, dev, "wp", "sp", "zp")
-    if wp.dim() != 3 or 2 * wp.shape[2] != K:
-        raise ValueError(f"wp: shape {tuple(wp.shape)} does not go with x {tuple(x.shape)}")
+    w, s, z, fmt, K, group = _w4_format(wp, sp, zp, dev, 3)
     if act not in _ACTS:
         raise ValueError(f"act {act!r} not in {tuple(_ACTS)}")
-    E, N = wp.shape[0], wp.shape[1]
+    rows, E, N = x.shape[0], wp.shape[0], wp.shape[1]
     R = rows if src is None else src.numel()
     out = (R, N if act == "none" else N // 2)
-    px = _addr(x, BF16, "x", dev)
+    px = _addr(x, BF16, "x", dev, (rows, K))
     po = _addr(offsets, I32, "offsets", dev, (E + 1,))
     ps = None if src is None else _addr(src, I32, "src", dev)
     if c is None:
@@ -585,7 +603,8 @@ def moe_gemm_w4(x, offsets, wp, sp, zp=None, src=None, topk: int = 1, act: str =
     pc = _addr(c, BF16, "c", dev, out)
     if R == 0:
         return c
-    _check(lib().r9k_moe_gemm_w4(px, rows, ps, topk, po, E, R, K, w, s, z, fmt, group, N, _ACTS[act], pc,
+    pw, nb, _keep = _scratch(workspace, moe_gemm_w4_workspace(rows, E, R, K, N, act), dev, stream)
+    _check(lib().r9k_moe_gemm_w4(px, rows, ps, topk, po, E, R, K, w, s, z, fmt, group, N, _ACTS[act], pc, pw, nb,
                                  _raw(stream, dev)), "r9k_moe_gemm_w4")
     return c
 

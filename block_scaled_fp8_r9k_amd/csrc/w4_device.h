@@ -72,39 +72,58 @@ __device__ __forceinline__ uint2 w4_bf16x4(v4f x) {
 // silu(g) * u in fp32
 __device__ __forceinline__ float w4_silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
+// Inclusive sum over the wave's 64 lanes (DPP row shifts, then the row ends
+// carried on).  Every lane must be active.
+__device__ __forceinline__ int w4_wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2 and 3
+    return v;
+}
+
 // Row block `item` of the experts' row ranges [offsets[e], offsets[e+1]), RB
-// rows to a block, blocks counted expert by expert.  Every wave finds it by
-// itself (64 experts a step): false if there are fewer blocks.  Offsets are held to
-// [0, R], so that wrong ones cannot lead out of the rows.
+// rows (a power of two) to a block, blocks counted expert by expert: the expert, and
+// its rows from the block's first on; false if there are fewer blocks.  Every wave
+// finds it by itself: each lane counts the blocks of its E / 64 experts, then the
+// chosen lane's experts are spread over the lanes.  Offsets are held to [0, R], so that
+// wrong ones cannot lead out of the rows.
 __device__ __forceinline__ bool w4_find_block(const int32_t *offsets, int E, int R, int RB, int item, int &e_out,
                                               int &r0, int &r1) {
-    const int lane = threadIdx.x & 63;
-    int base = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-        const int e = e0 + lane;
-        int o0 = e < E ? offsets[e] : 0, o1 = e < E ? offsets[e + 1] : 0;
-        o0 = min(max(o0, 0), R);
-        o1 = min(max(o1, o0), R);
-        const int nb = (o1 - o0 + RB - 1) / RB;
-        int incl = nb;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int v = __shfl_up(incl, d, 64);
-            if (lane >= d) incl += v;
-        }
-        const int total = __builtin_amdgcn_readlane(incl, 63);
-        if (item < base + total) {
-            const unsigned long long m = __ballot(base + incl > item);
-            const int l = __builtin_ctzll(m);
-            const int first = base + __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(nb, l);
-            e_out = e0 + l;
-            r0 = __builtin_amdgcn_readlane(o0, l) + (item - first) * RB;
-            r1 = __builtin_amdgcn_readlane(o1, l);
-            return true;
-        }
-        base += total;
+    const int lane = threadIdx.x & 63, sh = __builtin_ctz(RB);
+    const int per = (E + 63) >> 6;
+    auto blocks = [&](int e, int &o0) {
+        const int a = e < E ? offsets[e] : 0, b = e < E ? offsets[e + 1] : 0;
+        o0 = min(max(a, 0), R);
+        return (max(min(b, R), o0) - o0 + RB - 1) >> sh;
+    };
+    int o0 = 0, n = 0;
+    for (int i = 0; i < per; ++i) n += blocks(lane * per + i, o0);
+    int incl = w4_wave_scan(n);
+    if (item >= __builtin_amdgcn_readlane(incl, 63)) return false;
+    int l = __builtin_ctzll(__ballot(incl > item));
+    int before = __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(n, l);  // blocks before lane l's
+    int e = l * per;
+    if (per > 1) {  // per <= 64
+        n = lane < per ? blocks(e + lane, o0) : 0;
+        incl = before + w4_wave_scan(n);
+        l = __builtin_ctzll(__ballot(incl > item));
+        before = __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(n, l);
+        e += l;
     }
-    return false;
+    e_out = e;
+    r0 = __builtin_amdgcn_readlane(o0, l) + ((item - before) << sh);
+    r1 = min(max(offsets[e + 1], 0), R);
+    return true;
+}
+
+// p / topk for p < 2^31, with magic = ceil(2^32 / topk) (0 for topk = 1): at most one too large
+__device__ __forceinline__ uint32_t w4_div_topk(uint32_t p, uint32_t topk, uint32_t magic) {
+    if (magic == 0) return p;
+    const uint32_t d = __umulhi(p, magic);
+    return d - (d * topk > p);
 }
 
 }  // namespace r9k
