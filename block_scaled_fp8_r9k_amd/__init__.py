@@ -84,9 +84,7 @@ def lib() -> ctypes.CDLL:
         L.r9k_gemm_w4.argtypes = [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64,
                                   c_void_p, c_void_p, c_size_t, c_void_p]
         L.r9k_moe_gemm_w4.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64,
-                                      c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64, c_int, c_void_p, c_void_p,
-                                      c_size_t, c_void_p]
-        L.r9k_moe_gemm_w4_workspace.argtypes = [c_int64] * 5 + [c_int, POINTER(c_size_t)]
+                                      c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64, c_int, c_void_p, c_void_p]
         L.r9k_moe_permute_workspace.argtypes = [c_int64, c_int64, c_int64, POINTER(c_size_t)]
         L.r9k_moe_permute.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int64, c_int64, c_void_p,
                                       c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]
@@ -573,16 +571,7 @@ def gemm_w4(a, wp, sp, zp=None, c=None, workspace=None, stream=None) -> torch.Te
 _ACTS = {"none": ACT_NONE, "silu_mul": ACT_SILU_MUL}
 
 
-@functools.lru_cache(maxsize=4096)
-def moe_gemm_w4_workspace(rows: int, E: int, R: int, K: int, N: int, act: str = "none") -> int:
-    """Workspace bytes for moe_gemm_w4 of these sizes (r9k_moe_gemm_w4_workspace); 0 for many."""
-    b = c_size_t(0)
-    _check(lib().r9k_moe_gemm_w4_workspace(rows, E, R, K, N, _ACTS[act], ctypes.byref(b)),
-           "r9k_moe_gemm_w4_workspace")
-    return b.value
-
-
-def moe_gemm_w4(x, offsets, wp, sp, zp=None, src=None, topk: int = 1, act: str = "none", c=None, workspace=None,
+def moe_gemm_w4(x, offsets, wp, sp, zp=None, src=None, topk: int = 1, act: str = "none", c=None,
                 stream=None) -> torch.Tensor:
     """The experts' products on sorted rows (r9k_moe_gemm_w4): offsets [E+1] and src [R] from moe_permute, (wp, sp,
     zp) the packed weights [E,N,K/2] -> [R,N] bf16, or with act="silu_mul" [R,N/2].  Without src, x [R,K] holds the
@@ -603,8 +592,7 @@ def moe_gemm_w4(x, offsets, wp, sp, zp=None, src=None, topk: int = 1, act: str =
     pc = _addr(c, BF16, "c", dev, out)
     if R == 0:
         return c
-    pw, nb, _keep = _scratch(workspace, moe_gemm_w4_workspace(rows, E, R, K, N, act), dev, stream)
-    _check(lib().r9k_moe_gemm_w4(px, rows, ps, topk, po, E, R, K, w, s, z, fmt, group, N, _ACTS[act], pc, pw, nb,
+    _check(lib().r9k_moe_gemm_w4(px, rows, ps, topk, po, E, R, K, w, s, z, fmt, group, N, _ACTS[act], pc,
                                  _raw(stream, dev)), "r9k_moe_gemm_w4")
     return c
 

@@ -645,40 +645,35 @@ int r9k_pack_weight_w4(const uint8_t *wq, const void *s, const uint8_t *z, int64
     return launch_result(launch_pack_weight_w4(wq, s, z, N, K, format, group, wp, sp, zp, (hipStream_t)stream));
 }
 
-// A 4-bit product's kernel, and its workspace: [sums of the activations' groups][K-split partials]
-struct W4Ws {
+// A 4-bit product's kernel, and its workspace: the partial sums of a K split, which
+// only dense products take.
+struct W4Plan {
     W4TiledCfg tiled;
     W4Cfg cfg;
-    size_t part, total;
+    size_t bytes;
 };
-static W4Ws w4_ws(int64_t arows, int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
-    W4Ws w{w4_tiled_config(M, K, N, E, silu), {}, 0, 0};
-    int split = w.tiled.ksplit;
-    if (w.tiled.wm) {
-        w.part = w4_sums_bytes(arows, K, 32);  // for the finest groups, whatever the weight's are
-    } else {
-        w.cfg = w4_config(M, K, N, E, silu);
-        split = w.cfg.ksplit;
-    }
-    w.total = w.part + (split > 1 ? align_up((size_t)split * (size_t)(M * N) * sizeof(float), 256) : 0);
+static W4Plan w4_plan(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
+    W4Plan w{w4_tiled_config(M, K, N, E, silu), {}, 0};
+    if (!w.tiled.on) w.cfg = w4_config(M, K, N, E, silu);
+    const int split = w.tiled.on ? w.tiled.ksplit : w.cfg.ksplit;
+    if (split > 1) w.bytes = align_up((size_t)split * (size_t)(M * N) * sizeof(float), 256);
     return w;
 }
 
 static int run_w4(W4Args &a, int format, int group, void *workspace, size_t ws_bytes, hipStream_t s) {
-    const W4Ws w = w4_ws(a.arows, a.M, a.K, a.N, a.offsets ? a.E : 0, a.silu != 0);
-    if (w.total && !workspace) return R9K_ERR_NULLPTR;
-    if (ws_bytes < w.total) return R9K_ERR_WORKSPACE;
+    const W4Plan w = w4_plan(a.M, a.K, a.N, a.offsets ? a.E : 0, a.silu != 0);
+    if (w.bytes && !workspace) return R9K_ERR_NULLPTR;
+    if (ws_bytes < w.bytes) return R9K_ERR_WORKSPACE;
     if (int rc = check_device()) return rc;
-    a.sums = (float *)workspace;
-    a.part = (float *)((uint8_t *)workspace + w.part);
-    return launch_result(w.tiled.wm ? launch_gemm_w4_tiled(a, format, group, w.tiled, s)
+    a.part = (float *)workspace;
+    return launch_result(w.tiled.on ? launch_gemm_w4_tiled(a, format, group, w.tiled, s)
                                     : launch_gemm_w4(a, format, group, w.cfg, s));
 }
 
 int r9k_gemm_w4_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes) {
     if (!bytes) return R9K_ERR_NULLPTR;
     if (M < 0 || M > MAX_DIM || !w4_shape(N, K, 16)) return R9K_ERR_SHAPE;
-    *bytes = M ? w4_ws(M, M, K, N, 0, false).total : 0;
+    *bytes = M ? w4_plan(M, K, N, 0, false).bytes : 0;
     return R9K_OK;
 }
 
@@ -690,7 +685,7 @@ int r9k_gemm_w4(const uint16_t *a, int64_t M, int64_t K, const uint8_t *wp, cons
     if (!aligned16(a) || !aligned16(wp) || !aligned16(sp) || !aligned16(zp) || !aligned16(c) || !aligned16(workspace))
         return R9K_ERR_ALIGN;
     if (M == 0) return R9K_OK;
-    W4Args w{a, wp, sp, zp, c, M, K, N, nullptr, nullptr, 1, 1, M, 0, nullptr, nullptr};
+    W4Args w{a, wp, sp, zp, c, M, K, N, nullptr, nullptr, 1, 1, M, 0, nullptr};
     return run_w4(w, format, group, workspace, ws_bytes, (hipStream_t)stream);
 }
 
@@ -699,30 +694,20 @@ static bool w4_moe_shape(int64_t arows, int64_t E, int64_t R, int64_t K, int64_t
            w4_shape(N, K, silu ? 32 : 16) && N <= MAX_DIM && (R == 0 || arows >= 1);
 }
 
-int r9k_moe_gemm_w4_workspace(int64_t arows, int64_t E, int64_t R, int64_t K, int64_t N, int act, size_t *bytes) {
-    if (!bytes) return R9K_ERR_NULLPTR;
-    const bool silu = act == R9K_ACT_SILU_MUL;
-    if (!w4_moe_shape(arows, E, R, K, N, silu)) return R9K_ERR_SHAPE;
-    if (act != R9K_ACT_NONE && !silu) return R9K_ERR_ARG;
-    *bytes = R ? w4_ws(arows, R, K, N, E, silu).total : 0;
-    return R9K_OK;
-}
-
 int r9k_moe_gemm_w4(const uint16_t *a, int64_t arows, const int32_t *src, int64_t topk, const int32_t *offsets,
                     int64_t E, int64_t R, int64_t K, const uint8_t *wp, const void *sp, const uint8_t *zp,
-                    int format, int group, int64_t N, int act, uint16_t *c, void *workspace,
-                    size_t ws_bytes, void *stream) {
+                    int format, int group, int64_t N, int act, uint16_t *c, void *stream) {
     if (!a || !offsets || !wp || !sp || !c) return R9K_ERR_NULLPTR;
     const bool silu = act == R9K_ACT_SILU_MUL;
     if (!w4_moe_shape(arows, E, R, K, N, silu) || topk < 1 || topk > MAX_DIM || (!src && arows < R))
         return R9K_ERR_SHAPE;
     if (!w4_known(format, group, zp != nullptr) || (act != R9K_ACT_NONE && !silu)) return R9K_ERR_ARG;
     if (!aligned16(a) || !aligned16(src) || !aligned16(offsets) || !aligned16(wp) || !aligned16(sp) ||
-        !aligned16(zp) || !aligned16(c) || !aligned16(workspace))
+        !aligned16(zp) || !aligned16(c))
         return R9K_ERR_ALIGN;
     if (R == 0) return R9K_OK;
-    W4Args w{a, wp, sp, zp, c, R, K, N, offsets, src, E, topk, arows, silu ? 1 : 0, nullptr, nullptr};
-    return run_w4(w, format, group, workspace, ws_bytes, (hipStream_t)stream);
+    W4Args w{a, wp, sp, zp, c, R, K, N, offsets, src, E, topk, arows, silu ? 1 : 0, nullptr};
+    return run_w4(w, format, group, nullptr, 0, (hipStream_t)stream);
 }
 
 // ---- rows sorted by expert -----------------------------------------------------

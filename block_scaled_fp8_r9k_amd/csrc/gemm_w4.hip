@@ -23,6 +23,7 @@
 // With silu the first half of a wave's tiles are gate columns, the second half
 // the up columns that belong to them.
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "r9k_internal.h"
@@ -32,7 +33,7 @@ namespace r9k {
 
 namespace {
 
-// LDS that a CTA's activation rows may take
+// LDS of a CTA: its activation rows, then the K slices' sums in their place
 constexpr int64_t W4_LDS = 150 * 1024;
 
 // The lane's scales (and zeros) of one tile's chunk, as loaded.
@@ -44,8 +45,11 @@ struct W4Scale {
 
 }  // namespace
 
-template <int FMT, int GRP, int MT, int NT, int D, int NTHR>
-__global__ __launch_bounds__(NTHR) void k_gemm_w4(W4Args p) {
+// LONG: the general form, for slices of more than D chunks and for activation rows
+// that do not fit LDS at once.  Without it a slice is loaded whole before its first
+// chunk is computed, in straight code: the waits are then exact, chunk by chunk.
+template <int FMT, int GRP, int MT, int NT, int D, bool LONG>
+__global__ __launch_bounds__(512) void k_gemm_w4(W4Args p) {
     constexpr int NG = 128 / GRP;  // groups a chunk
     constexpr int KPG = GRP / 32;  // MFMA steps a group
     extern __shared__ __align__(16) uint8_t lds[];
@@ -86,12 +90,21 @@ __global__ __launch_bounds__(NTHR) void k_gemm_w4(W4Args p) {
         }
     }
 
+    // the activation row of each row of the block, in lane r; an index that points
+    // outside the activations means row 0
+    uint32_t arow = r0 + min(lane, rows - 1);
+    if (p.src) {
+        arow = w4_div_topk((uint32_t)p.src[arow], (uint32_t)p.topk, p.tmagic);
+        if (arow >= (uint32_t)p.arows) arow = 0;
+    }
+
     v4f acc[NT][MT];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[j][m] = v4f{0.f, 0.f, 0.f, 0.f};
 
+    constexpr int SB = FMT == W4_MXFP4 ? 64 : 32 * NG, ZB = 16 * NG;  // bytes of scales and zeros a tile's chunk
     uint4 wr[D][NT];
     W4Scale<FMT, NG> sc[D][NT];
     const uint8_t *al[MT];
@@ -146,7 +159,7 @@ __global__ __launch_bounds__(NTHR) void k_gemm_w4(W4Args p) {
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const float z = (float)((sc[d][j].z[i] >> (8 * r)) & 255u);
+                            const float z = (float)(((sc[d][j].z[i] | p.zfill) >> (8 * r)) & 255u);
                             acc[j][m][r] = __builtin_fmaf(s[r], __builtin_fmaf(-z, sum[i][m][0], pr[m][r]), acc[j][m][r]);
                         }
                 }
@@ -154,88 +167,108 @@ __global__ __launch_bounds__(NTHR) void k_gemm_w4(W4Args p) {
         }
     };
 
-    // Segments of p.seg chunks, whose activation rows fit LDS (all of the CTA's
-    // chunks where they do); a wave takes its slice [cb, ce) of each.
-    for (int s0 = kb; s0 < ke; s0 += p.seg) {
-        const int s1 = min(ke, s0 + p.seg);
+    // The chunks [s0, s1): their activation rows go into LDS; the wave computes its
+    // slice of them.
+    auto segment = [&](int s0, int s1) {
         const int cb = min(s1, s0 + slice * p.cps), ce = min(s1, cb + p.cps);
 
         // 1. the rows into LDS, padded by 16 bytes so that the 16 rows of a fragment
         // read fall on distinct banks; a wave moves 64 16-byte pieces of a row at a
-        // time, straight into LDS.  A row index that points outside the activations
-        // reads row 0.
+        // time, straight into LDS
         const int ppr = (s1 - s0) * 16;  // pieces a row
         const int bpr = (s1 - s0 + 3) >> 2, blocks = rows * bpr, pitch = ppr * 16 + 16;
-        if (s0 > kb) __syncthreads();  // every wave is done with the segment before
         for (int i = wave; i < blocks; i += nw) {
             // bmagic = ceil(2^20 / bpr) of a whole segment
-            const int r = s1 - s0 == p.seg ? (int)((uint32_t)i * p.bmagic >> 20) : i / bpr;
+            const int r = !LONG || s1 - s0 == p.seg ? (int)((uint32_t)i * p.bmagic >> 20) : i / bpr;
             const int c0 = (i - r * bpr) * 64;
-            int64_t row = r0 + r;
-            if (p.src) {
-                const uint32_t t = w4_div_topk((uint32_t)p.src[row], (uint32_t)p.topk, p.tmagic);
-                row = t < (uint32_t)p.arows ? t : 0;
-            }
-            if (c0 + lane < ppr) load_lds16(p.a + row * p.K + s0 * 128 + 8 * (c0 + lane), lds0 + r * pitch + c0 * 16);
+            const uint16_t *row = p.a + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)arow, r) * p.K + s0 * 128;
+            if (c0 + lane < ppr) load_lds16(row + 8 * (c0 + lane), lds0 + r * pitch + c0 * 16);
         }
         __builtin_amdgcn_sched_barrier(0);
 
-        // 2. the weight stream, through one descriptor a tile that ends with the
-        // slice: loads past the end return zeros and move nothing
-        __amdgpu_buffer_rsrc_t wd[NT];
-        const uint8_t *sb[NT];
-        const uint8_t *zb[NT];
+        // 2. the weight stream, through descriptors that end with the slice: loads past
+        // the end return zeros and move nothing.  Without zero points theirs is empty.
+        __amdgpu_buffer_rsrc_t wd[NT], sd[NT], zd[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const int64_t t0 = ((int64_t)e * tiles + tile[j]) * C;  // the tile's first chunk
             wd[j] = __builtin_amdgcn_make_buffer_rsrc((void *)(p.wp + t0 * 1024), (short)0, ce * 1024, 0x00020000);
-            sb[j] = (const uint8_t *)p.sp + t0 * (FMT == W4_MXFP4 ? 64 : 32 * NG) +
-                    (FMT == W4_MXFP4 ? 4 * l16 : 8 * NG * q);
-            zb[j] = p.zp + t0 * 16 * NG + 4 * NG * q;
+            sd[j] = __builtin_amdgcn_make_buffer_rsrc((void *)((const uint8_t *)p.sp + t0 * SB), (short)0, ce * SB, 0x00020000);
+            if constexpr (FMT == W4_INT)
+                zd[j] = __builtin_amdgcn_make_buffer_rsrc((void *)(p.zp + t0 * ZB), (short)0, p.zp ? ce * ZB : 0, 0x00020000);
         }
-        auto load = [&](int c, int d) {
-            const int cc = max(min(c, ce - 1), 0);  // the scales' loads stay inside the weight
+        const int wvo = 16 * lane, svo = FMT == W4_MXFP4 ? 4 * l16 : 8 * NG * q, zvo = 4 * NG * q;
+        auto load_scales = [&](int c, int d) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 if constexpr (FMT == W4_MXFP4) {
-                    sc[d][j].s[0] = *(const uint32_t *)(sb[j] + (int64_t)cc * 64);
+                    sc[d][j].s[0] = __builtin_amdgcn_raw_buffer_load_b32(sd[j], svo + c * SB, 0, 0);
+                } else if constexpr (NG == 1) {
+                    const auto v = __builtin_amdgcn_raw_buffer_load_b64(sd[j], svo + c * SB, 0, 0);
+                    sc[d][j].s[0] = v[0];
+                    sc[d][j].s[1] = v[1];
+                    sc[d][j].z[0] = __builtin_amdgcn_raw_buffer_load_b32(zd[j], zvo + c * ZB, 0, 0);
                 } else {
-                    const uint2 *s2 = (const uint2 *)(sb[j] + (int64_t)cc * 32 * NG);
 #pragma unroll
-                    for (int i = 0; i < NG; ++i) {
-                        sc[d][j].s[2 * i] = s2[i].x;
-                        sc[d][j].s[2 * i + 1] = s2[i].y;
+                    for (int i = 0; i < NG / 2; ++i) {
+                        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(sd[j], svo + c * SB + 16 * i, 0, 0);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) sc[d][j].s[4 * i + r] = v[r];
                     }
-                    if (p.zp) {
-#pragma unroll
-                        for (int i = 0; i < NG; ++i)
-                            sc[d][j].z[i] = *(const uint32_t *)(zb[j] + (int64_t)cc * 16 * NG + 4 * i);
+                    if constexpr (NG == 2) {
+                        const auto v = __builtin_amdgcn_raw_buffer_load_b64(zd[j], zvo + c * ZB, 0, 0);
+                        sc[d][j].z[0] = v[0];
+                        sc[d][j].z[1] = v[1];
                     } else {
+                        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(zd[j], zvo + c * ZB, 0, 0);
 #pragma unroll
-                        for (int i = 0; i < NG; ++i) sc[d][j].z[i] = 0x08080808u;
+                        for (int r = 0; r < 4; ++r) sc[d][j].z[r] = v[r];
                     }
                 }
             }
+        };
+        auto load_codes = [&](int c, int d) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) wr[d][j] = load_buf_nt16(wd[j], 16 * lane + c * 1024);
+            for (int j = 0; j < NT; ++j) wr[d][j] = load_buf_nt16(wd[j], wvo + c * 1024);
         };
 #pragma unroll
-        for (int d = 0; d < D; ++d) load(cb + d, d);
+        for (int d = 0; d < D; ++d) load_scales(cb + d, d);
         __builtin_amdgcn_sched_barrier(0);
-
-        // the rows have landed once at most the D * NT code loads behind them are in flight
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            load_codes(cb + d, d);
+            __builtin_amdgcn_sched_barrier(0);  // in the order of use
+        }
+        // the rows (and scales) have landed once at most the D * NT code loads behind them are in flight
         wait_vm<D * NT>();
         __syncthreads();
 #pragma unroll
         for (int m = 0; m < MT; ++m) al[m] = lds + min(16 * m + l16, rows - 1) * pitch + 16 * q;
 
-        for (int c = cb; c < ce; c += D) {
+        if constexpr (LONG) {
+            for (int c = cb; c < ce; c += D) {
 #pragma unroll
-            for (int d = 0; d < D; ++d) {
-                if (c + d < ce) compute(c + d - s0, d);
-                if (c + d + D < ce) load(c + d + D, d);
+                for (int d = 0; d < D; ++d) {
+                    if (c + d < ce) compute(c + d - s0, d);
+                    if (c + d + D < ce) {
+                        load_scales(c + d + D, d);
+                        load_codes(c + d + D, d);
+                    }
+                }
             }
+        } else {
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+                if (cb + d < ce) compute(cb + d - s0, d);
         }
+    };
+    if constexpr (LONG) {
+        for (int s0 = kb; s0 < ke; s0 += p.seg) {
+            if (s0 > kb) __syncthreads();  // every wave is done with the segment before
+            segment(s0, min(ke, s0 + p.seg));
+        }
+    } else {
+        segment(kb, ke);
     }
 
 #pragma unroll
@@ -279,51 +312,95 @@ __global__ __launch_bounds__(NTHR) void k_gemm_w4(W4Args p) {
     }
 }
 
-// [first version: one rule for every shape]
-W4Cfg w4_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
-    W4Cfg c;
-    const int64_t rows = E ? (M + E - 1) / E : M, C = K / 128;
-    c.mt = rows <= 16 ? 1 : 2;
-    c.nt = 2;
-    c.wn = 1;
-    c.wk = 8;
-    c.ksplit = 1;
-    const int *f = tuning().w4;
-    if (f[0]) c.nt = f[0];
-    if (f[1]) c.wn = f[1];
-    if (f[2]) c.wk = f[2];
-    if (f[3] && !E) c.ksplit = f[3];
-    if (silu && c.nt == 1) c.nt = 2;
-    c.ksplit = (int)std::min<int64_t>(c.ksplit, C);
-    const int64_t most = std::min<int64_t>(M, 16 * c.mt), span = (C + c.ksplit - 1) / c.ksplit;
-    const int64_t fit = std::max<int64_t>(1, (W4_LDS / most - 16) / 256);  // chunks of a segment
-    c.seg = (int)(span <= fit ? span : (span + (span + fit - 1) / fit - 1) / ((span + fit - 1) / fit));
-    c.ksplit = (int)((C + span - 1) / span);  // no split without chunks
-    c.wk = (int)std::min<int64_t>(c.wk, c.seg);
-    const int waves = c.mt == 1 ? 16 : 8;
-    while (c.wn > waves || (c.wn & (c.wn - 1))) --c.wn;
-    c.wk = std::min(c.wk, waves / c.wn);
-    return c;
+// The launch of the least estimated time.  A compute unit's CTAs take turns for the
+// LDS and registers they need; its busiest unit moves A (activations into LDS) and W
+// (codes) and pays for each CTA and wave; a turn is as long as the longest slice; a K
+// split adds its partials and the reduce launch.  Fitted to 28 dense shapes (M = 1, 4, 16,
+// 32; K and N from 512 to 14336) and 4 expert shapes in int4 (group 128, zeros) and
+// mxfp4, 17 launches each, in graphs with the weights out of the caches: the launch
+// it picks takes 3% longer than the fastest of the 17 on average (at most 16%).
+// E.g. one row of 4096 x 4096 5.1 us with four slices of one tile a wave, 5.6 with eight;
+// 16 rows of 14336 x 4096 16 us in four splits, 24 in one.
+struct W4Shape {
+    int nt, wn, wk;
+};
+static double w4_cost(const W4Cfg &c, int64_t rows, int64_t C, int64_t M, int64_t N, double items) {
+    const int waves = c.wn * c.wk;
+    const int64_t span = (C + c.ksplit - 1) / c.ksplit, segs = (span + c.seg - 1) / c.seg;
+    const int64_t tiles = N / 16, per = (int64_t)c.nt * c.wn;
+    const double ctas = (double)((tiles + per - 1) / per * c.ksplit) * items;
+    const double lds = (double)std::max<int64_t>(rows * (c.seg * 256 + 16), (int64_t)waves * c.nt * c.mt * 1024);
+    const double fit = std::max(1.0, std::min(std::floor(163840.0 / lds), std::floor(20.0 / waves)));
+    const double rounds = std::ceil(ctas / 256.0), turns = std::ceil(rounds / fit);
+    double us = 2.1 + rounds * (0.0176 * 0.25 * (double)(rows * span) + 0.0356 * (double)(per * span) + 0.175 + 0.059 * waves);
+    us += turns * (0.1115 * (double)((c.seg + c.wk - 1) / c.wk * segs * c.nt * c.mt) + 1.12 * (double)(segs - 1));
+    if (c.ksplit > 1) us += 2.5 + 2.0e-6 * (double)(c.ksplit * M * N);
+    return us;
 }
 
-template <int FMT, int GRP, int MT, int NT, int NTHR>
+W4Cfg w4_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
+    static constexpr W4Shape shapes[] = {{1, 1, 4}, {1, 1, 8}, {1, 2, 2}, {1, 2, 4}, {1, 4, 2}, {2, 1, 2},
+                                         {2, 1, 4}, {2, 1, 8}, {2, 2, 2}, {2, 2, 4}, {2, 4, 2}};
+    const int64_t C = K / 128;
+    // experts: the row blocks that uniform routing makes, and the rows of one
+    const double touched = E ? (double)E * (1.0 - std::pow(1.0 - 1.0 / (double)E, (double)M)) : 1.0;
+    const double ave = (double)M / touched;
+    W4Cfg best{};
+    best.mt = (E ? ave : (double)M) <= 16.0 ? 1 : 2;
+    const int64_t RB = 16 * best.mt, most = std::min<int64_t>(M, RB);
+    const int64_t rows = E ? std::min<int64_t>(most, (int64_t)std::ceil(ave)) : most;
+    const double items = E ? touched * std::max(1.0, ave / (double)RB) : (double)((M + RB - 1) / RB);
+    const int64_t fit = std::max<int64_t>(1, (W4_LDS / most - 16) / 256);  // chunks whose rows fit LDS
+    const int *tune = tuning().w4;
+    const W4Shape wish{std::max(tune[0], silu ? 2 : 1), tune[1], tune[2]};
+    bool force = false;
+    for (const W4Shape &sh : shapes) force |= tune[0] && sh.nt == wish.nt && sh.wn == wish.wn && sh.wk == wish.wk;
+    double best_us = 0.0;
+    for (const W4Shape &sh : shapes) {
+        if (force && (sh.nt != wish.nt || sh.wn != wish.wn || sh.wk != wish.wk)) continue;
+        if (silu && sh.nt == 1) continue;
+        for (int ks = 1; ks <= (E ? 1 : 4); ks *= 2) {
+            W4Cfg c = best;
+            c.nt = sh.nt;
+            c.wn = sh.wn;
+            const int64_t want = force && tune[3] && !E ? tune[3] : ks;
+            // a split where one CTA a compute unit is not reached without it
+            if (!force && ks > 1 && (double)(N / 16) / (sh.nt * sh.wn) * items * (ks / 2) >= 256.0) break;
+            const int64_t span = (C + std::min(want, C) - 1) / std::min(want, C);
+            c.ksplit = (int)((C + span - 1) / span);  // no split without chunks
+            const int64_t segs = (span + fit - 1) / fit;
+            c.seg = (int)((span + segs - 1) / segs);
+            c.wk = (int)std::min<int64_t>(sh.wk, c.seg);
+            const double us = w4_cost(c, rows, C, M, N, items);
+            if (best_us == 0.0 || us < best_us) {
+                best_us = us;
+                best = c;
+            }
+        }
+    }
+    return best;
+}
+
+// chunks ahead: as many registers as two waves a SIMD leave, scales included
+template <int FMT, int GRP, int NT>
+constexpr int W4_AHEAD = (GRP == 32 && FMT == W4_INT ? 4 : 8) / NT;
+
+template <int FMT, int GRP, int MT, int NT, bool LONG>
 static hipError_t launch_one(W4Args a, const W4Cfg &c, hipStream_t s) {
-    // chunks ahead: as many registers as two waves a SIMD leave, scales included
-    constexpr int D = (GRP == 32 && FMT == W4_INT ? 4 : 8) / NT;
-    auto kernel = k_gemm_w4<FMT, GRP, MT, NT, D, NTHR>;
+    auto kernel = k_gemm_w4<FMT, GRP, MT, NT, W4_AHEAD<FMT, GRP, NT>, LONG>;
+    // the dynamic LDS limit is a per-device function attribute: set it once per device
     static std::once_flag once[64];
     static hipError_t attr_err[64];
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return hipErrorInvalidDevice;
     std::call_once(once[dev], [&] {
-        attr_err[dev] = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+        attr_err[dev] = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, W4_LDS);
     });
     if (attr_err[dev] != hipSuccess) return attr_err[dev];
     const int64_t per = (int64_t)c.wn * (a.silu ? NT / 2 : NT), tiles = a.N / 16 / (a.silu ? 2 : 1);
-    const int64_t RB = 16 * MT;
+    const int64_t nblk = (tiles + per - 1) / per, RB = 16 * MT, C = a.K / 128;
     int64_t items = (a.M + RB - 1) / RB;
     if (a.offsets) items = (a.M + std::min(a.E, a.M) * (RB - 1)) / RB;
-    const int64_t nblk = (tiles + per - 1) / per, C = a.K / 128;
     a.wnl = __builtin_ctz((unsigned)c.wn);
     a.ksplit = c.ksplit;
     a.span = (int)((C + c.ksplit - 1) / c.ksplit);
@@ -332,19 +409,26 @@ static hipError_t launch_one(W4Args a, const W4Cfg &c, hipStream_t s) {
     const int bpr = (a.seg + 3) / 4;
     a.bmagic = (uint32_t)(((1 << 20) + bpr - 1) / bpr);
     a.tmagic = a.topk > 1 ? (uint32_t)(((uint64_t(1) << 32) + a.topk - 1) / a.topk) : 0;
-    const size_t rows = (size_t)std::min<int64_t>(a.M, RB) * (size_t)(c.seg * 256 + 16);
+    a.zfill = a.zp ? 0u : 0x08080808u;
+    const size_t rows = (size_t)std::min<int64_t>(a.M, RB) * (size_t)(a.seg * 256 + 16);
     const size_t lds = std::max<size_t>(rows, (size_t)c.wn * c.wk * NT * MT * 1024);
-    if (nblk > 0x7fffffff || items > 65535 || lds > 160 * 1024 || 64 * c.wn * c.wk > NTHR) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)nblk, (unsigned)items, (unsigned)c.ksplit), dim3(64 * c.wn * c.wk), lds, s, a);
+    if (nblk > 0x7fffffff || items > 65535 || lds > (size_t)W4_LDS || c.wn * c.wk > 8) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)nblk, (unsigned)items, (unsigned)c.ksplit), dim3(64 * c.wn * c.wk), lds,
+                       s, a);
     return hipGetLastError();
+}
+
+template <int FMT, int GRP, int MT, int NT>
+static hipError_t launch_nt(const W4Args &a, const W4Cfg &c, hipStream_t s) {
+    // one segment, the same in every split, and slices that are loaded whole
+    const int64_t C = a.K / 128, span = (C + c.ksplit - 1) / c.ksplit;
+    const bool whole = c.seg >= span && C % span == 0 && (c.seg + c.wk - 1) / c.wk <= W4_AHEAD<FMT, GRP, NT>;
+    return whole ? launch_one<FMT, GRP, MT, NT, false>(a, c, s) : launch_one<FMT, GRP, MT, NT, true>(a, c, s);
 }
 
 template <int FMT, int GRP, int MT>
 static hipError_t launch_mt(const W4Args &a, const W4Cfg &c, hipStream_t s) {
-    if constexpr (MT == 1)
-        if (c.wn * c.wk > 8)
-            return c.nt == 1 ? launch_one<FMT, GRP, MT, 1, 1024>(a, c, s) : launch_one<FMT, GRP, MT, 2, 1024>(a, c, s);
-    return c.nt == 1 ? launch_one<FMT, GRP, MT, 1, 512>(a, c, s) : launch_one<FMT, GRP, MT, 2, 512>(a, c, s);
+    return c.nt == 1 ? launch_nt<FMT, GRP, MT, 1>(a, c, s) : launch_nt<FMT, GRP, MT, 2>(a, c, s);
 }
 
 template <int FMT, int GRP>

@@ -2,21 +2,20 @@
 //
 // The same sums as the weight-streaming kernel (gemm_w4.hip), for row counts at
 // which the matrix instructions and not the weight bytes set the time.  C^T = W
-// A^T: each wave owns TN column tiles by four row tiles of 16; a CTA is 4 waves
-// along the columns by WM along the rows, 64 TN columns by 64 WM rows.
+// A^T: four waves along the columns, each with TN column tiles by four row tiles of
+// 16; a CTA is 64 TN columns by 64 rows.
 //
 // Per chunk of 128 K a stage in LDS holds the A tile (bf16), the packed codes of
-// the column tiles and their scales, all moved there by global_load_lds, NST - 1
-// chunks ahead.  A wave converts its codes to bf16 fragments once a chunk, in
+// the column tiles, their scales and zeros, all moved there by global_load_lds, NST
+// - 1 chunks ahead.  A wave converts its codes to bf16 fragments once a chunk, in
 // registers, and uses them for its four row tiles.
 //   int4: a group's product P starts from zero and is promoted into the fp32 sum
 //   by acc += s * P, so neither the weights nor the sums are rounded.  The zero
-//   points are not in the loop: sum_g z s S_g (S_g the sum of a group's activations)
-//   is itself a matrix product with K / group terms, and goes into the sums first,
-//   on the matrix cores: s z holds 12 bits, two bf16; S_g, fp32, is three; the six
-//   products are exact and take six of a lane quarter's eight K positions, four
-//   groups to an instruction.  S_g comes from a launch of its own (k_w4_sums), one
-//   pass over the activations.
+//   points' share, sum_g z s S_g (S_g the sum of a group's activations), is a matrix
+//   product with one term a group, and goes through the matrix cores too, every four
+//   groups: s z holds 12 bits, two bf16; S_g, fp32, is three; the six products are
+//   exact and take six of a lane quarter's eight K positions.  Wave w takes the sums of
+//   row tile w (an MFMA with ones for weights) and leaves them, split, in LDS.
 //   mxfp4: the scale is in the converted fragment (a power of two, exact) and the
 //   matrix instruction accumulates through all of K.
 // A rows are 256 bytes in LDS; 16-byte piece p of row r lies at piece p ^ (r % 16),
@@ -29,56 +28,38 @@
 
 namespace r9k {
 
-// Sums of each group's activations, fp32: sums[row][g], rows padded with zeros to
-// a multiple of four groups.
-__global__ __launch_bounds__(256) void k_w4_sums(const uint4 *__restrict__ a, int64_t n8, int k8, int grp, int G,
-                                                 int G4, float *__restrict__ sums) {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= n8) return;  // whole rows of 16 lanes and more: a group's lanes leave together
-    const uint4 v = a[id];
-    float s = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) +
-              ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
-    const int lanes = grp / 8;
-    for (int d = 1; d < lanes; d <<= 1) s += __shfl_xor(s, d, 64);
-    if ((threadIdx.x & (lanes - 1)) == 0) {
-        const int64_t row = id / k8;
-        const int g = (int)(id % k8) * 8 / grp;
-        sums[row * G4 + g] = s;
-        if (g == G - 1)
-            for (int p = G; p < G4; ++p) sums[row * G4 + p] = 0.0f;
-    }
-}
-
 namespace {
-template <int FMT, int GRP, int TN_, int WM_, int NST_>
+template <int FMT, int GRP, int TN_, int NST_>
 struct W4Tile {
-    static constexpr int TN = TN_, WM = WM_, NST = NST_, NW = 4 * WM, THREADS = 64 * NW;
+    static constexpr int TN = TN_, NST = NST_, THREADS = 256, BM = 64;
     static constexpr int NG = 128 / GRP, KPG = GRP / 32;
-    static constexpr int BM = 64 * WM;
     static constexpr int ABYTES = BM * 256, WBYTES = 4 * TN * 1024;
     static constexpr int SDW = FMT == W4_MXFP4 ? 16 * TN : 8 * NG * TN;  // dwords of a wave's scales
-    static constexpr int SLOADS = (SDW + 63) / 64, SBYTES = SLOADS * 256;
-    static constexpr int STAGE = ABYTES + WBYTES + NW * SBYTES;
-    static constexpr int WLOADS = 4 * TN / NW, ALOADS = 4;
-    static constexpr int LOADS = WLOADS + ALOADS + SLOADS;  // load instructions a wave and stage
-    static constexpr int CPITCH = 64 * TN * 2 + 16;         // output tile rows in LDS
-    static constexpr int SMEM = NST * STAGE > BM * CPITCH ? NST * STAGE : BM * CPITCH;
-    static_assert(WLOADS * NW == 4 * TN, "loads split evenly");
+    static constexpr int ZDW = FMT == W4_MXFP4 ? 0 : 4 * NG * TN;        // and zeros
+    static constexpr int SLOADS = (SDW + 63) / 64, ZLOADS = (ZDW + 63) / 64;
+    static constexpr int SBYTES = SLOADS * 256, ZBYTES = ZLOADS * 256;
+    static constexpr int STAGE = ABYTES + WBYTES + 4 * (SBYTES + ZBYTES);
+    static constexpr int LOADS = TN + 4 + SLOADS + ZLOADS;  // load instructions a wave and stage
+    static constexpr int SUMS = FMT == W4_MXFP4 ? 0 : 2 * BM * 4 * 16;  // two steps of split sums, 4 groups each
+    static constexpr int CPITCH = 64 * TN * 2 + 16;                     // output tile rows in LDS
+    static constexpr int SMEM = NST * STAGE + SUMS > BM * CPITCH ? NST * STAGE + SUMS : BM * CPITCH;
     static_assert(SMEM <= 160 * 1024, "LDS");
+    static_assert((NST - 2) * LOADS < 64, "vmcnt");
 };
 
 __device__ __forceinline__ uint32_t hi16(float lo, float hi) {  // upper halves of two fp32
     return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
 }
+__device__ __forceinline__ float top16(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
 }  // namespace
 
 template <int FMT, int GRP, class T>
 __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
     constexpr int TN = T::TN, NG = T::NG, KPG = T::KPG, NST = T::NST, BM = T::BM;
+    constexpr int CPS = 4 / NG;  // chunks of a zero point step (four groups)
     extern __shared__ __align__(16) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wn = wave & 3, wm = wave >> 2;
     const int C = (int)(p.K / 128), tiles = (int)(p.N / 16);
 
     // block -> (column block, row block).  Blocks go round-robin to the 8 XCDs.
@@ -133,41 +114,54 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
         return t < (uint32_t)p.arows ? t : 0;
     };
 
-    // this wave's share of a stage's loads
-    const uint8_t *ap[T::ALOADS], *wp[T::WLOADS], *sp[T::SLOADS];
+    // this wave's share of a stage's loads: a quarter of the rows, its own column
+    // tiles with their scales and zeros (without zero points the scales again, unread)
+    const uint8_t *ap[4], *wp[TN], *sp[T::SLOADS], *zp[T::ZLOADS + 1];
 #pragma unroll
-    for (int u = 0; u < T::ALOADS; ++u) {
-        const int row = 4 * (T::ALOADS * wave + u) + q;  // 4 rows of 16 pieces an instruction
+    for (int u = 0; u < 4; ++u) {
+        const int row = 4 * (4 * wave + u) + q;  // 4 rows of 16 pieces an instruction
         ap[u] = (const uint8_t *)p.a + source_row(r0 + row) * p.K * 2 + cb * 256 + 16 * (l16 ^ (row & 15));
     }
 #pragma unroll
-    for (int u = 0; u < T::WLOADS; ++u) {
-        const int idx = T::WLOADS * wave + u;
-        wp[u] = p.wp + (((int64_t)e * tiles + col_tile(idx / TN, idx % TN)) * C + cb) * 1024 + 16 * lane;
-    }
+    for (int u = 0; u < TN; ++u)
+        wp[u] = p.wp + (((int64_t)e * tiles + col_tile(wave, u)) * C + cb) * 1024 + 16 * lane;
+    constexpr int SPT = 4 * T::SDW / TN, ZPT = 4 * T::ZDW / TN;  // bytes a tile's chunk
 #pragma unroll
     for (int u = 0; u < T::SLOADS; ++u) {
-        constexpr int DPT = T::SDW / TN;  // dwords a tile
-        const int d = min(64 * u + lane, T::SDW - 1);
-        sp[u] = (const uint8_t *)p.sp + (((int64_t)e * tiles + col_tile(wn, d / DPT)) * C + cb) * (4 * DPT) + 4 * (d % DPT);
+        const int d = min(64 * u + lane, T::SDW - 1) * 4;
+        sp[u] = (const uint8_t *)p.sp + (((int64_t)e * tiles + col_tile(wave, d / SPT)) * C + cb) * SPT + d % SPT;
+    }
+    if constexpr (FMT == W4_INT) {
+#pragma unroll
+        for (int u = 0; u < T::ZLOADS; ++u) {
+            const int d = min(64 * u + lane, T::ZDW - 1) * 4;
+            const uint8_t *z = p.zp ? p.zp : (const uint8_t *)p.sp;
+            zp[u] = z + (((int64_t)e * tiles + col_tile(wave, d / ZPT)) * C + cb) * ZPT + d % ZPT;
+        }
     }
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
+    const int soff = T::ABYTES + T::WBYTES + wave * (T::SBYTES + T::ZBYTES), zoff = soff + T::SBYTES;
     auto issue = [&](int st) {
         const uint32_t base = lds0 + st * T::STAGE;
 #pragma unroll
-        for (int u = 0; u < T::WLOADS; ++u) {
-            load_lds16(wp[u], base + T::ABYTES + (T::WLOADS * wave + u) * 1024);
+        for (int u = 0; u < TN; ++u) {
+            load_lds16(wp[u], base + T::ABYTES + (TN * wave + u) * 1024);
             wp[u] += 1024;
         }
 #pragma unroll
-        for (int u = 0; u < T::ALOADS; ++u) {
-            load_lds16(ap[u], base + (T::ALOADS * wave + u) * 1024);
+        for (int u = 0; u < 4; ++u) {
+            load_lds16(ap[u], base + (4 * wave + u) * 1024);
             ap[u] += 256;
         }
 #pragma unroll
         for (int u = 0; u < T::SLOADS; ++u) {
-            load_lds4(sp[u], base + T::ABYTES + T::WBYTES + wave * T::SBYTES + u * 256);
-            sp[u] += 4 * (T::SDW / TN);
+            load_lds4(sp[u], base + soff + u * 256);
+            sp[u] += SPT;
+        }
+#pragma unroll
+        for (int u = 0; u < T::ZLOADS; ++u) {
+            load_lds4(zp[u], base + zoff + u * 256);
+            zp[u] += ZPT;
         }
     };
 
@@ -177,42 +171,34 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
 #pragma unroll
         for (int m = 0; m < 4; ++m) acc[j][m] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    if constexpr (FMT == W4_INT) {
-        // acc -= sum_g (s z)[n][g] * S[m][g]; lane: row l16 of either operand, group 4 i + q
-        const float *srow[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) srow[m] = p.sums + source_row(r0 + 64 * wm + 16 * m + l16) * p.g4 + q;
-        const int g0 = cb * NG, g1 = ce * NG;
-        for (int i = g0 / 4; 4 * i < g1; ++i) {
-            const int g = 4 * i + q;
-            const bool mine = g >= g0 && g < g1;
-            w4_v8bf sf[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float s = srow[m][4 * i];
-                const float h = __uint_as_float(__float_as_uint(s) & 0xFFFF0000u), d = s - h;
-                const float mm = __uint_as_float(__float_as_uint(d) & 0xFFFF0000u), l = d - mm;
-                sf[m] = __builtin_bit_cast(w4_v8bf, w4_v4u{hi16(h, mm), hi16(l, h), hi16(mm, l), 0});
-            }
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const int64_t at = ((((int64_t)e * tiles + col_tile(wn, j)) * C + min(g / NG, C - 1)) * 4 + (l16 >> 2)) * NG * 4 +
-                                   (g % NG) * 4 + (l16 & 3);
-                const float s = __uint_as_float((uint32_t)((const uint16_t *)p.sp)[at] << 16);
-                const float z = p.zp ? (float)p.zp[at] : 8.0f;
-                const float f = mine ? -s * z : 0.0f;
-                const float h = __uint_as_float(__float_as_uint(f) & 0xFFFF0000u), l = f - h;
-                const w4_v8bf wf = __builtin_bit_cast(w4_v8bf, w4_v4u{hi16(h, h), hi16(h, l), hi16(l, l), 0});
-#pragma unroll
-                for (int m = 0; m < 4; ++m) acc[j][m] = w4_mfma(wf, sf[m], acc[j][m]);
-            }
-        }
-    }
-
     // fragment addresses inside a stage: row tile m, step k at (aoff ^ 64 k) + 4096 m
-    const int aoff = (64 * wm + l16) * 256 + ((q ^ l16) << 4);
-    const int woff = T::ABYTES + wn * TN * 1024 + 16 * lane;
-    const int soff = T::ABYTES + T::WBYTES + wave * T::SBYTES;
+    const int aoff = l16 * 256 + ((q ^ l16) << 4);
+    const int woff = T::ABYTES + wave * TN * 1024 + 16 * lane;
+
+    // Zero points.  sz: -s z of row l16 of each column tile, for the step's group q;
+    // split sums of row r, group g of a step: 16 bytes at (r * 4 + g) * 16 of its half.
+    float sz[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) sz[j] = 0.0f;
+    uint8_t *sums = lds + NST * T::STAGE;
+    int cis = 0, half = 0;  // chunk in the step, the step's half
+    auto zero_step = [&](int h, int groups) {  // acc += sz x sums over the step's groups
+        w4_v8bf sf[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            uint4 v = *(const uint4 *)(sums + h * (T::SUMS / 2) + ((16 * m + l16) * 4 + q) * 16);
+            if (q >= groups) v = make_uint4(0, 0, 0, 0);
+            sf[m] = w4_frag(v);
+        }
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const float hi = top16(sz[j]), lo = sz[j] - hi;
+            const w4_v8bf wf = __builtin_bit_cast(w4_v8bf, w4_v4u{hi16(hi, hi), hi16(hi, lo), hi16(lo, lo), 0});
+#pragma unroll
+            for (int m = 0; m < 4; ++m) acc[j][m] = w4_mfma(wf, sf[m], acc[j][m]);
+            sz[j] = 0.0f;
+        }
+    };
 
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // from here on only the stages' loads are counted
 #pragma unroll
@@ -220,8 +206,9 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
         if (cb + k < ce) issue(k);
     int st = 0;
     for (int c = cb; c < ce; ++c) {
-        // this chunk's stage has landed: the wave's loads issued after it are those of chunk c + 1 (three stages)
-        if (NST == 3 && c + 1 < ce) wait_vm<T::LOADS>();
+        // this chunk's stage has landed: the wave's loads issued after it are those of the NST - 2 chunks behind it
+        // (fewer at the end: then wait for all)
+        if (c + NST - 2 < ce) wait_vm<(NST - 2) * T::LOADS>();
         else wait_vm<0>();
         __syncthreads();
         if (c + NST - 1 < ce) issue(st == 0 ? NST - 1 : st - 1);
@@ -250,9 +237,29 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
                 }
             }
         } else {
+            // the step before is complete: its sums are in LDS since the barrier
+            if (c > cb && cis == 0) zero_step(half ^ 1, 4);
+            // the sums of row tile `wave`, as three bf16 pieces against the pieces of sz in zero_step
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                v4f sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < KPG; ++k)
+                    sum = w4_mfma(w4_ones(), w4_frag(*(const uint4 *)(sb + (aoff ^ (64 * (i * KPG + k))) + 4096 * wave)), sum);
+                const float h = top16(sum[0]), d = sum[0] - h, mid = top16(d), l = d - mid;
+                if (q == 0)
+                    *(uint4 *)(sums + half * (T::SUMS / 2) + ((16 * wave + l16) * 4 + cis * NG + i) * 16) =
+                        make_uint4(hi16(h, mid), hi16(l, h), hi16(mid, l), 0);
+            }
             uint4 code[TN];
 #pragma unroll
-            for (int j = 0; j < TN; ++j) code[j] = *(const uint4 *)(sb + woff + 1024 * j);
+            for (int j = 0; j < TN; ++j) {
+                code[j] = *(const uint4 *)(sb + woff + 1024 * j);
+                const int at = ((l16 >> 2) * NG + q % NG) * 4 + (l16 & 3);
+                const float s = __uint_as_float((uint32_t)*(const uint16_t *)(sb + soff + SPT * j + 2 * at) << 16);
+                const float z = p.zp ? (float)*(sb + zoff + ZPT * j + at) : 8.0f;
+                if (q / NG == cis) sz[j] = -s * z;
+            }
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 w4_v8bf wf[TN][KPG];
@@ -262,7 +269,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
                     const uint32_t word[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
 #pragma unroll
                     for (int k = 0; k < KPG; ++k) wf[j][k] = w4_int_frag(word[i * KPG + k]);
-                    const uint2 s2 = *(const uint2 *)(sb + soff + 32 * NG * j + 8 * NG * q + 8 * i);
+                    const uint2 s2 = *(const uint2 *)(sb + soff + SPT * j + 8 * NG * q + 8 * i);
                     s[j][0] = bf16_lo(s2.x);
                     s[j][1] = bf16_hi(s2.x);
                     s[j][2] = bf16_lo(s2.y);
@@ -287,23 +294,32 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
                         for (int r = 0; r < 4; ++r) acc[j][m][r] = __builtin_fmaf(s[j][r], pr[j][r], acc[j][m][r]);
                 }
             }
+            if (++cis == CPS) {
+                cis = 0;
+                half ^= 1;
+            }
         }
+    }
+    if constexpr (FMT == W4_INT) {
+        __syncthreads();  // the last step's sums; it may hold fewer than four groups
+        if (cis) zero_step(half, cis * NG);
+        else zero_step(half ^ 1, 4);
     }
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int m = 0; m < 4; ++m) pin_acc(acc[j][m]);  // the MFMAs run with every lane enabled
 
-    // lane holds, per tile (j, m), row 64 wm + 16 m + l16 and columns 4 q .. +3 of tile j
+    // lane holds, per tile (j, m), row 16 m + l16 and columns 4 q .. +3 of tile j
     const int rows = r1 - r0;
     if (p.ksplit > 1) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-            const int t = (bx * 4 + wn) * TN + j;
+            const int t = (bx * 4 + wave) * TN + j;
             if (t >= tiles) continue;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const int r = 64 * wm + 16 * m + l16;
+                const int r = 16 * m + l16;
                 if (r < rows) *(v4f *)(p.part + ((int64_t)ks * p.M + r0 + r) * p.N + 16 * t + 4 * q) = acc[j][m];
             }
         }
@@ -329,7 +345,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
         if (16 * j >= wcols) continue;
 #pragma unroll
         for (int m = 0; m < 4; ++m)
-            *(uint2 *)(lds + (64 * wm + 16 * m + l16) * T::CPITCH + 2 * (wn * wcols + 16 * j + 4 * q)) = w4_bf16x4(acc[j][m]);
+            *(uint2 *)(lds + (16 * m + l16) * T::CPITCH + 2 * (wave * wcols + 16 * j + 4 * q)) = w4_bf16x4(acc[j][m]);
     }
     __syncthreads();
     const int64_t ldc = p.silu ? p.N / 2 : p.N;
@@ -342,29 +358,49 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
     }
 }
 
+// From 33 rows on, where the streaming kernel would read the weight more than once (for
+// experts from 14 rows on average, where many have more than 16: 2048 -> 2 x 768 of 128
+// experts, int4, 51.1 against 79.1 us at 8 rows an expert, 81.6 against 77.8 at 16, 118
+// against 77.7 at 32): the column tiles a wave and the K split of the least estimated time.  A chunk of a CTA takes `alone` when it has the
+// compute unit to itself and `shared` where the unit's CTAs keep it busy; a split adds
+// the partials and the reduce launch.  Fitted to 16 shapes (48 to 400 rows, K and N from
+// 1024 to 14336, int4 in groups of 128 with zeros, each of 12 launches): within 6%
+// (rms), and the pick 0.5% behind the fastest on average (at most 6%; other formats up
+// to 10%).  E.g. 100 rows of 4096 x 4096: 18.7 us in 4 splits of 2 tiles a wave, 26.5 whole.
+// Prefill and experts take 4 tiles a wave (4096 x 4096 x 12288: 426 us, 533 with 2).
 W4TiledCfg w4_tiled_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
-    W4TiledCfg c{0, 4, 1};
-    const int64_t rows = E ? (M + E - 1) / E : M;
-    if (rows > 32) c.wm = 1;  // [first version]
+    static constexpr struct {
+        int tn;
+        double alone, shared;
+    } costs[] = {{1, 0.77, 0.555}, {2, 1.03, 0.747}, {4, 1.615, 1.115}};
+    W4TiledCfg best{false, 4, 1};
     const int *force = tuning().w4_tiled;
-    if (force[0] >= 0) {
-        c.wm = force[0];
-        if (force[1]) c.tn = force[1];
-        if (force[2] && !E) c.ksplit = (int)std::min<int64_t>(force[2], K / 128);
+    best.on = force[0] >= 0 ? force[0] > 0 : E ? M > 14 * E : M > 32;
+    if (!best.on) return best;
+    const int64_t C = K / 128, tiles = N / 16;
+    double best_us = 0.0;
+    for (const auto &t : costs) {
+        if (E && t.tn != 4 && !(force[0] > 0 && force[1] == t.tn && !(silu && t.tn == 1))) continue;
+        if (!E && force[0] > 0 && force[1] && force[1] != t.tn) continue;
+        for (int64_t ks = 1; ks <= (E ? 1 : 8) && ks <= C; ks *= 2) {
+            const int64_t want = force[0] > 0 && force[2] && !E ? std::min<int64_t>(force[2], C) : ks;
+            const double ctas = (double)((M + 63) / 64 * ((tiles + 4 * t.tn - 1) / (4 * t.tn)) * want);
+            double load = ctas / 256.0;
+            if (load <= 2.0) load = std::ceil(load);
+            double us = 3.6 + (double)((C + want - 1) / want) * std::max(t.alone, load * t.shared);
+            if (want > 1) us += 2.8 + 1.7e-6 * (double)(want * M * N);
+            if (best_us == 0.0 || us < best_us) {
+                best_us = us;
+                best = W4TiledCfg{true, t.tn, (int)want};
+            }
+        }
     }
-    if (silu && c.tn == 1) c.tn = 2;
-    return c;
+    return best;
 }
 
-static int64_t w4_g4(int64_t K, int grp) { return (K / grp + 3) / 4 * 4; }
-
-size_t w4_sums_bytes(int64_t rows, int64_t K, int grp) {
-    return align_up((size_t)rows * (size_t)w4_g4(K, grp) * 4, 256);
-}
-
-template <int FMT, int GRP, int TN, int WM, int NST>
+template <int FMT, int GRP, int TN, int NST>
 static hipError_t launch_tile(W4Args a, const W4TiledCfg &c, hipStream_t s) {
-    using T = W4Tile<FMT, GRP, TN, WM, NST>;
+    using T = W4Tile<FMT, GRP, TN, NST>;
     // the dynamic LDS limit is a per-device function attribute: set it once per device
     static std::once_flag once[64];
     static hipError_t attr_err[64];
@@ -391,23 +427,15 @@ static hipError_t launch_tile(W4Args a, const W4TiledCfg &c, hipStream_t s) {
 
 template <int FMT, int GRP>
 static hipError_t launch_fmt(const W4Args &a, const W4TiledCfg &c, hipStream_t s) {
-    if (c.wm == 2) return launch_tile<FMT, GRP, 4, 2, 3>(a, c, s);
     switch (c.tn) {
-        case 1: return launch_tile<FMT, GRP, 1, 1, 3>(a, c, s);
-        case 2: return launch_tile<FMT, GRP, 2, 1, 2>(a, c, s);
-        default: return launch_tile<FMT, GRP, 4, 1, 2>(a, c, s);
+        case 1: return launch_tile<FMT, GRP, 1, 3>(a, c, s);
+        case 2: return launch_tile<FMT, GRP, 2, 2>(a, c, s);
+        default: return launch_tile<FMT, GRP, 4, 2>(a, c, s);
     }
 }
 
-hipError_t launch_gemm_w4_tiled(W4Args a, int fmt, int grp, const W4TiledCfg &c, hipStream_t s) {
+hipError_t launch_gemm_w4_tiled(const W4Args &a, int fmt, int grp, const W4TiledCfg &c, hipStream_t s) {
     hipError_t err;
-    if (fmt == W4_INT) {
-        a.g4 = (int)w4_g4(a.K, grp);
-        const int64_t n8 = a.arows * (a.K / 8);
-        hipLaunchKernelGGL(k_w4_sums, dim3((unsigned)((n8 + 255) / 256)), dim3(256), 0, s, (const uint4 *)a.a, n8,
-                           (int)(a.K / 8), grp, (int)(a.K / grp), a.g4, a.sums);
-        if ((err = hipGetLastError()) != hipSuccess) return err;
-    }
     if (fmt == W4_MXFP4) err = launch_fmt<W4_MXFP4, 32>(a, c, s);
     else if (grp == 32) err = launch_fmt<W4_INT, 32>(a, c, s);
     else if (grp == 64) err = launch_fmt<W4_INT, 64>(a, c, s);

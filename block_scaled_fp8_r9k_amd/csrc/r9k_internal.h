@@ -19,7 +19,8 @@ namespace r9k {
 //   R9K_BF16A_GS                    bf16-activation variant: K-groups per wave
 //   R9K_MID                         mid-width kernel: 0 never, 1 wherever it fits (else the planner's choice)
 //   R9K_MID_CFG=mt,wn,wk,d[,ks]     mid-width kernel launch shape and K split (ignored where it does not fit)
-//   R9K_W4_TILED=wm,tn,ks           4-bit weights, tiled kernel: rows / 64, column tiles a wave, K split (wm 0: never)
+//   R9K_W4=nt,wn,wk[,ks]            4-bit weights, streaming kernel: column tiles a wave, waves along columns, K slices, K split
+//   R9K_W4_TILED=on[,tn[,ks]]       4-bit weights, tiled kernel: 0 never, 1 always; column tiles a wave, K split
 //   R9K_MOE_MTR                     MoE expert GEMMs: row tiles of 16 pairs a pass (1 or 2)
 struct Tuning {
     int decode_wn, decode_wk;
@@ -30,8 +31,8 @@ struct Tuning {
     int bf16a_gs;
     int mid;  // -1: not set
     int mid_cfg[5];
-    int w4[4];        // 4-bit weight-streaming kernel: column tiles a wave, waves along columns, K slices, K split (0: the planner's)
-    int w4_tiled[3];  // 4-bit tiled kernel: wm (0: never), tn, ksplit; wm -1: the planner's
+    int w4[4];        // 4-bit weight-streaming kernel (0: the planner's)
+    int w4_tiled[3];  // 4-bit tiled kernel: 0 never, 1 always (-1: the planner's), column tiles a wave, K split
     int moe_mtr;  // MoE row tiles a pass (1 or 2; 0 = by the average pairs an expert gets)
 };
 const Tuning &tuning();
@@ -222,12 +223,11 @@ struct W4Args {
     const int32_t *src;      // expert products: row r reads activation row src[r] / topk; NULL: row r
     int64_t E, topk, arows;
     int silu;                // 1: columns [0, N/2) gate, [N/2, N) up, c = silu(gate) * up
-    float *sums;             // tiled kernel, int4: sums of each activation row's groups (workspace)
-    float *part;             // tiled kernel with a K split: fp32 partials [ksplit][M][N] (workspace)
+    float *part;             // with a K split: fp32 partials [ksplit][M][N] (workspace)
     // set by the launchers
-    int nblk, nrow, ksplit, g4;     // tiled kernel: column blocks, row blocks, K split, groups a row of sums
+    int nblk, nrow, ksplit;         // tiled kernel: column blocks, row blocks, K split
     int wnl, span, seg, cps;        // streaming kernel: log2 of the waves along the columns; chunks a split, a segment, a wave's slice
-    uint32_t bmagic, tmagic;        // ceil(2^20 / (64-piece blocks a row)), ceil(2^32 / topk)
+    uint32_t bmagic, tmagic, zfill; // ceil(2^20 / (64-piece blocks a row)), ceil(2^32 / topk), the zeros where none are given
 };
 struct W4Cfg {
     int mt;      // row tiles of 16 a CTA
@@ -238,13 +238,12 @@ struct W4Cfg {
 };
 W4Cfg w4_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu);
 struct W4TiledCfg {
-    int wm;      // 64-row blocks a CTA: 0 (the weight-streaming kernel takes the shape), 1 or 2
+    bool on;     // false: the weight-streaming kernel takes the shape
     int tn;      // column tiles a wave (4 waves along the columns)
     int ksplit;  // CTAs along K (dense products only)
 };
 W4TiledCfg w4_tiled_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu);
-size_t w4_sums_bytes(int64_t rows, int64_t K, int grp);
-hipError_t launch_gemm_w4_tiled(W4Args a, int fmt, int grp, const W4TiledCfg &c, hipStream_t s);
+hipError_t launch_gemm_w4_tiled(const W4Args &a, int fmt, int grp, const W4TiledCfg &c, hipStream_t s);
 hipError_t launch_gemm_w4(const W4Args &a, int fmt, int grp, const W4Cfg &c, hipStream_t s);
 
 // ---- rows sorted by expert (moe_sort.hip) ----

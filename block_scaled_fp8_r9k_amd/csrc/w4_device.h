@@ -87,36 +87,44 @@ __device__ __forceinline__ int w4_wave_scan(int v) {
 // Row block `item` of the experts' row ranges [offsets[e], offsets[e+1]), RB
 // rows (a power of two) to a block, blocks counted expert by expert: the expert, and
 // its rows from the block's first on; false if there are fewer blocks.  Every wave
-// finds it by itself: each lane counts the blocks of its E / 64 experts, then the
-// chosen lane's experts are spread over the lanes.  Offsets are held to [0, R], so that
-// wrong ones cannot lead out of the rows.
+// finds it by itself, four experts a lane and 256 a round, in one round trip to memory
+// for up to 256 experts.  Offsets are held to [0, R], so that wrong ones cannot lead
+// out of the rows.
 __device__ __forceinline__ bool w4_find_block(const int32_t *offsets, int E, int R, int RB, int item, int &e_out,
                                               int &r0, int &r1) {
     const int lane = threadIdx.x & 63, sh = __builtin_ctz(RB);
-    const int per = (E + 63) >> 6;
-    auto blocks = [&](int e, int &o0) {
-        const int a = e < E ? offsets[e] : 0, b = e < E ? offsets[e + 1] : 0;
-        o0 = min(max(a, 0), R);
-        return (max(min(b, R), o0) - o0 + RB - 1) >> sh;
-    };
-    int o0 = 0, n = 0;
-    for (int i = 0; i < per; ++i) n += blocks(lane * per + i, o0);
-    int incl = w4_wave_scan(n);
-    if (item >= __builtin_amdgcn_readlane(incl, 63)) return false;
-    int l = __builtin_ctzll(__ballot(incl > item));
-    int before = __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(n, l);  // blocks before lane l's
-    int e = l * per;
-    if (per > 1) {  // per <= 64
-        n = lane < per ? blocks(e + lane, o0) : 0;
-        incl = before + w4_wave_scan(n);
-        l = __builtin_ctzll(__ballot(incl > item));
-        before = __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(n, l);
-        e += l;
+    for (int e0 = 0; e0 < E; e0 += 256) {
+        const int e = e0 + 4 * lane;
+        int o[5], nb[4], n = 0;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) o[i] = offsets[min(e + i, E)];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) o[i] = min(max(o[i], 0), R);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            nb[i] = (max(o[i + 1], o[i]) - o[i] + RB - 1) >> sh;  // none past the last expert
+            n += nb[i];
+        }
+        const int incl = w4_wave_scan(n), total = __builtin_amdgcn_readlane(incl, 63);
+        if (item >= total) {
+            item -= total;
+            continue;
+        }
+        const int l = __builtin_ctzll(__ballot(incl > item));
+        item -= __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(n, l);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int b = __builtin_amdgcn_readlane(nb[i], l);
+            if (item < b) {
+                e_out = e0 + 4 * l + i;
+                r0 = __builtin_amdgcn_readlane(o[i], l) + (item << sh);
+                r1 = __builtin_amdgcn_readlane(o[i + 1], l);
+                return true;
+            }
+            item -= b;
+        }
     }
-    e_out = e;
-    r0 = __builtin_amdgcn_readlane(o0, l) + ((item - before) << sh);
-    r1 = min(max(offsets[e + 1], 0), R);
-    return true;
+    return false;
 }
 
 // p / topk for p < 2^31, with magic = ceil(2^32 / topk) (0 for topk = 1): at most one too large

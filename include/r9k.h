@@ -460,23 +460,15 @@ int r9k_gemm_w4(const uint16_t *a, int64_t M, int64_t K, const uint8_t *wp, cons
  *   most R); wp, sp, zp: E weights of N rows packed as one -> c.
  * offsets and src are device data the host cannot check: offsets are held to
  * [0, R], and an index outside a reads row 0.
- * Errors: NULLPTR (a, offsets, wp, sp, c, or a workspace where one is needed); SHAPE if R < 0, arows < 1 (with R > 0), E
+ * Errors: NULLPTR (a, offsets, wp, sp, c); SHAPE if R < 0, arows < 1 (with R > 0), E
  * < 1 or > 2048, topk < 1, K not a positive multiple of 128, N of 16 (of 32 with
  * silu), or without src arows < R; ARG for an unknown format, group or act, or zeros with
- * R9K_W4_MXFP4; ALIGN; WORKSPACE; DEVICE; LAUNCH.  R = 0 launches nothing. */
+ * R9K_W4_MXFP4; ALIGN; DEVICE; LAUNCH.  R = 0 launches nothing. */
 #define R9K_ACT_NONE 0
 #define R9K_ACT_SILU_MUL 1
-
-/* Workspace bytes of r9k_moe_gemm_w4 for these sizes, in any format (host only; 0
- * for many, and then the workspace may be NULL).  Needs no initialisation; calls
- * sharing one must not overlap in time.
- * Errors: NULLPTR (bytes); SHAPE as for the call; ARG for an unknown act. */
-int r9k_moe_gemm_w4_workspace(int64_t arows, int64_t E, int64_t R, int64_t K, int64_t N, int act, size_t *bytes);
-
 int r9k_moe_gemm_w4(const uint16_t *a, int64_t arows, const int32_t *src, int64_t topk, const int32_t *offsets,
                     int64_t E, int64_t R, int64_t K, const uint8_t *wp, const void *sp, const uint8_t *zp,
-                    int format, int group, int64_t N, int act, uint16_t *c, void *workspace,
-                    size_t ws_bytes, void *stream);
+                    int format, int group, int64_t N, int act, uint16_t *c, void *stream);
 
 /* ------------------------------------------------------------------------ */
 /* Rows sorted by expert, and back                                           */
