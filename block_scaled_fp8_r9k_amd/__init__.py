@@ -638,8 +638,9 @@ def moe_permute(x, topk_ids, E: int, xs=None, src=None, pos=None, offsets=None, 
         px = pxs = None
         pi = psrc = ppos = poff
     pw, nb, _keep = _scratch(workspace, moe_permute_workspace(T, E, topk), dev, stream)
-    _check(lib().r9k_moe_permute(px, dt, T, H, pi, topk, E, pxs, psrc, ppos, poff, pw, nb, _raw(stream, dev)),
-           "r9k_moe_permute")
+    rc = lib().r9k_moe_permute(px, dt, T, H, pi, topk, E, pxs, psrc, ppos, poff, pw, nb, _raw(stream, dev))
+    if rc:
+        _check(rc, "r9k_moe_permute")
     return xs, src, pos, offsets
 
 

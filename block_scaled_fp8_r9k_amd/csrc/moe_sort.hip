@@ -100,24 +100,25 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_count(const int32_t *__re
 // of all parts, scans the experts' totals, counts its own part wave by wave
 // (consecutive quarters of it), and ranks a wave's slots 64 at a time.
 __global__ __launch_bounds__(SORT_THREADS) void k_sort_place(const int32_t *__restrict__ ids, int R, int E, int per,
-                                                             int bits, int parts, const int32_t *__restrict__ count,
+                                                             int bits, const int32_t *__restrict__ count,
                                                              int32_t *__restrict__ src, int32_t *__restrict__ pos,
                                                              int32_t *__restrict__ offsets) {
     extern __shared__ int32_t lds_i[];
     int32_t *next = lds_i;                     // [4][E]: the next row of expert e for wave w
     int32_t *scratch = lds_i + 4 * (int64_t)E; // [4], and the running total
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int part = blockIdx.x;
+    const int part = blockIdx.x, parts = gridDim.x;
 
     int run = 0;  // rows of the experts before this step's 256
     for (int e0 = 0; e0 < E; e0 += SORT_THREADS) {
         const int e = e0 + tid;
         int before = 0, all = 0;
         if (e < E) {
+#pragma unroll 16
             for (int b = 0; b < parts; ++b) {
                 const int c = count[(int64_t)b * E + e];
                 all += c;
-                if (b < part) before += c;
+                before += b < part ? c : 0;
             }
         }
         const int incl = block_scan256(all, scratch);
@@ -174,13 +175,79 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_place(const int32_t *__re
     }
 }
 
-// Each token's row to the rows of its slots; one CTA a token.
+// Few slots: sort and rows in one launch.  CTA t counts, for each slot of token t, the
+// slots before it in the order (those of lower experts, and earlier ones of its own),
+// one slot a wave at a time, and copies the token's row; the last CTA adds up the
+// experts' first rows and marks the rows that no slot fills.  R * R comparisons in all.
+__global__ __launch_bounds__(SORT_THREADS) void k_sort_small(const int32_t *__restrict__ ids, int T, int topk, int E,
+                                                             const uint4 *__restrict__ x, int64_t w16,
+                                                             uint4 *__restrict__ xs, int32_t *__restrict__ src,
+                                                             int32_t *__restrict__ pos, int32_t *__restrict__ offsets) {
+    extern __shared__ int32_t lds_i[];  // [max(E, topk)] and 5 for the scan
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int R = T * topk, t = blockIdx.x;
+    if (t == T) {
+        int32_t *scratch = lds_i + max(E, topk);
+        for (int e = tid; e < E; e += SORT_THREADS) lds_i[e] = 0;
+        __syncthreads();
+        for (int p = tid; p < R; p += SORT_THREADS) {
+            const int e = ids[p];
+            if (e >= 0 && e < E) atomicAdd(&lds_i[e], 1);  // whole numbers: the order does not show
+        }
+        __syncthreads();
+        int run = 0;
+        for (int e0 = 0; e0 < E; e0 += SORT_THREADS) {
+            const int e = e0 + tid, n = e < E ? lds_i[e] : 0;
+            const int incl = block_scan256(n, scratch);
+            if (tid == SORT_THREADS - 1) scratch[4] = incl;
+            __syncthreads();
+            if (e < E) offsets[e] = run + incl - n;
+            run += scratch[4];
+            __syncthreads();
+        }
+        if (tid == 0) offsets[E] = run;
+        for (int r = run + tid; r < R; r += SORT_THREADS) src[r] = -1;
+        return;
+    }
+    // the row's pieces are on their way while the slots are counted
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (x && tid < w16) v = x[(int64_t)t * w16 + tid];
+    for (int j = wave; j < topk; j += SORT_THREADS / 64) {
+        const int p = t * topk + j, e = ids[p];
+        int row = -1;
+        if (e >= 0 && e < E) {
+            int n = 0;
+            for (int i = lane; i < R; i += 64) {
+                const int o = ids[i];
+                n += (o >= 0 && o < e) || (o == e && i < p);
+            }
+            row = __builtin_amdgcn_readlane(w4_wave_scan(n), 63);
+        }
+        if (lane == 0) {
+            lds_i[j] = row;
+            pos[p] = row;
+            if (row >= 0) src[row] = p;
+        }
+    }
+    if (!x) return;
+    __syncthreads();
+    for (int64_t i = tid; i < w16; i += SORT_THREADS) {
+        if (i >= SORT_THREADS) v = x[(int64_t)t * w16 + i];
+        for (int j = 0; j < topk; ++j) {
+            const int64_t r = lds_i[j];
+            if (r >= 0) xs[r * w16 + i] = v;
+        }
+    }
+}
+
+// Each token's row to the rows of its slots; 2^lpt threads a token, 256 >> lpt tokens a CTA.
 __global__ __launch_bounds__(SORT_THREADS) void k_permute_rows(const uint4 *__restrict__ x, int64_t w16, int topk,
-                                                               int64_t R, const int32_t *__restrict__ pos,
+                                                               int64_t T, int lpt, const int32_t *__restrict__ pos,
                                                                uint4 *__restrict__ xs) {
-    const int64_t t = blockIdx.x;
+    const int64_t t = ((int64_t)blockIdx.x << (8 - lpt)) + (threadIdx.x >> lpt), R = T * topk;
+    if (t >= T) return;
     const int32_t *pt = pos + t * topk;
-    for (int64_t i = threadIdx.x; i < w16; i += SORT_THREADS) {
+    for (int64_t i = threadIdx.x & ((1 << lpt) - 1); i < w16; i += 1 << lpt) {
         const uint4 v = x[t * w16 + i];
         for (int j = 0; j < topk; ++j) {
             const int64_t r = pt[j];
@@ -189,41 +256,64 @@ __global__ __launch_bounds__(SORT_THREADS) void k_permute_rows(const uint4 *__re
     }
 }
 
-template <bool F32>
+// A token takes 2^lpt threads (as many as its row has 16-byte pieces, up to the CTA),
+// a CTA 256 >> lpt tokens; WIDE: the CTA, so that its positions and weights are scalars.
+// Four rows are asked for at a time.  Dropped slots read row 0 and drop what they read.
+template <bool F32, bool WIDE>
 __global__ __launch_bounds__(SORT_THREADS) void k_unpermute(const uint4 *__restrict__ y, int64_t w16, int topk,
-                                                            int64_t R, const int32_t *__restrict__ pos,
+                                                            int64_t T, int lpt, const int32_t *__restrict__ pos,
                                                             const float *__restrict__ w, uint4 *__restrict__ out) {
-    const int64_t t = blockIdx.x;
-    const int64_t i = (int64_t)blockIdx.y * SORT_THREADS + threadIdx.x;
-    if (i >= w16) return;
+    constexpr int B = 4, N = Row16<F32>::N;
+    const int64_t t = WIDE ? (int64_t)blockIdx.x : ((int64_t)blockIdx.x << (8 - lpt)) + (threadIdx.x >> lpt), R = T * topk;
+    const int64_t i = WIDE ? (int64_t)blockIdx.y * SORT_THREADS + threadIdx.x
+                           : ((int64_t)blockIdx.y << lpt) + (threadIdx.x & ((1 << lpt) - 1));
+    if (t >= T || i >= w16) return;
     Row16<F32> acc;
 #pragma unroll
-    for (int k = 0; k < Row16<F32>::N; ++k) acc.v[k] = 0.0f;
-    for (int j = 0; j < topk; ++j) {
-        const int64_t r = pos[t * topk + j];
-        if (r < 0 || r >= R) continue;
-        const float g = w ? w[t * topk + j] : 1.0f;
-        const Row16<F32> v = row_unpack<F32>(y[r * w16 + i]);
+    for (int k = 0; k < N; ++k) acc.v[k] = 0.0f;
+    for (int j0 = 0; j0 < topk; j0 += B) {
+        uint4 v[B] = {};
+        float g[B] = {};
+        bool live[B];
 #pragma unroll
-        for (int k = 0; k < Row16<F32>::N; ++k) acc.v[k] = __builtin_fmaf(g, v.v[k], acc.v[k]);
+        for (int b = 0; b < B; ++b) {
+            live[b] = false;
+            if (j0 + b < topk) {
+                const int64_t r = pos[t * topk + j0 + b];
+                live[b] = r >= 0 && r < R;
+                g[b] = w ? w[t * topk + j0 + b] : 1.0f;
+                v[b] = y[(live[b] ? r : 0) * w16 + i];
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (j0 + b >= topk) continue;
+            const Row16<F32> x = row_unpack<F32>(v[b]);
+#pragma unroll
+            for (int k = 0; k < N; ++k) acc.v[k] = live[b] ? __builtin_fmaf(g[b], x.v[k], acc.v[k]) : acc.v[k];
+        }
     }
     out[t * w16 + i] = row_pack<F32>(acc);
 }
 
-template <bool F32>
+// Rows of up to 64 pieces (WIDE false): 2^lpt <= 64 threads a token, whose sums stay in
+// the wave.  Longer ones: a CTA a token, sums through LDS.
+template <bool F32, bool WIDE>
 __global__ __launch_bounds__(SORT_THREADS) void k_unpermute_bwd(const uint4 *__restrict__ g, const uint4 *__restrict__ y,
-                                                                int64_t w16, int topk, int64_t R,
+                                                                int64_t w16, int topk, int64_t T, int lpt,
                                                                 const int32_t *__restrict__ pos,
                                                                 const float *__restrict__ w, uint4 *__restrict__ gy,
                                                                 float *__restrict__ gw) {
     __shared__ float part[4];
-    const int64_t t = blockIdx.x;
+    const int per = WIDE ? SORT_THREADS : 1 << lpt, me = WIDE ? threadIdx.x : threadIdx.x & (per - 1);
+    const int64_t t = WIDE ? (int64_t)blockIdx.x : ((int64_t)blockIdx.x << (8 - lpt)) + (threadIdx.x >> lpt), R = T * topk;
+    if (!WIDE && t >= T) return;  // a token's threads leave together
     for (int j = 0; j < topk; ++j) {
         const int64_t r = pos[t * topk + j];
         float dot = 0.0f;
         if (r >= 0 && r < R) {
             const float s = w[t * topk + j];
-            for (int64_t i = threadIdx.x; i < w16; i += SORT_THREADS) {
+            for (int64_t i = me; i < w16; i += per) {
                 const Row16<F32> a = row_unpack<F32>(g[t * w16 + i]), b = row_unpack<F32>(y[r * w16 + i]);
                 Row16<F32> o;
 #pragma unroll
@@ -234,51 +324,74 @@ __global__ __launch_bounds__(SORT_THREADS) void k_unpermute_bwd(const uint4 *__r
                 gy[r * w16 + i] = row_pack<F32>(o);
             }
         }
+        if (WIDE) {
 #pragma unroll
-        for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d, 64);
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
-        __syncthreads();
-        if (threadIdx.x == 0) gw[t * topk + j] = (part[0] + part[1]) + (part[2] + part[3]);
+            for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d, 64);
+            __syncthreads();
+            if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+            __syncthreads();
+            if (threadIdx.x == 0) gw[t * topk + j] = (part[0] + part[1]) + (part[2] + part[3]);
+        } else {
+            for (int d = per >> 1; d; d >>= 1) dot += __shfl_xor(dot, d, 64);
+            if (me == 0) gw[t * topk + j] = dot;
+        }
     }
+}
+
+// log2 of the threads a token's row takes: as many as it has 16-byte pieces, 4 to 256
+static int row_lpt(int64_t w16) {
+    int l = 2;
+    while (l < 8 && (int64_t(1) << l) < w16) ++l;
+    return l;
 }
 
 // Slots a part holds: a multiple of 256, parts few enough that adding up their
 // counts stays short.
 static int sort_part(int64_t R) { return (int)std::max<int64_t>(1024, ((R + 255) / 256 + 255) / 256 * 256); }
 
+// Slots up to which one launch sorts them by comparing all pairs (4096: 2 us of
+// comparisons over the chip; the three launches of the general path cost more).
+constexpr int64_t SORT_SMALL = 4096;
+
 size_t moe_sort_workspace(int64_t R, int64_t E) {
+    if (R <= SORT_SMALL) return 0;
     const int64_t per = sort_part(R);
     return align_up((size_t)((R + per - 1) / per) * (size_t)E * 4, 256);
 }
 
 hipError_t launch_moe_permute(const SortArgs &a, hipStream_t s) {
     const int64_t R = a.T * a.topk;
+    if (R <= SORT_SMALL) {
+        hipLaunchKernelGGL(k_sort_small, dim3((unsigned)a.T + 1), dim3(SORT_THREADS),
+                           (size_t)std::max(a.E, a.topk) * 4 + 32, s, a.ids, (int)a.T, (int)a.topk, (int)a.E,
+                           (const uint4 *)a.x, a.row_bytes / 16, (uint4 *)a.xs, a.src, a.pos, a.offsets);
+        return hipGetLastError();
+    }
     const int per = sort_part(R);
     const unsigned parts = (unsigned)((R + per - 1) / per);
+    const int lpt = row_lpt(a.row_bytes / 16), tpc = 256 >> lpt;
     int bits = 1;
     while ((1 << bits) < a.E + 1) ++bits;
-    if (R)
-        hipLaunchKernelGGL(k_sort_count, dim3(parts), dim3(SORT_THREADS), (size_t)a.E * 4, s, a.ids, (int)R, (int)a.E,
-                           per, a.count);
-    hipLaunchKernelGGL(k_sort_place, dim3(std::max(parts, 1u)), dim3(SORT_THREADS), (size_t)a.E * 16 + 32, s, a.ids, (int)R,
-                       (int)a.E, per, bits, (int)parts, a.count, a.src, a.pos, a.offsets);
-    if (a.x && R)
-        hipLaunchKernelGGL(k_permute_rows, dim3((unsigned)a.T), dim3(SORT_THREADS), 0, s, (const uint4 *)a.x,
-                           a.row_bytes / 16, (int)a.topk, R, a.pos, (uint4 *)a.xs);
+    hipLaunchKernelGGL(k_sort_count, dim3(parts), dim3(SORT_THREADS), (size_t)a.E * 4, s, a.ids, (int)R, (int)a.E, per,
+                       a.count);
+    hipLaunchKernelGGL(k_sort_place, dim3(parts), dim3(SORT_THREADS), (size_t)a.E * 16 + 32, s, a.ids, (int)R,
+                       (int)a.E, per, bits, a.count, a.src, a.pos, a.offsets);
+    if (a.x)
+        hipLaunchKernelGGL(k_permute_rows, dim3((unsigned)((a.T + tpc - 1) / tpc)), dim3(SORT_THREADS), 0, s,
+                           (const uint4 *)a.x, a.row_bytes / 16, (int)a.topk, a.T, lpt, a.pos, (uint4 *)a.xs);
     return hipGetLastError();
 }
 
 hipError_t launch_moe_unpermute(const void *y, bool f32, int64_t row_bytes, int64_t T, int64_t topk,
                                 const int32_t *pos, const float *w, void *out, hipStream_t s) {
     const int64_t w16 = row_bytes / 16;
-    const dim3 grid((unsigned)T, (unsigned)((w16 + SORT_THREADS - 1) / SORT_THREADS));
-    if (f32)
-        hipLaunchKernelGGL(k_unpermute<true>, grid, dim3(SORT_THREADS), 0, s, (const uint4 *)y, w16, (int)topk, T * topk,
-                           pos, w, (uint4 *)out);
-    else
-        hipLaunchKernelGGL(k_unpermute<false>, grid, dim3(SORT_THREADS), 0, s, (const uint4 *)y, w16, (int)topk,
-                           T * topk, pos, w, (uint4 *)out);
+    const int lpt = row_lpt(w16), tpc = 256 >> lpt;
+    const dim3 grid((unsigned)((T + tpc - 1) / tpc), (unsigned)((w16 + (1 << lpt) - 1) >> lpt));
+    const bool wide = lpt == 8;
+    auto kernel = f32 ? (wide ? k_unpermute<true, true> : k_unpermute<true, false>)
+                      : (wide ? k_unpermute<false, true> : k_unpermute<false, false>);
+    hipLaunchKernelGGL(kernel, grid, dim3(SORT_THREADS), 0, s, (const uint4 *)y, w16, (int)topk, T, lpt, pos, w,
+                       (uint4 *)out);
     return hipGetLastError();
 }
 
@@ -286,12 +399,12 @@ hipError_t launch_moe_unpermute_backward(const void *g, const void *y, bool f32,
                                          int64_t topk, const int32_t *pos, const float *w, void *gy, float *gw,
                                          hipStream_t s) {
     const int64_t w16 = row_bytes / 16;
-    if (f32)
-        hipLaunchKernelGGL(k_unpermute_bwd<true>, dim3((unsigned)T), dim3(SORT_THREADS), 0, s, (const uint4 *)g,
-                           (const uint4 *)y, w16, (int)topk, T * topk, pos, w, (uint4 *)gy, gw);
-    else
-        hipLaunchKernelGGL(k_unpermute_bwd<false>, dim3((unsigned)T), dim3(SORT_THREADS), 0, s, (const uint4 *)g,
-                           (const uint4 *)y, w16, (int)topk, T * topk, pos, w, (uint4 *)gy, gw);
+    const bool wide = w16 > 64;
+    const int lpt = row_lpt(w16), tpc = wide ? 1 : 256 >> lpt;
+    auto kernel = f32 ? (wide ? k_unpermute_bwd<true, true> : k_unpermute_bwd<true, false>)
+                      : (wide ? k_unpermute_bwd<false, true> : k_unpermute_bwd<false, false>);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((T + tpc - 1) / tpc)), dim3(SORT_THREADS), 0, s, (const uint4 *)g,
+                       (const uint4 *)y, w16, (int)topk, T, lpt, pos, w, (uint4 *)gy, gw);
     return hipGetLastError();
 }
 

@@ -133,7 +133,7 @@ def test_permute_checks(L):
     f = L.r9k_moe_permute
     F = c_void_p(6 << 32)
     G = c_void_p(7 << 32)
-    ok = [A, 0, 4, 64, B, 2, 8, C, D, E16, F, G, 1 << 30, S]
+    ok = [A, 0, 4096, 64, B, 2, 8, C, D, E16, F, G, 1 << 30, S]  # slots enough to need a workspace
 
     def with_(**kw):
         x = list(ok)
