@@ -473,10 +473,11 @@ def _raw(stream, dev: int) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _new(shape, dtype, dev: int, stream) -> torch.Tensor:
-    """A fresh tensor for a call on `stream`, owned by that stream in torch's allocator."""
+def _new(shape, dtype, dev: int, stream, like: torch.Tensor | None = None) -> torch.Tensor:
+    """A fresh tensor for a call on `stream`, owned by that stream in torch's allocator.  `like`: a tensor of that
+    type and device, from which torch makes one in less time."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev) if like is None else like.new_empty(shape)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
     with torch.cuda.stream(stream):
@@ -486,9 +487,9 @@ def _new(shape, dtype, dev: int, stream) -> torch.Tensor:
 def _scratch(ws: torch.Tensor | None, nbytes: int, dev: int, stream):
     """(address, bytes, tensor) of a call's workspace: the caller's, or a fresh one, which torch keeps for
     this stream (or the graph being captured) until the call's work is done."""
+    if nbytes == 0:
+        return None, 0, None
     if ws is None:
-        if nbytes == 0:
-            return None, 0, None
         ws = _new((nbytes,), torch.uint8, dev, stream)
     return _addr(ws, U8, "workspace", dev) or None, ws.numel(), ws
 
@@ -552,6 +553,27 @@ def gemm_w4_workspace(M: int, K: int, N: int) -> int:
 def gemm_w4(a, wp, sp, zp=None, c=None, workspace=None, stream=None) -> torch.Tensor:
     """Product with a packed 4-bit weight (r9k_gemm_w4): a [M,K] bf16, (wp, sp, zp) from pack_weight_w4 -> C [M,N]
     bf16.  The format and the group follow from sp's type and shape."""
+    # The checks of a well-formed call with its output and workspace given, in one
+    # expression (a decode call's host time counts: 1.2 us less than one by one); any
+    # other call goes through the checks that name what is wrong.
+    dev = _cur_device() if a.is_cuda else -1
+    if c is not None and a.dtype in BF16 and c.dtype in BF16 and wp.dtype in U8 and len(a.shape) == len(sp.shape) == 2:
+        M, K = a.shape
+        N, groups = sp.shape
+        if (wp.shape == (N, K // 2) and c.shape == (M, N) and M and groups and K % (2 * groups) == 0
+                and sp.dtype in _W4_SCALES and a.is_contiguous() and wp.is_contiguous() and sp.is_contiguous()
+                and c.is_contiguous()
+                and a.get_device() == wp.get_device() == sp.get_device() == c.get_device() == dev
+                and (zp is None or (zp.dtype in U8 and zp.shape == (N, groups) and zp.is_contiguous()
+                                    and zp.get_device() == dev))):
+            need = gemm_w4_workspace(M, K, N)
+            pw, nb, _keep = (None, 0, None) if need == 0 else _scratch(workspace, need, dev, stream)
+            rc = lib().r9k_gemm_w4(a.data_ptr(), M, K, wp.data_ptr(), sp.data_ptr(),
+                                   None if zp is None else zp.data_ptr(), _W4_SCALES[sp.dtype], K // groups, N,
+                                   c.data_ptr(), pw, nb, _raw(stream, dev))
+            if rc:
+                _check(rc, "r9k_gemm_w4")
+            return c
     dev = _dev(a, "a")
     w, s, z, fmt, K, group = _w4_format(wp, sp, zp, dev, 2)
     M, N = a.shape[0], wp.shape[0]
@@ -562,9 +584,7 @@ def gemm_w4(a, wp, sp, zp=None, c=None, workspace=None, stream=None) -> torch.Te
     if M == 0:  # an empty batch: nothing to compute (an empty tensor has no device address to pass)
         return c
     pw, nb, _keep = _scratch(workspace, gemm_w4_workspace(M, K, N), dev, stream)
-    rc = lib().r9k_gemm_w4(pa, M, K, w, s, z, fmt, group, N, pc, pw, nb, _raw(stream, dev))
-    if rc:
-        _check(rc, "r9k_gemm_w4")
+    _check(lib().r9k_gemm_w4(pa, M, K, w, s, z, fmt, group, N, pc, pw, nb, _raw(stream, dev)), "r9k_gemm_w4")
     return c
 
 
@@ -592,8 +612,10 @@ def moe_gemm_w4(x, offsets, wp, sp, zp=None, src=None, topk: int = 1, act: str =
     pc = _addr(c, BF16, "c", dev, out)
     if R == 0:
         return c
-    _check(lib().r9k_moe_gemm_w4(px, rows, ps, topk, po, E, R, K, w, s, z, fmt, group, N, _ACTS[act], pc,
-                                 _raw(stream, dev)), "r9k_moe_gemm_w4")
+    rc = lib().r9k_moe_gemm_w4(px, rows, ps, topk, po, E, R, K, w, s, z, fmt, group, N, _ACTS[act], pc,
+                               _raw(stream, dev))
+    if rc:
+        _check(rc, "r9k_moe_gemm_w4")
     return c
 
 
@@ -627,13 +649,20 @@ def moe_permute(x, topk_ids, E: int, xs=None, src=None, pos=None, offsets=None, 
     elif xs is not None:
         raise ValueError("xs without x")
     if src is None:
-        src = _new((R,), torch.int32, dev, stream)
+        src = _new(R, torch.int32, dev, stream, topk_ids)
+        psrc = src.data_ptr()
+    else:
+        psrc = _addr(src, I32, "src", dev, (R,))
     if pos is None:
-        pos = _new((T, topk), torch.int32, dev, stream)
+        pos = _new((T, topk), torch.int32, dev, stream, topk_ids)
+        ppos = pos.data_ptr()
+    else:
+        ppos = _addr(pos, I32, "pos", dev, (T, topk))
     if offsets is None:
-        offsets = _new((E + 1,), torch.int32, dev, stream)
-    psrc, ppos = _addr(src, I32, "src", dev, (R,)), _addr(pos, I32, "pos", dev, (T, topk))
-    poff = _addr(offsets, I32, "offsets", dev, (E + 1,))
+        offsets = _new(E + 1, torch.int32, dev, stream, topk_ids)
+        poff = offsets.data_ptr()
+    else:
+        poff = _addr(offsets, I32, "offsets", dev, (E + 1,))
     if T == 0:  # no slots (empty tensors have no device address to pass): the call sees only the offsets
         px = pxs = None
         pi = psrc = ppos = poff
@@ -648,21 +677,29 @@ def _sorted_rows(y, pos, dev: int, name: str):
     T, topk = pos.shape
     ppos = _addr(pos, I32, "pos", dev)
     py = _addr(y, _ROWS, name, dev)
-    if y.dim() != 2 or y.shape[0] != T * topk:
-        raise ValueError(f"{name}: shape {tuple(y.shape)} does not go with {T} x {topk} slots")
-    return T, topk, y.shape[1], ppos, py
+    ys = y.shape
+    if len(ys) != 2 or ys[0] != T * topk:
+        raise ValueError(f"{name}: shape {tuple(ys)} does not go with {T} x {topk} slots")
+    return T, topk, ys[1], ppos, py
+
+
+def _out(t, shape, like, name: str, dev: int, stream):
+    """(tensor, address) of an output of `like`'s type: the caller's, checked, or a fresh one."""
+    if t is None:
+        t = _new(shape, like.dtype, dev, stream, like)
+        return t, t.data_ptr()
+    return t, _addr(t, (like.dtype,), name, dev, shape)
 
 
 def moe_permute_backward(gxs, pos, gx=None, stream=None) -> torch.Tensor:
     """Gradient of moe_permute: gxs [T*topk,H], pos [T,topk] -> gx [T,H], the sum over a token's kept slots."""
     dev = _dev(gxs, "gxs")
     T, topk, H, ppos, pg = _sorted_rows(gxs, pos, dev, "gxs")
-    if gx is None:
-        gx = _new((T, H), gxs.dtype, dev, stream)
-    po = _addr(gx, (gxs.dtype,), "gx", dev, (T, H))
+    gx, po = _out(gx, (T, H), gxs, "gx", dev, stream)
     if T:
-        _check(lib().r9k_moe_permute_backward(pg, _ROWS[gxs.dtype], T, H, ppos, topk, po, _raw(stream, dev)),
-               "r9k_moe_permute_backward")
+        rc = lib().r9k_moe_permute_backward(pg, _ROWS[gxs.dtype], T, H, ppos, topk, po, _raw(stream, dev))
+        if rc:
+            _check(rc, "r9k_moe_permute_backward")
     return gx
 
 
@@ -672,12 +709,11 @@ def moe_unpermute(y, pos, w=None, out=None, stream=None) -> torch.Tensor:
     dev = _dev(y, "y")
     T, topk, H, ppos, py = _sorted_rows(y, pos, dev, "y")
     pw = None if w is None else _addr(w, F32, "w", dev, (T, topk))
-    if out is None:
-        out = _new((T, H), y.dtype, dev, stream)
-    po = _addr(out, (y.dtype,), "out", dev, (T, H))
+    out, po = _out(out, (T, H), y, "out", dev, stream)
     if T:
-        _check(lib().r9k_moe_unpermute(py, _ROWS[y.dtype], T, H, ppos, pw, topk, po, _raw(stream, dev)),
-               "r9k_moe_unpermute")
+        rc = lib().r9k_moe_unpermute(py, _ROWS[y.dtype], T, H, ppos, pw, topk, po, _raw(stream, dev))
+        if rc:
+            _check(rc, "r9k_moe_unpermute")
     return out
 
 
@@ -688,12 +724,11 @@ def moe_unpermute_backward(gout, y, pos, w, gy=None, gw=None, stream=None):
     T, topk, H, ppos, py = _sorted_rows(y, pos, dev, "y")
     pg = _addr(gout, (y.dtype,), "gout", dev, (T, H))
     pw = _addr(w, F32, "w", dev, (T, topk))
-    if gy is None:
-        gy = _new(y.shape, y.dtype, dev, stream)
-    if gw is None:
-        gw = _new((T, topk), torch.float32, dev, stream)
-    pgy, pgw = _addr(gy, (y.dtype,), "gy", dev, y.shape), _addr(gw, F32, "gw", dev, (T, topk))
+    gy, pgy = _out(gy, y.shape, y, "gy", dev, stream)
+    gw, pgw = _out(gw, (T, topk), w, "gw", dev, stream)
     if T:
-        _check(lib().r9k_moe_unpermute_backward(pg, py, _ROWS[y.dtype], T, H, ppos, pw, topk, pgy, pgw,
-                                                _raw(stream, dev)), "r9k_moe_unpermute_backward")
+        rc = lib().r9k_moe_unpermute_backward(pg, py, _ROWS[y.dtype], T, H, ppos, pw, topk, pgy, pgw,
+                                              _raw(stream, dev))
+        if rc:
+            _check(rc, "r9k_moe_unpermute_backward")
     return gy, gw

@@ -652,7 +652,7 @@ struct W4Plan {
     W4Cfg cfg;
     size_t bytes;
 };
-static W4Plan w4_plan(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
+static W4Plan w4_plan_new(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
     W4Plan w{w4_tiled_config(M, K, N, E, silu), {}, 0};
     if (!w.tiled.on) w.cfg = w4_config(M, K, N, E, silu);
     const int split = w.tiled.on ? w.tiled.ksplit : w.cfg.ksplit;
@@ -660,8 +660,27 @@ static W4Plan w4_plan(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
     return w;
 }
 
+// The plan of a shape, kept for each thread's last shapes: planning takes about a
+// microsecond, a third of a launch.
+static const W4Plan &w4_plan(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
+    struct Entry {
+        int64_t M = -1, K, N, E;
+        bool silu;
+        W4Plan plan;
+    };
+    static thread_local Entry table[64];
+    const uint64_t h = ((uint64_t)M * 0x9E3779B97F4A7C15u) ^ ((uint64_t)K * 0xC2B2AE3D27D4EB4Fu) ^
+                       ((uint64_t)N * 0x165667B19E3779F9u) ^ ((uint64_t)(2 * E + silu) * 0x27D4EB2F165667C5u);
+    Entry &t = table[h >> 58];
+    if (t.M != M || t.K != K || t.N != N || t.E != E || t.silu != silu) {
+        t.plan = w4_plan_new(M, K, N, E, silu);
+        t.M = M, t.K = K, t.N = N, t.E = E, t.silu = silu;
+    }
+    return t.plan;
+}
+
 static int run_w4(W4Args &a, int format, int group, void *workspace, size_t ws_bytes, hipStream_t s) {
-    const W4Plan w = w4_plan(a.M, a.K, a.N, a.offsets ? a.E : 0, a.silu != 0);
+    const W4Plan &w = w4_plan(a.M, a.K, a.N, a.offsets ? a.E : 0, a.silu != 0);
     if (w.bytes && !workspace) return R9K_ERR_NULLPTR;
     if (ws_bytes < w.bytes) return R9K_ERR_WORKSPACE;
     if (int rc = check_device()) return rc;
