@@ -47,6 +47,10 @@ struct W4Tile {
     static_assert((NST - 2) * LOADS < 64, "vmcnt");
 };
 
+template <int S>
+struct Stage {
+    static constexpr int value = S;
+};
 __device__ __forceinline__ uint32_t hi16(float lo, float hi) {  // upper halves of two fp32
     return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
 }
@@ -116,15 +120,21 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
 
     // this wave's share of a stage's loads: a quarter of the rows, its own column
     // tiles with their scales and zeros (without zero points the scales again, unread)
-    const uint8_t *ap[4], *wp[TN], *sp[T::SLOADS], *zp[T::ZLOADS + 1];
+    // (scalar bases with 32-bit lane offsets, so that going on to the next chunk costs no
+    // vector instruction; activations of 4 GiB and more take 64-bit lane addresses)
+    const uint8_t *abase, *wbase[TN], *sp[T::SLOADS], *zp[T::ZLOADS + 1];
+    uint32_t aoffs[4];  // or the row, where the activations are wide
+    const bool wide = p.src && (uint64_t)p.arows * (uint64_t)p.K >= (uint64_t(1) << 31);
+    abase = (const uint8_t *)p.a + cb * 256 + (p.src ? 0 : (int64_t)r0 * p.K * 2);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const int row = 4 * (4 * wave + u) + q;  // 4 rows of 16 pieces an instruction
-        ap[u] = (const uint8_t *)p.a + source_row(r0 + row) * p.K * 2 + cb * 256 + 16 * (l16 ^ (row & 15));
+        const uint32_t from = (uint32_t)source_row(r0 + row) - (p.src ? 0 : (uint32_t)r0);
+        aoffs[u] = wide ? from : from * (uint32_t)(2 * p.K) + 16 * (l16 ^ (row & 15));
     }
 #pragma unroll
-    for (int u = 0; u < TN; ++u)
-        wp[u] = p.wp + (((int64_t)e * tiles + col_tile(wave, u)) * C + cb) * 1024 + 16 * lane;
+    for (int u = 0; u < TN; ++u) wbase[u] = p.wp + (((int64_t)e * tiles + col_tile(wave, u)) * C + cb) * 1024;
+    const uint32_t wlane = 16 * lane;
     constexpr int SPT = 4 * T::SDW / TN, ZPT = 4 * T::ZDW / TN;  // bytes a tile's chunk
 #pragma unroll
     for (int u = 0; u < T::SLOADS; ++u) {
@@ -145,14 +155,20 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
         const uint32_t base = lds0 + st * T::STAGE;
 #pragma unroll
         for (int u = 0; u < TN; ++u) {
-            load_lds16(wp[u], base + T::ABYTES + (TN * wave + u) * 1024);
-            wp[u] += 1024;
+            load_lds16(wbase[u], wlane, base + T::ABYTES + (TN * wave + u) * 1024);
+            wbase[u] += 1024;
         }
+        if (!wide) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            load_lds16(ap[u], base + (4 * wave + u) * 1024);
-            ap[u] += 256;
+            for (int u = 0; u < 4; ++u) load_lds16(abase, aoffs[u], base + (4 * wave + u) * 1024);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int row = 4 * (4 * wave + u) + q;
+                load_lds16(abase + (uint64_t)aoffs[u] * (uint64_t)(2 * p.K) + 16 * (l16 ^ (row & 15)), base + (4 * wave + u) * 1024);
+            }
         }
+        abase += 256;
 #pragma unroll
         for (int u = 0; u < T::SLOADS; ++u) {
             load_lds4(sp[u], base + soff + u * 256);
@@ -204,16 +220,15 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
 #pragma unroll
     for (int k = 0; k < NST - 1; ++k)
         if (cb + k < ce) issue(k);
-    int st = 0;
-    for (int c = cb; c < ce; ++c) {
+    auto chunk = [&](int c, auto stage) {
+        constexpr int st = decltype(stage)::value;
         // this chunk's stage has landed: the wave's loads issued after it are those of the NST - 2 chunks behind it
         // (fewer at the end: then wait for all)
         if (c + NST - 2 < ce) wait_vm<(NST - 2) * T::LOADS>();
         else wait_vm<0>();
         __syncthreads();
-        if (c + NST - 1 < ce) issue(st == 0 ? NST - 1 : st - 1);
+        if (c + NST - 1 < ce) issue((st + NST - 1) % NST);
         const uint8_t *sb = lds + st * T::STAGE;
-        st = st + 1 == NST ? 0 : st + 1;
 
         if constexpr (FMT == W4_MXFP4) {
             uint4 code[TN];
@@ -257,7 +272,8 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
                 code[j] = *(const uint4 *)(sb + woff + 1024 * j);
                 const int at = ((l16 >> 2) * NG + q % NG) * 4 + (l16 & 3);
                 const float s = __uint_as_float((uint32_t)*(const uint16_t *)(sb + soff + SPT * j + 2 * at) << 16);
-                const float z = p.zp ? (float)*(sb + zoff + ZPT * j + at) : 8.0f;
+                const uint32_t zb = *(sb + zoff + ZPT * j + at);  // (a scale's byte where there are no zeros)
+                const float z = (float)(p.zp ? zb : 8u);
                 if (q / NG == cis) sz[j] = -s * z;
             }
 #pragma unroll
@@ -293,12 +309,24 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
 #pragma unroll
                         for (int r = 0; r < 4; ++r) acc[j][m][r] = __builtin_fmaf(s[j][r], pr[j][r], acc[j][m][r]);
                 }
+                // the sums are formed here, not moved past the next branch with their products held
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) pin_acc(acc[j][m]);
             }
             if (++cis == CPS) {
                 cis = 0;
                 half ^= 1;
             }
         }
+    };
+    // the stages in turn, each with its own code: LDS addresses are then constants
+    for (int c = cb; c < ce; c += NST) {
+        chunk(c, Stage<0>{});
+        if (c + 1 < ce) chunk(c + 1, Stage<1>{});
+        if constexpr (NST == 3)
+            if (c + 2 < ce) chunk(c + 2, Stage<2>{});
     }
     if constexpr (FMT == W4_INT) {
         __syncthreads();  // the last step's sums; it may hold fewer than four groups
@@ -349,10 +377,10 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
     }
     __syncthreads();
     const int64_t ldc = p.silu ? p.N / 2 : p.N;
-    const int ppr = cols / 8;  // 16-byte pieces a row
+    const int pl = __builtin_ctz(cols / 8);  // log2 of the 16-byte pieces a row
     const int64_t n0 = (int64_t)bx * cols;
-    for (int id = tid; id < rows * ppr; id += T::THREADS) {
-        const int r = id / ppr, cc = id % ppr;
+    for (int id = tid; id < rows << pl; id += T::THREADS) {
+        const int r = id >> pl, cc = id & ((1 << pl) - 1);
         if (n0 + 8 * cc < ldc)
             *(uint4 *)(p.c + (int64_t)(r0 + r) * ldc + n0 + 8 * cc) = *(const uint4 *)(lds + r * T::CPITCH + 16 * cc);
     }
