@@ -205,3 +205,51 @@ def test_refusals(r9k):
     with pytest.raises(r9k.R9kError) as e:
         r9k.moe_unpermute_backward(x, ys, pos, w, gy=ys)
     assert e.value.code == -7
+
+
+def test_rows_past_4_gib(r9k):
+    """Sorted rows of 4.4 GiB: every row is its token's, and the way back gives each token topk times itself."""
+    T, k, E, H = 36000, 8, 64, 8192
+    ids = torch.from_numpy(_ids(T, k, E, "rand", 1)).cuda()
+    x = torch.randn((T, H), device="cuda").to(torch.bfloat16)
+    xs, src, pos, off = r9k.moe_permute(x, ids, E)
+    for lo in range(0, T * k, 40000):
+        hi = min(T * k, lo + 40000)
+        assert torch.equal(xs[lo:hi], x[src[lo:hi].long() // k])
+    assert torch.equal(r9k.moe_permute_backward(xs, pos), x * 8)      # a power of two: exact
+    gy, gw = r9k.moe_unpermute_backward(x, xs, pos, torch.full((T, k), 0.5, device="cuda"))
+    for lo in range(0, T * k, 40000):
+        hi = min(T * k, lo + 40000)
+        assert torch.equal(gy[lo:hi], xs[lo:hi] * 0.5)
+
+
+def test_graphs_and_streams(r9k):
+    """Two sorts of different sizes captured and replayed in turn with eager work between, and a side stream."""
+    cases = []
+    for T, k, E, H in ((40, 4, 16, 256), (3000, 6, 50, 512)):
+        ids = torch.from_numpy(_ids(T, k, E, "drop", T)).cuda()
+        x, w = _rows(T, H, torch.bfloat16, T).cuda(), torch.rand((T, k), device="cuda")
+
+        def step(x=x, ids=ids, w=w, E=E, xs=torch.zeros((T * k, H), dtype=torch.bfloat16, device="cuda"),
+                 gy=torch.zeros((T * k, H), dtype=torch.bfloat16, device="cuda"), **kw):
+            _, src, pos, off = r9k.moe_permute(x, ids, E, xs=xs, **kw)
+            out = r9k.moe_unpermute(xs, pos, w, **kw)
+            return [src, pos, off, out, *r9k.moe_unpermute_backward(x, xs, pos, w, gy=gy, **kw)]
+        want = [t.clone() for t in step()]
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got = step(stream=side)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs = step()
+        cases.append((g, outs, want, step))
+    for _ in range(4):
+        for g, outs, want, step in cases:
+            for t in outs:
+                t.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
+            assert all(torch.equal(a, b) for a, b in zip(step(), want))

@@ -375,3 +375,80 @@ def test_moe_layer(r9k, T, H, E, I, k, fmt, group, zeros):
         again = layer()[-1]
         torch.cuda.synchronize()
         assert torch.equal(got[-1], out) and torch.equal(again, out)
+
+
+# ------------------------------------------------------------ far and wide ----
+
+@pytest.mark.parametrize("seed", range(24))
+def test_drawn_products(r9k, seed):
+    """Shapes drawn over the whole range, the sizes' logarithms uniform; every format in turn."""
+    g = np.random.default_rng(900 + seed)
+    draw = lambda lo, hi, step: max(lo, int(round(np.exp(g.uniform(np.log(lo), np.log(hi))) / step)) * step)
+    fmt, group, zeros = FORMATS[seed % len(FORMATS)]
+    M, K, N = draw(1, 500, 1), draw(128, 9000, 128), draw(16, 3000, 16)
+    say("drawn", M, K, N, fmt, group, zeros)
+    w = weight((N,), K, fmt, group, zeros, seed)
+    check(r9k, acts(M, K, seed), w, group, packed(r9k, w), f"{fmt} g{group} {M}x{K}x{N}")
+
+
+@pytest.mark.parametrize("fmt,group,zeros", [("int4", 128, True), ("mxfp4", 32, False)])
+@pytest.mark.parametrize("T,k,E,K,N", [(300, 2, 600, 128, 32), (20, 64, 2048, 128, 64), (2000, 4, 300, 256, 64),
+                                       (3000, 10, 2048, 128, 32), (4000, 1, 1, 256, 96), (6, 3, 5, 8192, 32),
+                                       (60, 2, 3, 8192, 32), (5, 1, 2, 24576, 16 * 3 * 2)])
+def test_many_experts_and_long_rows(r9k, fmt, group, zeros, T, k, E, K, N):
+    say("experts", T, k, E, K, N, fmt)
+    ids = _routing(T, min(k, E), E, "rand", T + 1)
+    k = ids.shape[1]
+    src, pos, off = ref.sort(ids, E)
+    w = weight((E, N), K, fmt, group, zeros, T)
+    x = acts(T, K, T)
+    c = r9k.moe_gemm_w4(x.cuda(), torch.from_numpy(off).cuda(), *packed(r9k, w), src=torch.from_numpy(src).cuda(), topk=k)
+    c = c.cpu().to(ref.F64)
+    for e in range(E):
+        lo, hi = off[e], off[e + 1]
+        if lo < hi:
+            want, before = ref.product(x[torch.from_numpy(src[lo:hi]).long() // k], w[0][e], w[1][e],
+                                       None if w[2] is None else w[2][e], group)
+            assert torch.all((c[lo:hi] - want).abs() <= ref.bf16_bound(want, before)), e
+
+
+@pytest.mark.parametrize("rows", [70000, 140000])
+@pytest.mark.parametrize("R", [9, 150])
+def test_activations_past_32_bit_offsets(r9k, rows, R):
+    """Token rows beyond 2 GiB and beyond 4 GiB, read through the index, by either kernel."""
+    K, N, E = 16384, 64, 2
+    say("far rows", rows, R)
+    x = torch.zeros((rows, K), dtype=torch.bfloat16, device="cuda")
+    g = np.random.default_rng(rows)
+    pick = np.sort(np.append(g.integers(0, rows, R - 2), [0, rows - 1])).astype(np.int32)
+    a = acts(R, K, R)
+    x[torch.from_numpy(pick).long().cuda()] = a.cuda()      # (a row picked twice holds one of its two)
+    a = x[torch.from_numpy(pick).long().cuda()].cpu()
+    w = weight((E, N), K, "int4", 64, True, 3)
+    off = torch.tensor([0, R // 3, R], dtype=torch.int32)
+    c = r9k.moe_gemm_w4(x, off.cuda(), *packed(r9k, w), src=torch.from_numpy(pick).cuda()).cpu().to(ref.F64)
+    for e in range(E):
+        lo, hi = off[e], off[e + 1]
+        want, before = ref.product(a[lo:hi], w[0][e], w[1][e], w[2][e], 64)
+        assert torch.all((c[lo:hi] - want).abs() <= ref.bf16_bound(want, before)), e
+
+
+@pytest.mark.parametrize("R", [5, 2000])
+def test_weights_past_4_gib(r9k, R):
+    """Experts' codes of 4.3 GiB: the first and the last expert's products, on some of their columns."""
+    E, N, K, group = 34, 16384, 16384, 128
+    say("far weights", R)
+    wq = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, device="cuda")
+    s = (torch.rand((E, N, K // group), device="cuda") * 0.01).to(torch.bfloat16)
+    p = r9k.pack_weight_w4(wq, s)
+    x = acts(R, K, R)
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[1:] = R // 2
+    off[E] = R
+    c = r9k.moe_gemm_w4(x.cuda(), off.cuda(), *p)
+    cols = torch.cat((torch.arange(0, 16), torch.arange(N - 16, N)))
+    for e, lo, hi in ((0, 0, R // 2), (E - 1, R // 2, R)):
+        rows = torch.unique(torch.tensor([lo, (lo + hi) // 2, hi - 1]))
+        want, before = ref.product(x[rows], wq[e][cols.cuda()].cpu(), s[e][cols.cuda()].cpu(), None, group)
+        got = c[rows.cuda()][:, cols.cuda()].cpu().to(ref.F64)
+        assert torch.all((got - want).abs() <= ref.bf16_bound(want, before)), e

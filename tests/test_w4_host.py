@@ -214,3 +214,18 @@ def test_binding_refuses_host_tensors():
         r9k.moe_permute(None, torch.zeros((2, 2), dtype=i32), 4)
     with pytest.raises(ValueError):
         r9k.moe_unpermute(torch.zeros((4, 64)), torch.zeros((2, 2), dtype=i32))
+
+
+def test_plans_of_drawn_shapes(L):
+    """The workspace query over 3000 drawn shapes: whole fp32 partial outputs, at most eight of them, and the same
+    answer again."""
+    import random
+    rng = random.Random(11)
+    for _ in range(3000):
+        M = int(2 ** rng.uniform(0, 14))
+        K, N = 128 * int(2 ** rng.uniform(0, 9)), 16 * int(2 ** rng.uniform(0, 12))
+        rc, need = _ws(L.r9k_gemm_w4_workspace, M, K, N)
+        assert rc == 0 and need % 256 == 0
+        per = 4 * M * N
+        assert any(need == (per * s + 255) // 256 * 256 for s in range(2, 9)) or need == 0, (M, K, N, need)
+        assert _ws(L.r9k_gemm_w4_workspace, M, K, N) == (0, need)
