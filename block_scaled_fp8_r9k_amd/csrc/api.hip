@@ -64,10 +64,6 @@ const Tuning &tuning() {
         t.skinny_ksplit = num("R9K_SKINNY_KSPLIT");
         t.bf16a_gs = (int)num("R9K_BF16A_GS");
         t.mid = getenv("R9K_MID") ? (int)num("R9K_MID") : -1;
-        if (const char *e = getenv("R9K_W4")) sscanf(e, "%d,%d,%d,%d", &t.w4[0], &t.w4[1], &t.w4[2], &t.w4[3]);
-        t.w4_tiled[0] = -1;
-        if (const char *e = getenv("R9K_W4_TILED"))
-            if (sscanf(e, "%d,%d,%d", &t.w4_tiled[0], &t.w4_tiled[1], &t.w4_tiled[2]) < 1) t.w4_tiled[0] = -1;
         t.moe_mtr = (int)num("R9K_MOE_MTR");
         if (const char *e = getenv("R9K_MID_CFG"))
             if (sscanf(e, "%d,%d,%d,%d,%d", &t.mid_cfg[0], &t.mid_cfg[1], &t.mid_cfg[2], &t.mid_cfg[3],
@@ -106,10 +102,6 @@ int check_device() {
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 constexpr int64_t MAX_DIM = int64_t(1) << 24;
-
-// Experts that the sort and the expert products take: the sort keeps four counters an
-// expert in a CTA's LDS
-constexpr int64_t MOE_MAX_E = 2048;
 
 // The mid-width kernel's CTAs that one wave of the MI355X's 256 compute units holds
 constexpr int64_t MID_ONE_WAVE_CTAS = 256;
@@ -602,218 +594,6 @@ int r9k_moe_route(const float *logits, int64_t T, int64_t E, int64_t topk, int32
     if (T == 0) return R9K_OK;
     if (int rc = check_device()) return rc;
     return launch_result(launch_moe_route(logits, T, E, (int)topk, topk_ids, topk_w, (hipStream_t)stream));
-}
-
-// ---- 4-bit weights ------------------------------------------------------------
-
-static bool w4_known(int format, int group, bool zeros) {
-    if (format == R9K_W4_INT) return group == 32 || group == 64 || group == 128;
-    return format == R9K_W4_MXFP4 && group == 32 && !zeros;
-}
-
-static bool w4_shape(int64_t N, int64_t K, int64_t nmul) {
-    return N > 0 && K > 0 && N % nmul == 0 && K % 128 == 0 && N <= 128 * MAX_DIM && K <= MAX_DIM &&
-           N <= (int64_t(1) << 46) / K;
-}
-
-static bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
-}
-
-int r9k_quant_weight_w4(const uint16_t *w, int64_t N, int64_t K, int format, int group, uint8_t *wq, void *s,
-                        uint8_t *z, void *stream) {
-    if (!w || !wq || !s) return R9K_ERR_NULLPTR;
-    if (!w4_shape(N, K, 16) || N * K / 8 / 256 >= (int64_t(1) << 31)) return R9K_ERR_SHAPE;
-    if (!w4_known(format, group, z != nullptr)) return R9K_ERR_ARG;
-    if (!aligned16(w) || !aligned16(wq) || !aligned16(s) || !aligned16(z)) return R9K_ERR_ALIGN;
-    if (int rc = check_device()) return rc;
-    return launch_result(launch_quant_weight_w4(w, N, K, format, group, wq, s, z, (hipStream_t)stream));
-}
-
-int r9k_pack_weight_w4(const uint8_t *wq, const void *s, const uint8_t *z, int64_t N, int64_t K, int format,
-                       int group, uint8_t *wp, void *sp, uint8_t *zp, void *stream) {
-    if (!wq || !s || !wp || !sp) return R9K_ERR_NULLPTR;
-    if (!w4_shape(N, K, 16) || N / 16 * (K / 128) / 4 >= (int64_t(1) << 31)) return R9K_ERR_SHAPE;
-    if (!w4_known(format, group, z != nullptr) || (z == nullptr) != (zp == nullptr)) return R9K_ERR_ARG;
-    if (!aligned16(wq) || !aligned16(s) || !aligned16(z) || !aligned16(wp) || !aligned16(sp) || !aligned16(zp))
-        return R9K_ERR_ALIGN;
-    const int64_t ng = N * (K / group), sb = ng * (format == R9K_W4_INT ? 2 : 1);
-    if (overlap(wq, N * K / 2, wp, N * K / 2) || overlap(s, sb, sp, sb) || (z && overlap(z, ng, zp, ng)))
-        return R9K_ERR_ARG;  // in place is not supported
-    if (int rc = check_device()) return rc;
-    return launch_result(launch_pack_weight_w4(wq, s, z, N, K, format, group, wp, sp, zp, (hipStream_t)stream));
-}
-
-// A 4-bit product's kernel, and its workspace: the partial sums of a K split, which
-// only dense products take.
-struct W4Plan {
-    W4TiledCfg tiled;
-    W4Cfg cfg;
-    size_t bytes;
-};
-static W4Plan w4_plan_new(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
-    W4Plan w{w4_tiled_config(M, K, N, E, silu), {}, 0};
-    if (!w.tiled.on) w.cfg = w4_config(M, K, N, E, silu);
-    const int split = w.tiled.on ? w.tiled.ksplit : w.cfg.ksplit;
-    if (split > 1) w.bytes = align_up((size_t)split * (size_t)(M * N) * sizeof(float), 256);
-    return w;
-}
-
-// The plan of a shape, kept for each thread's last shapes: planning takes about a
-// microsecond, a third of a launch.
-static const W4Plan &w4_plan(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
-    struct Entry {
-        int64_t M = -1, K, N, E;
-        bool silu;
-        W4Plan plan;
-    };
-    static thread_local Entry table[64];
-    const uint64_t h = ((uint64_t)M * 0x9E3779B97F4A7C15u) ^ ((uint64_t)K * 0xC2B2AE3D27D4EB4Fu) ^
-                       ((uint64_t)N * 0x165667B19E3779F9u) ^ ((uint64_t)(2 * E + silu) * 0x27D4EB2F165667C5u);
-    Entry &t = table[h >> 58];
-    if (t.M != M || t.K != K || t.N != N || t.E != E || t.silu != silu) {
-        t.plan = w4_plan_new(M, K, N, E, silu);
-        t.M = M, t.K = K, t.N = N, t.E = E, t.silu = silu;
-    }
-    return t.plan;
-}
-
-static int run_w4(W4Args &a, int format, int group, void *workspace, size_t ws_bytes, hipStream_t s) {
-    const W4Plan &w = w4_plan(a.M, a.K, a.N, a.offsets ? a.E : 0, a.silu != 0);
-    if (w.bytes && !workspace) return R9K_ERR_NULLPTR;
-    if (ws_bytes < w.bytes) return R9K_ERR_WORKSPACE;
-    if (int rc = check_device()) return rc;
-    a.part = (float *)workspace;
-    return launch_result(w.tiled.on ? launch_gemm_w4_tiled(a, format, group, w.tiled, s)
-                                    : launch_gemm_w4(a, format, group, w.cfg, s));
-}
-
-int r9k_gemm_w4_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes) {
-    if (!bytes) return R9K_ERR_NULLPTR;
-    if (M < 0 || M > MAX_DIM || !w4_shape(N, K, 16)) return R9K_ERR_SHAPE;
-    *bytes = M ? w4_plan(M, K, N, 0, false).bytes : 0;
-    return R9K_OK;
-}
-
-int r9k_gemm_w4(const uint16_t *a, int64_t M, int64_t K, const uint8_t *wp, const void *sp, const uint8_t *zp,
-                int format, int group, int64_t N, uint16_t *c, void *workspace, size_t ws_bytes, void *stream) {
-    if (!a || !wp || !sp || !c) return R9K_ERR_NULLPTR;
-    if (M < 0 || M > MAX_DIM || !w4_shape(N, K, 16) || N > MAX_DIM) return R9K_ERR_SHAPE;
-    if (!w4_known(format, group, zp != nullptr)) return R9K_ERR_ARG;
-    if (!aligned16(a) || !aligned16(wp) || !aligned16(sp) || !aligned16(zp) || !aligned16(c) || !aligned16(workspace))
-        return R9K_ERR_ALIGN;
-    if (M == 0) return R9K_OK;
-    W4Args w{a, wp, sp, zp, c, M, K, N, nullptr, nullptr, 1, 1, M, 0, nullptr};
-    return run_w4(w, format, group, workspace, ws_bytes, (hipStream_t)stream);
-}
-
-static bool w4_moe_shape(int64_t arows, int64_t E, int64_t R, int64_t K, int64_t N, bool silu) {
-    return R >= 0 && R < 128 * MAX_DIM && E >= 1 && E <= MOE_MAX_E && arows >= 0 && arows < 128 * MAX_DIM &&
-           w4_shape(N, K, silu ? 32 : 16) && N <= MAX_DIM && (R == 0 || arows >= 1);
-}
-
-int r9k_moe_gemm_w4(const uint16_t *a, int64_t arows, const int32_t *src, int64_t topk, const int32_t *offsets,
-                    int64_t E, int64_t R, int64_t K, const uint8_t *wp, const void *sp, const uint8_t *zp,
-                    int format, int group, int64_t N, int act, uint16_t *c, void *stream) {
-    if (!a || !offsets || !wp || !sp || !c) return R9K_ERR_NULLPTR;
-    const bool silu = act == R9K_ACT_SILU_MUL;
-    if (!w4_moe_shape(arows, E, R, K, N, silu) || topk < 1 || topk > MAX_DIM || (!src && arows < R))
-        return R9K_ERR_SHAPE;
-    if (!w4_known(format, group, zp != nullptr) || (act != R9K_ACT_NONE && !silu)) return R9K_ERR_ARG;
-    if (!aligned16(a) || !aligned16(src) || !aligned16(offsets) || !aligned16(wp) || !aligned16(sp) ||
-        !aligned16(zp) || !aligned16(c))
-        return R9K_ERR_ALIGN;
-    if (R == 0) return R9K_OK;
-    W4Args w{a, wp, sp, zp, c, R, K, N, offsets, src, E, topk, arows, silu ? 1 : 0, nullptr};
-    return run_w4(w, format, group, nullptr, 0, (hipStream_t)stream);
-}
-
-// ---- rows sorted by expert -----------------------------------------------------
-
-static int check_sort_shape(int64_t T, int64_t topk) {
-    if (T < 0 || T > MAX_DIM || topk < 1 || topk > 64) return R9K_ERR_SHAPE;
-    return R9K_OK;
-}
-
-// bytes of a row, or 0 if the rows' type or width is not one the library moves
-static int64_t row_bytes(int dtype, int64_t H) {
-    if (H <= 0 || H > MAX_DIM) return 0;
-    const int64_t b = H * (dtype == R9K_F32 ? 4 : 2);
-    return b % 16 ? 0 : b;
-}
-
-int r9k_moe_permute_workspace(int64_t T, int64_t E, int64_t topk, size_t *bytes) {
-    if (!bytes) return R9K_ERR_NULLPTR;
-    if (int rc = check_sort_shape(T, topk)) return rc;
-    if (E < 1 || E > MOE_MAX_E) return R9K_ERR_SHAPE;
-    *bytes = moe_sort_workspace(T * topk, E);
-    return R9K_OK;
-}
-
-int r9k_moe_permute(const void *x, int dtype, int64_t T, int64_t H, const int32_t *topk_ids, int64_t topk, int64_t E,
-                    void *xs, int32_t *src, int32_t *pos, int32_t *offsets, void *workspace, size_t ws_bytes,
-                    void *stream) {
-    if (!topk_ids || !src || !pos || !offsets || (x == nullptr) != (xs == nullptr)) return R9K_ERR_NULLPTR;
-    if (int rc = check_sort_shape(T, topk)) return rc;
-    if (E < 1 || E > MOE_MAX_E) return R9K_ERR_SHAPE;
-    int64_t rb = 0;
-    if (x) {
-        if (dtype != R9K_BF16 && dtype != R9K_F32) return R9K_ERR_ARG;
-        rb = row_bytes(dtype, H);
-        if (!rb) return R9K_ERR_SHAPE;
-    }
-    if (!aligned16(x) || !aligned16(xs) || !aligned16(topk_ids) || !aligned16(src) || !aligned16(pos) ||
-        !aligned16(offsets) || !aligned16(workspace))
-        return R9K_ERR_ALIGN;
-    if (x && overlap(x, T * rb, xs, T * topk * rb)) return R9K_ERR_ARG;
-    const size_t need = moe_sort_workspace(T * topk, E);
-    if (need && !workspace) return R9K_ERR_NULLPTR;
-    if (ws_bytes < need) return R9K_ERR_WORKSPACE;
-    if (int rc = check_device()) return rc;
-    const SortArgs a{topk_ids, x, xs, src, pos, offsets, (int32_t *)workspace, T, topk, E, rb};
-    return launch_result(launch_moe_permute(a, (hipStream_t)stream));
-}
-
-static int run_unpermute(const void *y, int dtype, int64_t T, int64_t H, const int32_t *pos, const float *w,
-                         int64_t topk, void *out, void *stream) {
-    if (!y || !pos || !out) return R9K_ERR_NULLPTR;
-    if (int rc = check_sort_shape(T, topk)) return rc;
-    if (dtype != R9K_BF16 && dtype != R9K_F32) return R9K_ERR_ARG;
-    const int64_t rb = row_bytes(dtype, H);
-    if (!rb) return R9K_ERR_SHAPE;
-    if (!aligned16(y) || !aligned16(pos) || !aligned16(w) || !aligned16(out)) return R9K_ERR_ALIGN;
-    if (overlap(y, T * topk * rb, out, T * rb)) return R9K_ERR_ARG;
-    if (T == 0) return R9K_OK;
-    if (int rc = check_device()) return rc;
-    return launch_result(
-        launch_moe_unpermute(y, dtype == R9K_F32, rb, T, topk, pos, w, out, (hipStream_t)stream));
-}
-
-int r9k_moe_unpermute(const void *y, int dtype, int64_t T, int64_t H, const int32_t *pos, const float *w,
-                      int64_t topk, void *out, void *stream) {
-    return run_unpermute(y, dtype, T, H, pos, w, topk, out, stream);
-}
-
-int r9k_moe_permute_backward(const void *gxs, int dtype, int64_t T, int64_t H, const int32_t *pos, int64_t topk,
-                             void *gx, void *stream) {
-    return run_unpermute(gxs, dtype, T, H, pos, nullptr, topk, gx, stream);
-}
-
-int r9k_moe_unpermute_backward(const void *gout, const void *y, int dtype, int64_t T, int64_t H, const int32_t *pos,
-                               const float *w, int64_t topk, void *gy, float *gw, void *stream) {
-    if (!gout || !y || !pos || !w || !gy || !gw) return R9K_ERR_NULLPTR;
-    if (int rc = check_sort_shape(T, topk)) return rc;
-    if (dtype != R9K_BF16 && dtype != R9K_F32) return R9K_ERR_ARG;
-    const int64_t rb = row_bytes(dtype, H);
-    if (!rb) return R9K_ERR_SHAPE;
-    if (!aligned16(gout) || !aligned16(y) || !aligned16(pos) || !aligned16(w) || !aligned16(gy) || !aligned16(gw))
-        return R9K_ERR_ALIGN;
-    if (overlap(y, T * topk * rb, gy, T * topk * rb) || overlap(gout, T * rb, gy, T * topk * rb)) return R9K_ERR_ARG;
-    if (T == 0) return R9K_OK;
-    if (int rc = check_device()) return rc;
-    return launch_result(launch_moe_unpermute_backward(gout, y, dtype == R9K_F32, rb, T, topk, pos, w, gy, gw,
-                                                       (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -76,6 +76,23 @@ using CfgC = Cfg<2, 4, 8, 2>;
 using CfgM1 = Cfg<4, 2, 1, 3>;
 using CfgM2 = Cfg<2, 4, 2, 3>;
 
+// Global -> LDS loads (lane l's bytes land at LDS address `l_addr` + size * l,
+// the address taken from M0).  Issued from inline asm so that the compiler
+// neither waits for them at every barrier nor before every LDS read (it cannot
+// tell that the reads touch another stage); the kernel waits for them itself
+// with wait_vm, counting this wave's load instructions.
+__device__ __forceinline__ uint32_t lds_addr(const uint8_t *p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)p;
+}
+// The global address is a wave-uniform base (SGPRs) plus a 32-bit lane offset;
+// the LDS address goes in M0, which the compiler sets from the operand.
+__device__ __forceinline__ void load_lds16(const void *base, uint32_t off, uint32_t l_addr) {
+    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(l_addr) : "memory");
+}
+__device__ __forceinline__ void load_lds4(const void *base, uint32_t off, uint32_t l_addr) {
+    asm volatile("global_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(l_addr) : "memory");
+}
+
 __device__ __forceinline__ int swz(int row, int chunk) { return row * 128 + ((chunk ^ ((row >> 1) & 7)) << 4); }
 
 // an MFMA fragment: 16 bytes at p0 and 16 at p1 (chunks q and q + 4 of a
@@ -122,6 +139,13 @@ __device__ constexpr int mfma_j(int k) {
 // into the free slot at once, tile 3 after tile 0's last MFMA (k = 5), then
 // tile t during tile t - 2
 __device__ constexpr int wread_k(int t) { return t == 2 ? 0 : t == 3 ? 6 : 4 * (t - 2); }
+
+// wait until at most VM of this wave's vector-memory instructions are in flight
+template <int VM>
+__device__ __forceinline__ void wait_vm() {
+    static_assert(VM >= 0 && VM < 64, "vmcnt");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(VM) : "memory");
+}
 }  // namespace
 
 // PK: the weights are in fragment order (r9k_pack_weight).  The W tile of a

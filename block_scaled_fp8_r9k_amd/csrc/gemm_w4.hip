@@ -26,7 +26,7 @@
 #include <cmath>
 #include <mutex>
 
-#include "r9k_internal.h"
+#include "w4_internal.h"
 #include "w4_device.h"
 
 namespace r9k {
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(512) void k_gemm_w4(W4Args p) {
     uint4 wr[D][NT];
     W4Scale<FMT, NG> sc[D][NT];
     const uint8_t *al[MT];
-    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(w4_lds_addr(lds));
 
     auto compute = [&](int c, int d) {
         w4_v8bf af[MT][4];
@@ -182,7 +182,7 @@ __global__ __launch_bounds__(512) void k_gemm_w4(W4Args p) {
             const int r = !LONG || s1 - s0 == p.seg ? (int)((uint32_t)i * p.bmagic >> 20) : i / bpr;
             const int c0 = (i - r * bpr) * 64;
             const uint16_t *row = p.a + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)arow, r) * p.K + s0 * 128;
-            if (c0 + lane < ppr) load_lds16(row + 8 * (c0 + lane), lds0 + r * pitch + c0 * 16);
+            if (c0 + lane < ppr) w4_load16(row + 8 * (c0 + lane), lds0 + r * pitch + c0 * 16);
         }
         __builtin_amdgcn_sched_barrier(0);
 
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(512) void k_gemm_w4(W4Args p) {
             __builtin_amdgcn_sched_barrier(0);  // in the order of use
         }
         // the rows (and scales) have landed once at most the D * NT code loads behind them are in flight
-        wait_vm<D * NT>();
+        w4_wait_vm<D * NT>();
         __syncthreads();
 #pragma unroll
         for (int m = 0; m < MT; ++m) al[m] = lds + min(16 * m + l16, rows - 1) * pitch + 16 * q;
@@ -351,7 +351,7 @@ W4Cfg w4_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
     const int64_t rows = E ? std::min<int64_t>(most, (int64_t)std::ceil(ave)) : most;
     const double items = E ? touched * std::max(1.0, ave / (double)RB) : (double)((M + RB - 1) / RB);
     const int64_t fit = std::max<int64_t>(1, (W4_LDS / most - 16) / 256);  // chunks whose rows fit LDS
-    const int *tune = tuning().w4;
+    const int *tune = w4_tuning().stream;
     const W4Shape wish{std::max(tune[0], silu ? 2 : 1), tune[1], tune[2]};
     bool force = false;
     for (const W4Shape &sh : shapes) force |= tune[0] && sh.nt == wish.nt && sh.wn == wish.wn && sh.wk == wish.wk;

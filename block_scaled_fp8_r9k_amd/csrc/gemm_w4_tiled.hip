@@ -23,7 +23,7 @@
 #include <algorithm>
 #include <mutex>
 
-#include "r9k_internal.h"
+#include "w4_internal.h"
 #include "w4_device.h"
 
 namespace r9k {
@@ -149,34 +149,34 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
             zp[u] = z + (((int64_t)e * tiles + col_tile(wave, d / ZPT)) * C + cb) * ZPT + d % ZPT;
         }
     }
-    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(w4_lds_addr(lds));
     const int soff = T::ABYTES + T::WBYTES + wave * (T::SBYTES + T::ZBYTES), zoff = soff + T::SBYTES;
     auto issue = [&](int st) {
         const uint32_t base = lds0 + st * T::STAGE;
 #pragma unroll
         for (int u = 0; u < TN; ++u) {
-            load_lds16(wbase[u], wlane, base + T::ABYTES + (TN * wave + u) * 1024);
+            w4_load16(wbase[u], wlane, base + T::ABYTES + (TN * wave + u) * 1024);
             wbase[u] += 1024;
         }
         if (!wide) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) load_lds16(abase, aoffs[u], base + (4 * wave + u) * 1024);
+            for (int u = 0; u < 4; ++u) w4_load16(abase, aoffs[u], base + (4 * wave + u) * 1024);
         } else {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int row = 4 * (4 * wave + u) + q;
-                load_lds16(abase + (uint64_t)aoffs[u] * (uint64_t)(2 * p.K) + 16 * (l16 ^ (row & 15)), base + (4 * wave + u) * 1024);
+                w4_load16(abase + (uint64_t)aoffs[u] * (uint64_t)(2 * p.K) + 16 * (l16 ^ (row & 15)), base + (4 * wave + u) * 1024);
             }
         }
         abase += 256;
 #pragma unroll
         for (int u = 0; u < T::SLOADS; ++u) {
-            load_lds4(sp[u], base + soff + u * 256);
+            w4_load4(sp[u], base + soff + u * 256);
             sp[u] += SPT;
         }
 #pragma unroll
         for (int u = 0; u < T::ZLOADS; ++u) {
-            load_lds4(zp[u], base + zoff + u * 256);
+            w4_load4(zp[u], base + zoff + u * 256);
             zp[u] += ZPT;
         }
     };
@@ -224,8 +224,8 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
         constexpr int st = decltype(stage)::value;
         // this chunk's stage has landed: the wave's loads issued after it are those of the NST - 2 chunks behind it
         // (fewer at the end: then wait for all)
-        if (c + NST - 2 < ce) wait_vm<(NST - 2) * T::LOADS>();
-        else wait_vm<0>();
+        if (c + NST - 2 < ce) w4_wait_vm<(NST - 2) * T::LOADS>();
+        else w4_wait_vm<0>();
         __syncthreads();
         if (c + NST - 1 < ce) issue((st + NST - 1) % NST);
         const uint8_t *sb = lds + st * T::STAGE;
@@ -402,7 +402,7 @@ W4TiledCfg w4_tiled_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu
         double alone, shared;
     } costs[] = {{1, 0.77, 0.555}, {2, 1.03, 0.747}, {4, 1.615, 1.115}};
     W4TiledCfg best{false, 4, 1};
-    const int *force = tuning().w4_tiled;
+    const int *force = w4_tuning().tiled;
     best.on = force[0] >= 0 ? force[0] > 0 : E ? M > 14 * E : M > 32;
     if (!best.on) return best;
     const int64_t C = K / 128, tiles = N / 16;

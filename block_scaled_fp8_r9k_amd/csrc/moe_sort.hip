@@ -11,7 +11,7 @@
 // row read or written once, in 16-byte pieces.
 #include <algorithm>
 
-#include "r9k_internal.h"
+#include "w4_internal.h"
 #include "w4_device.h"
 
 namespace r9k {

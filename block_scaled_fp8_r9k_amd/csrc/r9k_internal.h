@@ -19,8 +19,6 @@ namespace r9k {
 //   R9K_BF16A_GS                    bf16-activation variant: K-groups per wave
 //   R9K_MID                         mid-width kernel: 0 never, 1 wherever it fits (else the planner's choice)
 //   R9K_MID_CFG=mt,wn,wk,d[,ks]     mid-width kernel launch shape and K split (ignored where it does not fit)
-//   R9K_W4=nt,wn,wk[,ks]            4-bit weights, streaming kernel: column tiles a wave, waves along columns, K slices, K split
-//   R9K_W4_TILED=on[,tn[,ks]]       4-bit weights, tiled kernel: 0 never, 1 always; column tiles a wave, K split
 //   R9K_MOE_MTR                     MoE expert GEMMs: row tiles of 16 pairs a pass (1 or 2)
 struct Tuning {
     int decode_wn, decode_wk;
@@ -31,8 +29,6 @@ struct Tuning {
     int bf16a_gs;
     int mid;  // -1: not set
     int mid_cfg[5];
-    int w4[4];        // 4-bit weight-streaming kernel (0: the planner's)
-    int w4_tiled[3];  // 4-bit tiled kernel: 0 never, 1 always (-1: the planner's), column tiles a wave, K split
     int moe_mtr;  // MoE row tiles a pass (1 or 2; 0 = by the average pairs an expert gets)
 };
 const Tuning &tuning();
@@ -205,62 +201,6 @@ MoeLayout moe_layout(int64_t T, int64_t H, int64_t E, int64_t I, int64_t topk);
 hipError_t launch_moe_decode(const MoeArgs &args, bool fused, hipStream_t s);
 hipError_t launch_moe_route(const float *logits, int64_t T, int64_t E, int topk, int32_t *ids, float *w,
                             hipStream_t s);
-
-// ---- 4-bit weights (w4_weight.hip, gemm_w4.hip) ----
-// fmt: W4_INT or W4_MXFP4; grp: values a scale covers; the packed layout is in w4_device.h
-hipError_t launch_quant_weight_w4(const uint16_t *w, int64_t N, int64_t K, int fmt, int grp, uint8_t *wq, void *s,
-                                  uint8_t *z, hipStream_t st);
-hipError_t launch_pack_weight_w4(const uint8_t *wq, const void *s, const uint8_t *z, int64_t N, int64_t K, int fmt,
-                                 int grp, uint8_t *wp, void *sp, uint8_t *zp, hipStream_t st);
-struct W4Args {
-    const uint16_t *a;       // activations [arows][K] bf16
-    const uint8_t *wp;       // packed codes [E][N*K/2]
-    const void *sp;          // packed scales
-    const uint8_t *zp;       // packed zeros, or NULL
-    uint16_t *c;             // [M][N] bf16, or [M][N/2] with silu
-    int64_t M, K, N;         // M: rows of c (expert products: the most that offsets cover)
-    const int32_t *offsets;  // expert products: [E + 1] first rows; NULL for a dense product
-    const int32_t *src;      // expert products: row r reads activation row src[r] / topk; NULL: row r
-    int64_t E, topk, arows;
-    int silu;                // 1: columns [0, N/2) gate, [N/2, N) up, c = silu(gate) * up
-    float *part;             // with a K split: fp32 partials [ksplit][M][N] (workspace)
-    // set by the launchers
-    int nblk, nrow, ksplit;         // tiled kernel: column blocks, row blocks, K split
-    int wnl, span, seg, cps;        // streaming kernel: log2 of the waves along the columns; chunks a split, a segment, a wave's slice
-    uint32_t bmagic, tmagic, zfill; // ceil(2^20 / (64-piece blocks a row)), ceil(2^32 / topk), the zeros where none are given
-};
-struct W4Cfg {
-    int mt;      // row tiles of 16 a CTA
-    int nt;      // column tiles a wave
-    int wn, wk;  // waves along the columns, K slices
-    int ksplit;  // CTAs along K (dense products only)
-    int seg;     // chunks of 128 K whose activation rows a CTA holds in LDS at a time
-};
-W4Cfg w4_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu);
-struct W4TiledCfg {
-    bool on;     // false: the weight-streaming kernel takes the shape
-    int tn;      // column tiles a wave (4 waves along the columns)
-    int ksplit;  // CTAs along K (dense products only)
-};
-W4TiledCfg w4_tiled_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu);
-hipError_t launch_gemm_w4_tiled(const W4Args &a, int fmt, int grp, const W4TiledCfg &c, hipStream_t s);
-hipError_t launch_gemm_w4(const W4Args &a, int fmt, int grp, const W4Cfg &c, hipStream_t s);
-
-// ---- rows sorted by expert (moe_sort.hip) ----
-struct SortArgs {
-    const int32_t *ids;  // [T][topk]
-    const void *x;       // [T] rows, or NULL: the sort alone
-    void *xs;            // [T*topk] rows
-    int32_t *src, *pos, *offsets, *count;
-    int64_t T, topk, E, row_bytes;
-};
-size_t moe_sort_workspace(int64_t R, int64_t E);
-hipError_t launch_moe_permute(const SortArgs &a, hipStream_t s);
-hipError_t launch_moe_unpermute(const void *y, bool f32, int64_t row_bytes, int64_t T, int64_t topk,
-                                const int32_t *pos, const float *w, void *out, hipStream_t s);
-hipError_t launch_moe_unpermute_backward(const void *g, const void *y, bool f32, int64_t row_bytes, int64_t T,
-                                         int64_t topk, const int32_t *pos, const float *w, void *gy, float *gw,
-                                         hipStream_t s);
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

@@ -134,4 +134,34 @@ __device__ __forceinline__ uint32_t w4_div_topk(uint32_t p, uint32_t topk, uint3
     return d - (d * topk > p);
 }
 
+// ---- loads straight into LDS --------------------------------------------------
+
+// Global -> LDS loads (lane l's bytes land at LDS address `l_addr` + size * l,
+// the address taken from M0).  Issued from inline asm so that the compiler
+// neither waits for them at every barrier nor before every LDS read (it cannot
+// tell that the reads touch another stage); the kernel waits for them itself
+// with w4_wait_vm, counting this wave's load instructions.
+__device__ __forceinline__ uint32_t w4_lds_addr(const uint8_t *p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)p;
+}
+// The global address is a wave-uniform base (SGPRs) plus a 32-bit lane offset;
+// the LDS address goes in M0, which the compiler sets from the operand.
+__device__ __forceinline__ void w4_load16(const void *base, uint32_t off, uint32_t l_addr) {
+    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(l_addr) : "memory");
+}
+// The same with a 64-bit address in each lane.
+__device__ __forceinline__ void w4_load16(const void *p, uint32_t l_addr) {
+    asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(l_addr) : "memory");
+}
+__device__ __forceinline__ void w4_load4(const void *p, uint32_t l_addr) {
+    asm volatile("global_load_lds_dword %0, off" ::"v"(p), "{m0}"(l_addr) : "memory");
+}
+
+// wait until at most VM of this wave's vector-memory instructions are in flight
+template <int VM>
+__device__ __forceinline__ void w4_wait_vm() {
+    static_assert(VM >= 0 && VM < 64, "vmcnt");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(VM) : "memory");
+}
+
 }  // namespace r9k

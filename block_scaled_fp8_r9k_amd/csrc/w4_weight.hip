@@ -1,6 +1,6 @@
 // 4-bit weights at load time: the group quantiser and the packed layout.
 // Not on any hot path: each reads its input once and writes its output once.
-#include "r9k_internal.h"
+#include "w4_internal.h"
 #include "w4_device.h"
 
 namespace r9k {
