@@ -159,6 +159,7 @@ int r9k_gemm_w4(const uint16_t *a, int64_t M, int64_t K, const uint8_t *wp, cons
     if (!w4_known(format, group, zp != nullptr)) return R9K_ERR_ARG;
     if (!aligned16(a) || !aligned16(wp) || !aligned16(sp) || !aligned16(zp) || !aligned16(c) || !aligned16(workspace))
         return R9K_ERR_ALIGN;
+    if (overlap(a, 2 * M * K, c, 2 * M * N)) return R9K_ERR_ARG;
     if (M == 0) return R9K_OK;
     W4Args w{a, wp, sp, zp, c, M, K, N, nullptr, nullptr, 1, 1, M, 0, nullptr};
     return run_w4(w, format, group, workspace, ws_bytes, (hipStream_t)stream);
@@ -180,6 +181,7 @@ int r9k_moe_gemm_w4(const uint16_t *a, int64_t arows, const int32_t *src, int64_
     if (!aligned16(a) || !aligned16(src) || !aligned16(offsets) || !aligned16(wp) || !aligned16(sp) ||
         !aligned16(zp) || !aligned16(c))
         return R9K_ERR_ALIGN;
+    if (overlap(a, 2 * arows * K, c, (silu ? 1 : 2) * R * N)) return R9K_ERR_ARG;
     if (R == 0) return R9K_OK;
     W4Args w{a, wp, sp, zp, c, R, K, N, offsets, src, E, topk, arows, silu ? 1 : 0, nullptr};
     return run_w4(w, format, group, nullptr, 0, (hipStream_t)stream);
@@ -223,6 +225,10 @@ int r9k_moe_permute(const void *x, int dtype, int64_t T, int64_t H, const int32_
         !aligned16(offsets) || !aligned16(workspace))
         return R9K_ERR_ALIGN;
     if (x && overlap(x, T * rb, xs, T * topk * rb)) return R9K_ERR_ARG;
+    const int64_t slots = 4 * T * topk;  // bytes of an index; a slot's row depends on every id
+    if (overlap(topk_ids, slots, src, slots) || overlap(topk_ids, slots, pos, slots) ||
+        overlap(topk_ids, slots, offsets, 4 * (E + 1)))
+        return R9K_ERR_ARG;
     const size_t need = moe_sort_workspace(T * topk, E);
     if (need && !workspace) return R9K_ERR_NULLPTR;
     if (ws_bytes < need) return R9K_ERR_WORKSPACE;
@@ -265,7 +271,10 @@ int r9k_moe_unpermute_backward(const void *gout, const void *y, int dtype, int64
     if (!rb) return R9K_ERR_SHAPE;
     if (!aligned16(gout) || !aligned16(y) || !aligned16(pos) || !aligned16(w) || !aligned16(gy) || !aligned16(gw))
         return R9K_ERR_ALIGN;
-    if (overlap(y, T * topk * rb, gy, T * topk * rb) || overlap(gout, T * rb, gy, T * topk * rb)) return R9K_ERR_ARG;
+    const int64_t slots = 4 * T * topk;  // bytes of gw
+    if (overlap(y, T * topk * rb, gy, T * topk * rb) || overlap(gout, T * rb, gy, T * topk * rb) ||
+        overlap(y, T * topk * rb, gw, slots) || overlap(gout, T * rb, gw, slots) || overlap(w, slots, gw, slots))
+        return R9K_ERR_ARG;
     if (T == 0) return R9K_OK;
     if (int rc = check_device()) return rc;
     return launch_result(launch_moe_unpermute_backward(gout, y, dtype == R9K_F32, rb, T, topk, pos, w, gy, gw,

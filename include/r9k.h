@@ -439,9 +439,11 @@ int r9k_gemm_w4_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes);
  * any number of rows.  The activations are used as given and the weight's values
  * exactly: products, group sums and their scaling are fp32.
  *   a [M][K] bf16 -> c [M][N] bf16 (not overlapping an input).
+ * An infinity or NaN among a row's activations leaves that row of c without a
+ * finite value (NaN in places where the formula has an infinity) and no other row.
  * Errors: NULLPTR (a, wp, sp, c, or a workspace where one is needed); SHAPE if
  * M < 0, K is not a positive multiple of 128 or N of 16; ARG for an unknown
- * format, a group the format does not have, or zeros with R9K_W4_MXFP4; ALIGN;
+ * format, a group the format does not have, zeros with R9K_W4_MXFP4, or c overlapping a; ALIGN;
  * WORKSPACE; DEVICE; LAUNCH.  M = 0 launches nothing. */
 int r9k_gemm_w4(const uint16_t *a, int64_t M, int64_t K, const uint8_t *wp, const void *sp, const uint8_t *zp,
                 int format, int group, int64_t N, uint16_t *c, void *workspace, size_t ws_bytes, void *stream);
@@ -462,8 +464,8 @@ int r9k_gemm_w4(const uint16_t *a, int64_t M, int64_t K, const uint8_t *wp, cons
  * [0, R], and an index outside a reads row 0.
  * Errors: NULLPTR (a, offsets, wp, sp, c); SHAPE if R < 0, arows < 1 (with R > 0), E
  * < 1 or > 2048, topk < 1, K not a positive multiple of 128, N of 16 (of 32 with
- * silu), or without src arows < R; ARG for an unknown format, group or act, or zeros with
- * R9K_W4_MXFP4; ALIGN; DEVICE; LAUNCH.  R = 0 launches nothing. */
+ * silu), or without src arows < R; ARG for an unknown format, group or act, zeros with
+ * R9K_W4_MXFP4, or c overlapping a; ALIGN; DEVICE; LAUNCH.  R = 0 launches nothing. */
 #define R9K_ACT_NONE 0
 #define R9K_ACT_SILU_MUL 1
 int r9k_moe_gemm_w4(const uint16_t *a, int64_t arows, const int32_t *src, int64_t topk, const int32_t *offsets,
@@ -495,7 +497,7 @@ int r9k_moe_permute_workspace(int64_t T, int64_t E, int64_t topk, size_t *bytes)
  *   [T][topk], offsets [E+1] int32.
  * Errors: NULLPTR (one of x and xs alone included); SHAPE if T < 0 or > 2^24, topk < 1 or > 64, E < 1
  * or > 2048, or a row is not a positive multiple of 16 bytes; ARG for an unknown
- * dtype or xs overlapping x; ALIGN; WORKSPACE; DEVICE; LAUNCH.  T = 0 writes the
+ * dtype, xs overlapping x, or an index overlapping the ids; ALIGN; WORKSPACE; DEVICE; LAUNCH.  T = 0 writes the
  * offsets (zeros) and nothing else. */
 int r9k_moe_permute(const void *x, int dtype, int64_t T, int64_t H, const int32_t *topk_ids, int64_t topk, int64_t E,
                     void *xs, int32_t *src, int32_t *pos, int32_t *offsets, void *workspace, size_t ws_bytes,
@@ -523,7 +525,9 @@ int r9k_moe_unpermute(const void *y, int dtype, int64_t T, int64_t H, const int3
  *   as they were), gw[t][j] = sum_h gout[t][h] * y[pos[t][j]][h] in fp32, 0 for a
  *   dropped slot.
  *   gout [T][H], y [T*topk][H], pos, w as above -> gy [T*topk][H], gw [T][topk] fp32.
- * Errors: as r9k_moe_unpermute, ARG for gy overlapping gout or y. */
+ * The kept slots' positions are distinct, as r9k_moe_permute writes them.
+ * Errors: as r9k_moe_unpermute, ARG for gy overlapping gout or y, or gw overlapping
+ * gout, y or w. */
 int r9k_moe_unpermute_backward(const void *gout, const void *y, int dtype, int64_t T, int64_t H, const int32_t *pos,
                                const float *w, int64_t topk, void *gy, float *gw, void *stream);
 

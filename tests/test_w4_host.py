@@ -187,6 +187,31 @@ def test_unpermute_checks(L):
     assert with_(3, 0) == 0
 
 
+def test_outputs_on_top_of_inputs(L):
+    """An output that lies on what other threads of the call still read is refused, whole or by its last bytes."""
+    F, G, H = (c_void_p(i << 32) for i in (6, 7, 8))
+
+    def at(p, off):
+        return c_void_p(p.value + off)
+    # c [3, 48] against a [3, 256]
+    for c in (A, at(A, 2 * 3 * 256 - 16), at(A, -2 * 3 * 48 + 16)):
+        assert L.r9k_gemm_w4(A, 3, 256, B, C, NUL, INT, 64, 48, c, E16, 1 << 40, S) == -7
+        assert L.r9k_gemm_w4(A, 0, 256, B, C, NUL, INT, 64, 48, c, E16, 1 << 40, S) == 0
+    # c [16, 64 or 32] against a [8, 256]
+    for act, width in ((0, 64), (1, 32)):
+        for c in (A, at(A, 2 * 8 * 256 - 16), at(A, -2 * 16 * width + 16)):
+            assert L.r9k_moe_gemm_w4(A, 8, B, 2, C, 4, 16, 256, D, E16, NUL, INT, 128, 64, act, c, S) == -7
+    # src, pos [4, 2] and offsets [9] against the ids [4, 2]
+    for i in (8, 9, 10):
+        for p in (B, at(B, 16)):
+            x = [A, 0, 4, 64, B, 2, 8, C, D, E16, F, G, 1 << 30, S]
+            x[i] = p
+            assert L.r9k_moe_permute(*x) == -7
+    # gw [4, 2] against gout, y, w
+    for p in (A, B, D, at(B, 4 * 2 * 64 * 4 - 16), at(D, 16)):
+        assert L.r9k_moe_unpermute_backward(A, B, 1, 4, 64, C, D, 2, H, p, S) == -7
+
+
 @pytest.mark.skipif(_gpu_present(), reason="valid arguments would reach a real device")
 def test_no_device_is_reported(L):
     big, F, G = 1 << 40, c_void_p(6 << 32), c_void_p(7 << 32)
