@@ -52,6 +52,9 @@ inline int launch_result(hipError_t e) { return e == hipSuccess ? R9K_OK : R9K_E
 
 constexpr int64_t MAX_DIM = int64_t(1) << 24;
 
+// Blocks of 256 threads in a launch: the runtime refuses 2^32 threads and more
+constexpr int64_t MAX_BLOCKS = int64_t(1) << 24;
+
 // Experts that the sort and the expert products take: the sort keeps four counters an
 // expert in a CTA's LDS
 constexpr int64_t MOE_MAX_E = 2048;
@@ -80,7 +83,7 @@ static bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
 int r9k_quant_weight_w4(const uint16_t *w, int64_t N, int64_t K, int format, int group, uint8_t *wq, void *s,
                         uint8_t *z, void *stream) {
     if (!w || !wq || !s) return R9K_ERR_NULLPTR;
-    if (!w4_shape(N, K, 16) || N * K / 8 / 256 >= (int64_t(1) << 31)) return R9K_ERR_SHAPE;
+    if (!w4_shape(N, K, 16) || N * K / 8 / 256 >= MAX_BLOCKS) return R9K_ERR_SHAPE;
     if (!w4_known(format, group, z != nullptr)) return R9K_ERR_ARG;
     if (!aligned16(w) || !aligned16(wq) || !aligned16(s) || !aligned16(z)) return R9K_ERR_ALIGN;
     if (int rc = check_device()) return rc;
@@ -90,7 +93,7 @@ int r9k_quant_weight_w4(const uint16_t *w, int64_t N, int64_t K, int format, int
 int r9k_pack_weight_w4(const uint8_t *wq, const void *s, const uint8_t *z, int64_t N, int64_t K, int format,
                        int group, uint8_t *wp, void *sp, uint8_t *zp, void *stream) {
     if (!wq || !s || !wp || !sp) return R9K_ERR_NULLPTR;
-    if (!w4_shape(N, K, 16) || N / 16 * (K / 128) / 4 >= (int64_t(1) << 31)) return R9K_ERR_SHAPE;
+    if (!w4_shape(N, K, 16) || N / 16 * (K / 128) / 4 >= MAX_BLOCKS) return R9K_ERR_SHAPE;
     if (!w4_known(format, group, z != nullptr) || (z == nullptr) != (zp == nullptr)) return R9K_ERR_ARG;
     if (!aligned16(wq) || !aligned16(s) || !aligned16(z) || !aligned16(wp) || !aligned16(sp) || !aligned16(zp))
         return R9K_ERR_ALIGN;
@@ -147,7 +150,7 @@ static int run_w4(W4Args &a, int format, int group, void *workspace, size_t ws_b
 
 int r9k_gemm_w4_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes) {
     if (!bytes) return R9K_ERR_NULLPTR;
-    if (M < 0 || M > MAX_DIM || !w4_shape(N, K, 16)) return R9K_ERR_SHAPE;
+    if (M < 0 || M > MAX_DIM || !w4_shape(N, K, 16) || N > MAX_DIM) return R9K_ERR_SHAPE;
     *bytes = M ? w4_plan(M, K, N, 0, false).bytes : 0;
     return R9K_OK;
 }
@@ -190,7 +193,7 @@ int r9k_moe_gemm_w4(const uint16_t *a, int64_t arows, const int32_t *src, int64_
 // ---- rows sorted by expert -----------------------------------------------------
 
 static int check_sort_shape(int64_t T, int64_t topk) {
-    if (T < 0 || T > MAX_DIM || topk < 1 || topk > 64) return R9K_ERR_SHAPE;
+    if (T < 0 || T >= MAX_BLOCKS || topk < 1 || topk > 64) return R9K_ERR_SHAPE;  // up to a block a token
     return R9K_OK;
 }
 

@@ -443,7 +443,7 @@ static hipError_t launch_tile(W4Args a, const W4TiledCfg &c, hipStream_t s) {
     const int64_t nblk = (n + cols - 1) / cols;
     int64_t nrow = (a.M + T::BM - 1) / T::BM;
     if (a.offsets) nrow = ((a.M + std::min(a.E, a.M) * (T::BM - 1)) / T::BM + 7) / 8 * 8;
-    if (nblk * nrow > 0x7fffffff) return hipErrorInvalidValue;
+    if (nblk * nrow >= 1 << 24) return hipErrorInvalidValue;  // 2^32 threads
     a.nblk = (int)nblk;
     a.nrow = (int)nrow;
     a.ksplit = c.ksplit;

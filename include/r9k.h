@@ -411,7 +411,7 @@ int r9k_moe_ws_offset(int64_t T, int64_t H, int64_t E, int64_t I, int64_t topk, 
  *   R9K_W4_MXFP4:        s = clamp(exponent field of amax - 2, 1, 254),
  *                        q = e2m1(w / 2^(s - 127)), ties to the even code, saturating.
  *   w [N][K] bf16 -> wq, s, z as above.
- * Errors: NULLPTR; SHAPE if N is not a positive multiple of 16 or K of 128; ARG for
+ * Errors: NULLPTR; SHAPE if N is not a positive multiple of 16 or K of 128, or N * K is 2^35 or more; ARG for
  * an unknown format, a group the format does not have, or zeros with R9K_W4_MXFP4;
  * ALIGN; DEVICE; LAUNCH. */
 int r9k_quant_weight_w4(const uint16_t *w, int64_t N, int64_t K, int format, int group, uint8_t *wq, void *s,
@@ -423,7 +423,7 @@ int r9k_quant_weight_w4(const uint16_t *w, int64_t N, int64_t K, int format, int
  * j = 0..3) the codes of row 16 t + l % 16, k = 128 c + 32 j + 8 (l / 16) + 0..7;
  * the byte order inside and that of sp and zp are the library's own.  Experts'
  * weights [E][N][K/2] are packed as one weight of E * N rows.
- * Errors: as r9k_quant_weight_w4; ARG also if an output overlaps its input, or
+ * Errors: as r9k_quant_weight_w4, SHAPE from N * K = 2^37 on; ARG also if an output overlaps its input, or
  * zp is given without z or z without zp. */
 int r9k_pack_weight_w4(const uint8_t *wq, const void *s, const uint8_t *z, int64_t N, int64_t K, int format,
                        int group, uint8_t *wp, void *sp, uint8_t *zp, void *stream);
@@ -495,7 +495,7 @@ int r9k_moe_permute_workspace(int64_t T, int64_t E, int64_t topk, size_t *bytes)
  * dtype and H are then not looked at.
  *   x [T][H], xs [T*topk][H] (dtype); topk_ids [T][topk]; src [T*topk], pos
  *   [T][topk], offsets [E+1] int32.
- * Errors: NULLPTR (one of x and xs alone included); SHAPE if T < 0 or > 2^24, topk < 1 or > 64, E < 1
+ * Errors: NULLPTR (one of x and xs alone included); SHAPE if T < 0 or >= 2^24, topk < 1 or > 64, E < 1
  * or > 2048, or a row is not a positive multiple of 16 bytes; ARG for an unknown
  * dtype, xs overlapping x, or an index overlapping the ids; ALIGN; WORKSPACE; DEVICE; LAUNCH.  T = 0 writes the
  * offsets (zeros) and nothing else. */

@@ -212,6 +212,23 @@ def test_outputs_on_top_of_inputs(L):
         assert L.r9k_moe_unpermute_backward(A, B, 1, 4, 64, C, D, 2, H, p, S) == -7
 
 
+def test_sizes_past_a_launch(L):
+    """Sizes whose launch would hold 2^32 threads are refused before anything is launched, and the workspace queries
+    refuse what their calls refuse."""
+    T = 1 << 24
+    F, G = c_void_p(6 << 40), c_void_p(7 << 40)
+    far = c_void_p(1 << 46)
+    assert L.r9k_quant_weight_w4(A, 1 << 20, 1 << 15, INT, 128, B, C, D, S) == -2
+    assert L.r9k_pack_weight_w4(A, B, NUL, 1 << 22, 1 << 15, INT, 128, far, F, NUL, S) == -2
+    assert _ws(L.r9k_moe_permute_workspace, T, 8, 1)[0] == -2 and _ws(L.r9k_moe_permute_workspace, T - 1, 8, 1)[0] == 0
+    assert L.r9k_moe_permute(A, 0, T, 64, B, 1, 8, far, D, E16, F, G, 1 << 40, S) == -2
+    assert L.r9k_moe_unpermute(A, 0, T, 64, B, C, 1, far, S) == -2
+    assert L.r9k_moe_permute_backward(A, 0, T, 64, B, 1, far, S) == -2
+    assert L.r9k_moe_unpermute_backward(A, F, 0, T, 64, B, C, 1, far, G, S) == -2
+    assert _ws(L.r9k_gemm_w4_workspace, 1, 128, (1 << 24) + 16)[0] == -2
+    assert L.r9k_gemm_w4(A, 1, 128, B, C, NUL, INT, 128, (1 << 24) + 16, D, E16, 1 << 40, S) == -2
+
+
 @pytest.mark.skipif(_gpu_present(), reason="valid arguments would reach a real device")
 def test_no_device_is_reported(L):
     big, F, G = 1 << 40, c_void_p(6 << 32), c_void_p(7 << 32)
