@@ -47,9 +47,9 @@ struct W4Tile {
     static_assert((NST - 2) * LOADS < 64, "vmcnt");
 };
 
-template <int S>
-struct Stage {
-    static constexpr int value = S;
+template <int V>
+struct Const {
+    static constexpr int value = V;
 };
 __device__ __forceinline__ uint32_t hi16(float lo, float hi) {  // upper halves of two fp32
     return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
@@ -98,6 +98,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
     e = __builtin_amdgcn_readfirstlane(e);
     r0 = __builtin_amdgcn_readfirstlane(r0);
     r1 = __builtin_amdgcn_readfirstlane(r1);
+    const int mt = (r1 - r0 + 15) >> 4;  // row tiles that hold rows
     const int ks = blockIdx.y;
     const int cb = (int)((int64_t)ks * C / p.ksplit), ce = (int)((int64_t)(ks + 1) * C / p.ksplit);
 
@@ -158,7 +159,8 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
             w4_load16(wbase[u], wlane, base + T::ABYTES + (TN * wave + u) * 1024);
             wbase[u] += 1024;
         }
-        if (!wide) {
+        if (NST == 2 && wave >= mt) {  // rows that are not there (with three stages every wave's loads are counted)
+        } else if (!wide) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) w4_load16(abase, aoffs[u], base + (4 * wave + u) * 1024);
         } else {
@@ -198,10 +200,11 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
     for (int j = 0; j < TN; ++j) sz[j] = 0.0f;
     uint8_t *sums = lds + NST * T::STAGE;
     int cis = 0, half = 0;  // chunk in the step, the step's half
-    auto zero_step = [&](int h, int groups) {  // acc += sz x sums over the step's groups
-        w4_v8bf sf[4];
+    auto zero_step = [&](auto row_tiles, int h, int groups) {  // acc += sz x sums over the step's groups
+        constexpr int MT = decltype(row_tiles)::value;
+        w4_v8bf sf[MT];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
+        for (int m = 0; m < MT; ++m) {
             uint4 v = *(const uint4 *)(sums + h * (T::SUMS / 2) + ((16 * m + l16) * 4 + q) * 16);
             if (q >= groups) v = make_uint4(0, 0, 0, 0);
             sf[m] = w4_frag(v);
@@ -211,7 +214,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
             const float hi = top16(sz[j]), lo = sz[j] - hi;
             const w4_v8bf wf = __builtin_bit_cast(w4_v8bf, w4_v4u{hi16(hi, hi), hi16(hi, lo), hi16(lo, lo), 0});
 #pragma unroll
-            for (int m = 0; m < 4; ++m) acc[j][m] = w4_mfma(wf, sf[m], acc[j][m]);
+            for (int m = 0; m < MT; ++m) acc[j][m] = w4_mfma(wf, sf[m], acc[j][m]);
             sz[j] = 0.0f;
         }
     };
@@ -220,8 +223,8 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
 #pragma unroll
     for (int k = 0; k < NST - 1; ++k)
         if (cb + k < ce) issue(k);
-    auto chunk = [&](int c, auto stage) {
-        constexpr int st = decltype(stage)::value;
+    auto chunk = [&](auto row_tiles, int c, auto stage) {
+        constexpr int MT = decltype(row_tiles)::value, st = decltype(stage)::value;
         // this chunk's stage has landed: the wave's loads issued after it are those of the NST - 2 chunks behind it
         // (fewer at the end: then wait for all)
         if (c + NST - 2 < ce) w4_wait_vm<(NST - 2) * T::LOADS>();
@@ -240,31 +243,33 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                w4_v8bf af[4];
+                w4_v8bf af[MT];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) af[m] = w4_frag(*(const uint4 *)(sb + (aoff ^ (64 * k)) + 4096 * m));
+                for (int m = 0; m < MT; ++m) af[m] = w4_frag(*(const uint4 *)(sb + (aoff ^ (64 * k)) + 4096 * m));
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
                     const uint32_t word[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
                     const w4_v8bf wf = w4_fp4_frag(word[k], __uint_as_float(((sc[j] >> (8 * k)) & 255u) << 23));
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) acc[j][m] = w4_mfma(wf, af[m], acc[j][m]);
+                    for (int m = 0; m < MT; ++m) acc[j][m] = w4_mfma(wf, af[m], acc[j][m]);
                 }
             }
         } else {
             // the step before is complete: its sums are in LDS since the barrier
-            if (c > cb && cis == 0) zero_step(half ^ 1, 4);
+            if (c > cb && cis == 0) zero_step(row_tiles, half ^ 1, 4);
             // the sums of row tile `wave`, as three bf16 pieces against the pieces of sz in zero_step
+            if (MT == 4 || wave < MT) {
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                v4f sum = {0.f, 0.f, 0.f, 0.f};
+                for (int i = 0; i < NG; ++i) {
+                    v4f sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < KPG; ++k)
-                    sum = w4_mfma(w4_ones(), w4_frag(*(const uint4 *)(sb + (aoff ^ (64 * (i * KPG + k))) + 4096 * wave)), sum);
-                const float h = top16(sum[0]), d = sum[0] - h, mid = top16(d), l = d - mid;
-                if (q == 0)
-                    *(uint4 *)(sums + half * (T::SUMS / 2) + ((16 * wave + l16) * 4 + cis * NG + i) * 16) =
-                        make_uint4(hi16(h, mid), hi16(l, h), hi16(mid, l), 0);
+                    for (int k = 0; k < KPG; ++k)
+                        sum = w4_mfma(w4_ones(), w4_frag(*(const uint4 *)(sb + (aoff ^ (64 * (i * KPG + k))) + 4096 * wave)), sum);
+                    const float h = top16(sum[0]), d = sum[0] - h, mid = top16(d), l = d - mid;
+                    if (q == 0)
+                        *(uint4 *)(sums + half * (T::SUMS / 2) + ((16 * wave + l16) * 4 + cis * NG + i) * 16) =
+                            make_uint4(hi16(h, mid), hi16(l, h), hi16(mid, l), 0);
+                }
             }
             uint4 code[TN];
 #pragma unroll
@@ -292,7 +297,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
                     s[j][3] = bf16_hi(s2.y);
                 }
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
+                for (int m = 0; m < MT; ++m) {
                     w4_v8bf af[KPG];
 #pragma unroll
                     for (int k = 0; k < KPG; ++k)
@@ -313,7 +318,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) pin_acc(acc[j][m]);
+                    for (int m = 0; m < MT; ++m) pin_acc(acc[j][m]);
             }
             if (++cis == CPS) {
                 cis = 0;
@@ -322,16 +327,24 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
         }
     };
     // the stages in turn, each with its own code: LDS addresses are then constants
-    for (int c = cb; c < ce; c += NST) {
-        chunk(c, Stage<0>{});
-        if (c + 1 < ce) chunk(c + 1, Stage<1>{});
-        if constexpr (NST == 3)
-            if (c + 2 < ce) chunk(c + 2, Stage<2>{});
-    }
-    if constexpr (FMT == W4_INT) {
-        __syncthreads();  // the last step's sums; it may hold fewer than four groups
-        if (cis) zero_step(half, cis * NG);
-        else zero_step(half ^ 1, 4);
+    auto chunks = [&](auto row_tiles) {
+        for (int c = cb; c < ce; c += NST) {
+            chunk(row_tiles, c, Const<0>{});
+            if (c + 1 < ce) chunk(row_tiles, c + 1, Const<1>{});
+            if constexpr (NST == 3)
+                if (c + 2 < ce) chunk(row_tiles, c + 2, Const<2>{});
+        }
+        if constexpr (FMT == W4_INT) {
+            __syncthreads();  // the last step's sums; it may hold fewer than four groups
+            if (cis) zero_step(row_tiles, half, cis * NG);
+            else zero_step(row_tiles, half ^ 1, 4);
+        }
+    };
+    switch (mt) {  // only the row tiles that hold rows are computed
+        case 1: chunks(Const<1>{}); break;
+        case 2: chunks(Const<2>{}); break;
+        case 3: chunks(Const<3>{}); break;
+        default: chunks(Const<4>{});
     }
 #pragma unroll
     for (int j = 0; j < TN; ++j)

@@ -249,6 +249,30 @@ def _routing(T, k, E, kind, seed):
 
 
 @pytest.mark.parametrize("fmt,group,zeros", FORMATS)
+@pytest.mark.parametrize("M", [7, 33, 150])
+def test_a_row_without_a_finite_value_stays_alone(r9k, fmt, group, zeros, M):
+    """An infinity or NaN among a row's activations: no finite value in that row of the product, and the other rows are
+    to the bit what they are without it, dense and as experts' rows."""
+    say("gemm_w4 non-finite", fmt, group, zeros, M)
+    K, N, E = 512, 96, 2
+    w = weight((E, N), K, fmt, group, zeros, 31)
+    p, x = packed(r9k, w), acts(M, K, 4)
+    y = x.clone()
+    bad = [0, 3, 5, M - 1]
+    for r, k, v in zip(bad, (0, 200, K - 1, 77), (float("inf"), float("nan"), -float("inf"), float("inf"))):
+        y[r, k] = v
+    good = torch.ones(M, dtype=torch.bool)
+    good[bad] = False
+    off = torch.tensor([0, 4, M], dtype=torch.int32).cuda()
+    one = tuple(None if t is None else t[0].contiguous() for t in p)
+    for f in (lambda t: r9k.gemm_w4(t.cuda(), *one), lambda t: r9k.moe_gemm_w4(t.cuda(), off, *p),
+              lambda t: r9k.moe_gemm_w4(t.cuda(), off, *p, act="silu_mul")):
+        fine, got = f(x).cpu(), f(y).cpu()
+        assert torch.all(torch.isfinite(fine)) and torch.equal(got[good], fine[good])
+        assert not torch.any(torch.isfinite(got[bad]))
+
+
+@pytest.mark.parametrize("fmt,group,zeros", FORMATS)
 @pytest.mark.parametrize("T,k,E,K,N,kind", [(1, 1, 1, 128, 32, "rand"), (1, 8, 16, 256, 96, "rand"), (5, 2, 7, 384, 64, "drop"),
                                             (16, 4, 32, 256, 224, "rand"), (40, 2, 3, 256, 160, "rand"),
                                             (90, 3, 6, 128, 64, "skew"), (150, 2, 4, 256, 96, "one"),
