@@ -17,6 +17,15 @@
 // products have.  The CTA's waves hold consecutive K slices of the same tiles;
 // their sums are added through LDS in ascending order.
 //
+// Bound by the packed weights' bytes, each read once (per 16 or 32 rows), and below a few
+// MB by launch and latency: one row of 4096 x 14336 in int4 (groups of 128, zeros) 10 us
+// (2.9 TB/s, 70 vector instructions a chunk and wave beside the loads; a plain read of as
+// many bytes takes 6.0 us, with as many instructions 7.8), 16 rows of 14336 x 4096 in
+// mxfp4 13.6 us (2.3 TB/s, the reduce launch 4 of them), 16 tokens' top 8 of 128 experts,
+// 2048 -> 2 x 768 in int4, 33 us (4.1 TB/s).  K slices inside a CTA fill the chip where
+// there are few columns without partials in memory; a persistent loop over tiles was
+// slower than a CTA a tile (its prologue hides behind other CTAs' streams).
+//
 // For expert products the rows are ranges of `offsets`, one per expert; a CTA
 // finds its expert and row block there (the grid covers the most blocks that R
 // rows can make), and may read its activation rows through the sort's index.
@@ -319,8 +328,9 @@ __global__ __launch_bounds__(512) void k_gemm_w4(W4Args p) {
 // 32; K and N from 512 to 14336) and 4 expert shapes in int4 (group 128, zeros) and
 // mxfp4, 17 launches each, in graphs with the weights out of the caches: the launch
 // it picks takes 3% longer than the fastest of the 17 on average (at most 16%).
-// E.g. one row of 4096 x 4096 5.1 us with four slices of one tile a wave, 5.6 with eight;
-// 16 rows of 14336 x 4096 16 us in four splits, 24 in one.
+// E.g. one row of 4096 x 4096 5.2 us with four slices of one tile a wave, 5.7 with eight;
+// 16 rows of 14336 x 4096 16 us in the split it picks, 25 in one.  Up to 400 rows it
+// also decides against the tiled kernel (figures there).
 struct W4Shape {
     int nt, wn, wk;
 };
@@ -329,7 +339,7 @@ static double w4_cost(const W4Cfg &c, int64_t rows, int64_t C, int64_t M, int64_
     const int64_t span = (C + c.ksplit - 1) / c.ksplit, segs = (span + c.seg - 1) / c.seg;
     const int64_t tiles = N / 16, per = (int64_t)c.nt * c.wn;
     const double ctas = (double)((tiles + per - 1) / per * c.ksplit) * items;
-    const double lds = (double)std::max<int64_t>(rows * (c.seg * 256 + 16), (int64_t)waves * c.nt * c.mt * 1024);
+    const double lds = (double)std::max<int64_t>(std::min<int64_t>(M, 16 * c.mt) * (c.seg * 256 + 16), (int64_t)waves * c.nt * c.mt * 1024);
     const double fit = std::max(1.0, std::min(std::floor(163840.0 / lds), std::floor(20.0 / waves)));
     const double rounds = std::ceil(ctas / 256.0), turns = std::ceil(rounds / fit);
     double us = 2.1 + rounds * (0.0176 * 0.25 * (double)(rows * span) + 0.0356 * (double)(per * span) + 0.175 + 0.059 * waves);
@@ -338,24 +348,33 @@ static double w4_cost(const W4Cfg &c, int64_t rows, int64_t C, int64_t M, int64_
     return us;
 }
 
+// Row blocks of RB rows that uniform routing of M rows to E experts makes: the experts with
+// more than 0, RB, 2 RB, ... rows, their counts taken as normal with the mean's variance.
+double w4_expert_blocks(int64_t M, int64_t E, int64_t RB) {
+    const double mean = (double)M / (double)E;
+    double blocks = (double)E * (1.0 - std::pow(1.0 - 1.0 / (double)E, (double)M));
+    for (int64_t j = RB; (double)j < mean + 4.0 * std::sqrt(mean) + 1.0; j += RB)
+        blocks += (double)E * 0.5 * std::erfc(((double)j + 0.5 - mean) / std::sqrt(2.0 * mean));
+    return blocks;
+}
+
 W4Cfg w4_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
     static constexpr W4Shape shapes[] = {{1, 1, 4}, {1, 1, 8}, {1, 2, 2}, {1, 2, 4}, {1, 4, 2}, {2, 1, 2},
                                          {2, 1, 4}, {2, 1, 8}, {2, 2, 2}, {2, 2, 4}, {2, 4, 2}};
     const int64_t C = K / 128;
-    // experts: the row blocks that uniform routing makes, and the rows of one
-    const double touched = E ? (double)E * (1.0 - std::pow(1.0 - 1.0 / (double)E, (double)M)) : 1.0;
-    const double ave = (double)M / touched;
     W4Cfg best{};
-    best.mt = (E ? ave : (double)M) <= 16.0 ? 1 : 2;
+    // one row tile up to 16 rows; experts up to 12 on average, where few have more than 16 (2048
+    // -> 2 x 768 of 128 experts, int4, 8 rows an expert: 50 us, 78 with two; 4096 -> 1536 of 8,
+    // 10 rows: 14.3 and 20.3; at 15 rows 23.0, at 20 rows 16.8 with two)
+    best.mt = M <= (E ? 12 * E : 16) ? 1 : 2;
     const int64_t RB = 16 * best.mt, most = std::min<int64_t>(M, RB);
-    const int64_t rows = E ? std::min<int64_t>(most, (int64_t)std::ceil(ave)) : most;
-    const double items = E ? touched * std::max(1.0, ave / (double)RB) : (double)((M + RB - 1) / RB);
+    const double items = E ? w4_expert_blocks(M, E, RB) : (double)((M + RB - 1) / RB);
+    const int64_t rows = E ? std::min<int64_t>(most, (int64_t)std::ceil((double)M / items)) : most;
     const int64_t fit = std::max<int64_t>(1, (W4_LDS / most - 16) / 256);  // chunks whose rows fit LDS
     const int *tune = w4_tuning().stream;
     const W4Shape wish{std::max(tune[0], silu ? 2 : 1), tune[1], tune[2]};
     bool force = false;
     for (const W4Shape &sh : shapes) force |= tune[0] && sh.nt == wish.nt && sh.wn == wish.wn && sh.wk == wish.wk;
-    double best_us = 0.0;
     for (const W4Shape &sh : shapes) {
         if (force && (sh.nt != wish.nt || sh.wn != wish.wn || sh.wk != wish.wk)) continue;
         if (silu && sh.nt == 1) continue;
@@ -372,9 +391,9 @@ W4Cfg w4_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
             c.seg = (int)((span + segs - 1) / segs);
             c.wk = (int)std::min<int64_t>(sh.wk, c.seg);
             const double us = w4_cost(c, rows, C, M, N, items);
-            if (best_us == 0.0 || us < best_us) {
-                best_us = us;
+            if (best.us == 0.0 || us < best.us) {
                 best = c;
+                best.us = us;
             }
         }
     }

@@ -3,7 +3,8 @@
 // The same sums as the weight-streaming kernel (gemm_w4.hip), for row counts at
 // which the matrix instructions and not the weight bytes set the time.  C^T = W
 // A^T: four waves along the columns, each with TN column tiles by four row tiles of
-// 16; a CTA is 64 TN columns by 64 rows.
+// 16; a CTA is 64 TN columns by 64 rows, of which only the row tiles that hold rows are
+// loaded and computed (32 rows an expert, 2048 -> 2 x 768 of 128 in int4: 68 us, 83 with all four).
 //
 // Per chunk of 128 K a stage in LDS holds the A tile (bf16), the packed codes of
 // the column tiles, their scales and zeros, all moved there by global_load_lds, NST
@@ -18,6 +19,14 @@
 //   row tile w (an MFMA with ones for weights) and leaves them, split, in LDS.
 //   mxfp4: the scale is in the converted fragment (a power of two, exact) and the
 //   matrix instruction accumulates through all of K.
+// What bounds it, 4096 x 4096 x 12288: int4 in groups of 128 with zeros 414 us (996
+// TFLOP/s; a bf16 library product 328 us) with the matrix cores busy 43% of the cycles and
+// the vector units 53%: decoding is 7 instructions for 8 codes once per four row tiles,
+// promotion 4 for every 16 x 16 x 128, and a 16 x 16 x 32 MFMA hides two vector
+// instructions.  Groups of 64 477 us, of 32 591 (the promotions double and quadruple);
+// mxfp4, with nothing to promote, 305 us (1350 TFLOP/s).  Measured and not taken:
+// 32 x 32 x 16 MFMA (492 us: two product chains a wave instead of sixteen), 128 rows a CTA
+// (its registers leave one CTA a compute unit), the zero points' sums in a launch of their own.
 // A rows are 256 bytes in LDS; 16-byte piece p of row r lies at piece p ^ (r % 16),
 // so that the 16 rows of a fragment read fall on distinct banks.
 #include <algorithm>
@@ -399,41 +408,42 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
     }
 }
 
-// From 33 rows on, where the streaming kernel would read the weight more than once (for
-// experts from 14 rows on average, where many have more than 16: 2048 -> 2 x 768 of 128
-// experts, int4, 51.1 against 79.1 us at 8 rows an expert, 81.6 against 77.8 at 16, 118
-// against 77.7 at 32): the column tiles a wave and the K split of the least estimated time.  A chunk of a CTA takes `alone` when it has the
-// compute unit to itself and `shared` where the unit's CTAs keep it busy; a split adds
-// the partials and the reduce launch.  Fitted to 16 shapes (48 to 400 rows, K and N from
-// 1024 to 14336, int4 in groups of 128 with zeros, each of 12 launches): within 6%
-// (rms), and the pick 0.5% behind the fastest on average (at most 6%; other formats up
-// to 10%).  E.g. 100 rows of 4096 x 4096: 18.7 us in 4 splits of 2 tiles a wave, 26.5 whole.
-// Prefill and experts take 4 tiles a wave (4096 x 4096 x 12288: 426 us, 533 with 2).
+// The column tiles a wave and the K split of the least estimated time.  A chunk of a CTA
+// takes `alone` when it has the compute unit to itself and `shared` where the unit's CTAs
+// keep it busy, less where not all four row tiles hold rows; experts' CTAs, which find
+// their rows first and share less in the caches, a quarter more; a split adds the partials
+// and the reduce launch.  Fitted to 16 shapes (48 to 400 rows, K and N from 1024 to 14336, int4 in
+// groups of 128 with zeros, each of 12 launches) within 6% (rms).  E.g. 100 rows of 4096 x
+// 4096: 18.2 us in 4 splits of 2 tiles a wave, 37 whole; 4096 x 4096 x 12288: 414 us with 4
+// tiles, 514 with 2.
+// The streaming kernel takes what it is estimated to do sooner, always up to 32 rows.  Both
+// timed on 90 shapes (33 to 400 rows dense, 3 to 250 rows an expert, 8 to 128 experts), the
+// pick was 2% behind the faster on average, 17% at most.  E.g. (streaming, tiled; us)
+//   64 rows, int4      1024 x 4096  5.7, 9.6   4096 x 4096  13.7, 14.6   4096 x 14336  24.1, 23.8
+//   400 rows, int4     1024 x 4096  11.6, 12.5  4096 x 4096  43.6, 31.7
+//   2048 -> 2 x 768 of 128 experts, int4, rows an expert   8: 50, 58   16: 82, 62   32: 120, 70
 W4TiledCfg w4_tiled_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
     static constexpr struct {
         int tn;
         double alone, shared;
     } costs[] = {{1, 0.77, 0.555}, {2, 1.03, 0.747}, {4, 1.615, 1.115}};
-    W4TiledCfg best{false, 4, 1};
+    W4TiledCfg best{false, 4, 1, 0.0};
     const int *force = w4_tuning().tiled;
-    best.on = force[0] >= 0 ? force[0] > 0 : E ? M > 14 * E : M > 32;
-    if (!best.on) return best;
+    if (force[0] == 0 || (force[0] < 0 && !E && M <= 32)) return best;
     const int64_t C = K / 128, tiles = N / 16;
-    double best_us = 0.0;
+    const double blocks = E ? w4_expert_blocks(M, E, 64) : (double)((M + 63) / 64);
+    const double fill = (E ? 1.25 : 1.0) * (0.65 + 0.35 * std::ceil(std::min(64.0, (double)M / blocks) / 16.0) / 4.0);
     for (const auto &t : costs) {
-        if (E && t.tn != 4 && !(force[0] > 0 && force[1] == t.tn && !(silu && t.tn == 1))) continue;
-        if (!E && force[0] > 0 && force[1] && force[1] != t.tn) continue;
+        if (silu && t.tn == 1) continue;
+        if (force[0] > 0 && force[1] && force[1] != t.tn) continue;
         for (int64_t ks = 1; ks <= (E ? 1 : 8) && ks <= C; ks *= 2) {
             const int64_t want = force[0] > 0 && force[2] && !E ? std::min<int64_t>(force[2], C) : ks;
-            const double ctas = (double)((M + 63) / 64 * ((tiles + 4 * t.tn - 1) / (4 * t.tn)) * want);
+            const double ctas = blocks * (double)((tiles + 4 * t.tn - 1) / (4 * t.tn) * want);
             double load = ctas / 256.0;
             if (load <= 2.0) load = std::ceil(load);
-            double us = 3.6 + (double)((C + want - 1) / want) * std::max(t.alone, load * t.shared);
+            double us = 3.6 + (double)((C + want - 1) / want) * std::max(t.alone, load * t.shared) * fill;
             if (want > 1) us += 2.8 + 1.7e-6 * (double)(want * M * N);
-            if (best_us == 0.0 || us < best_us) {
-                best_us = us;
-                best = W4TiledCfg{true, t.tn, (int)want};
-            }
+            if (best.us == 0.0 || us < best.us) best = W4TiledCfg{true, t.tn, (int)want, us};
         }
     }
     return best;

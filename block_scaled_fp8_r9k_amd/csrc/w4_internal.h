@@ -45,12 +45,15 @@ struct W4Cfg {
     int wn, wk;  // waves along the columns, K slices
     int ksplit;  // CTAs along K (dense products only)
     int seg;     // chunks of 128 K whose activation rows a CTA holds in LDS at a time
+    double us;   // the planner's estimate
 };
+double w4_expert_blocks(int64_t M, int64_t E, int64_t RB);  // row blocks that uniform routing makes
 W4Cfg w4_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu);
 struct W4TiledCfg {
-    bool on;     // false: the weight-streaming kernel takes the shape
+    bool on;     // false: the weight-streaming kernel takes the shape whatever the estimates
     int tn;      // column tiles a wave (4 waves along the columns)
     int ksplit;  // CTAs along K (dense products only)
+    double us;   // the planner's estimate
 };
 W4TiledCfg w4_tiled_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu);
 hipError_t launch_gemm_w4_tiled(const W4Args &a, int fmt, int grp, const W4TiledCfg &c, hipStream_t s);
