@@ -191,7 +191,7 @@ __global__ __launch_bounds__(512) void k_gemm_w4(W4Args p) {
             const int r = !LONG || s1 - s0 == p.seg ? (int)((uint32_t)i * p.bmagic >> 20) : i / bpr;
             const int c0 = (i - r * bpr) * 64;
             const uint16_t *row = p.a + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)arow, r) * p.K + s0 * 128;
-            if (c0 + lane < ppr) w4_load16(row + 8 * (c0 + lane), lds0 + r * pitch + c0 * 16);
+            w4_load16_first(row + 8 * (c0 + lane), lds0 + r * pitch + c0 * 16, ppr - c0);
         }
         __builtin_amdgcn_sched_barrier(0);
 
@@ -298,6 +298,10 @@ __global__ __launch_bounds__(512) void k_gemm_w4(W4Args p) {
     const int nt = p.silu ? NT / 2 : NT;  // output tiles a wave
     const int otiles = p.silu ? tiles / 2 : tiles;
     const int outs = wn * nt * MT;
+    // the block's rows of c or of this split's partials: at most 32 rows of 2^24 columns, 2^31 bytes
+    void *first = p.ksplit > 1 ? (void *)(p.part + ((int64_t)ks * p.M + r0) * p.N) : (void *)(p.c + r0 * ldc);
+    const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
+        first, (short)0, (int)((uint32_t)rows * (uint32_t)ldc * (p.ksplit > 1 ? 4u : 2u)), 0x00020000);
     for (int it = wave; it < outs; it += nw) {
         const int w = it & (wn - 1), j = (it >> p.wnl) / MT, m = (it >> p.wnl) % MT;
         auto total = [&](int jj) {
@@ -312,12 +316,11 @@ __global__ __launch_bounds__(512) void k_gemm_w4(W4Args p) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[r] = w4_silu_mul(x[r], u[r]);
         }
-        const int r = 16 * m + l16;
-        if (t < otiles && r < rows) {
-            const int64_t at = (int64_t)(r0 + r) * ldc + 16 * t + 4 * q;
-            if (p.ksplit > 1) *(v4f *)(p.part + (int64_t)ks * p.M * p.N + at) = x;
-            else *(uint2 *)(p.c + at) = w4_bf16x4(x);
-        }
+        if (t >= otiles) continue;
+        // a store past the last row falls behind the descriptor's end and is dropped (no lane is masked)
+        const uint32_t at = (uint32_t)(16 * m + l16) * (uint32_t)ldc + 16 * t + 4 * q;
+        if (p.ksplit > 1) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), out, 4 * at, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(w4_v2u, w4_bf16x4(x)), out, 2 * at, 0, 0);
     }
 }
 

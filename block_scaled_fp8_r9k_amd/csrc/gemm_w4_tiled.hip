@@ -275,9 +275,9 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
                     for (int k = 0; k < KPG; ++k)
                         sum = w4_mfma(w4_ones(), w4_frag(*(const uint4 *)(sb + (aoff ^ (64 * (i * KPG + k))) + 4096 * wave)), sum);
                     const float h = top16(sum[0]), d = sum[0] - h, mid = top16(d), l = d - mid;
-                    if (q == 0)
-                        *(uint4 *)(sums + half * (T::SUMS / 2) + ((16 * wave + l16) * 4 + cis * NG + i) * 16) =
-                            make_uint4(hi16(h, mid), hi16(l, h), hi16(mid, l), 0);
+                    // the four lanes of row l16 hold the same sum and write the same bytes: no lane is masked
+                    *(uint4 *)(sums + half * (T::SUMS / 2) + ((16 * wave + l16) * 4 + cis * NG + i) * 16) =
+                        make_uint4(hi16(h, mid), hi16(l, h), hi16(mid, l), 0);
                 }
             }
             uint4 code[TN];
@@ -288,7 +288,9 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
                 const float s = __uint_as_float((uint32_t)*(const uint16_t *)(sb + soff + SPT * j + 2 * at) << 16);
                 const uint32_t zb = *(sb + zoff + ZPT * j + at);  // (a scale's byte where there are no zeros)
                 const float z = (float)(p.zp ? zb : 8u);
-                if (q / NG == cis) sz[j] = -s * z;
+                float v = -s * z;
+                asm volatile("" : "+v"(v));  // formed in every lane, so that the choice is a select and masks no lane
+                sz[j] = q / NG == cis ? v : sz[j];
             }
 #pragma unroll
             for (int i = 0; i < NG; ++i) {

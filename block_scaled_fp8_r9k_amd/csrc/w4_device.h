@@ -25,6 +25,7 @@ namespace r9k {
 
 typedef __bf16 w4_v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 w4_v2bf __attribute__((ext_vector_type(2)));
+typedef unsigned int w4_v2u __attribute__((ext_vector_type(2)));
 typedef unsigned int w4_v4u __attribute__((ext_vector_type(4)));
 
 enum { W4_INT = 0, W4_MXFP4 = 1 };
@@ -152,6 +153,14 @@ __device__ __forceinline__ void w4_load16(const void *base, uint32_t off, uint32
 // The same with a 64-bit address in each lane.
 __device__ __forceinline__ void w4_load16(const void *p, uint32_t l_addr) {
     asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(l_addr) : "memory");
+}
+// The same for the first n lanes (n >= 1, the same in all lanes).  Called where the whole
+// wave is enabled; the mask is set and lifted here and not by a branch, so that no later
+// MFMA can be moved under it.
+__device__ __forceinline__ void w4_load16_first(const void *p, uint32_t l_addr, int n) {
+    const uint64_t mask = n >= 64 ? ~0ull : (1ull << n) - 1;
+    asm volatile("s_mov_b64 exec, %1\n\tglobal_load_lds_dwordx4 %0, off\n\ts_mov_b64 exec, -1" ::"v"(p), "s"(mask), "{m0}"(l_addr)
+                 : "memory");
 }
 __device__ __forceinline__ void w4_load4(const void *p, uint32_t l_addr) {
     asm volatile("global_load_lds_dword %0, off" ::"v"(p), "{m0}"(l_addr) : "memory");
