@@ -327,11 +327,11 @@ __global__ __launch_bounds__(512) void k_gemm_w4(W4Args p) {
 // The launch of the least estimated time.  A compute unit's CTAs take turns for the
 // LDS and registers they need; its busiest unit moves A (activations into LDS) and W
 // (codes) and pays for each CTA and wave; a turn is as long as the longest slice; a K
-// split adds its partials and the reduce launch.  Fitted to 28 dense shapes (M = 1, 4, 16,
-// 32; K and N from 512 to 14336) and 4 expert shapes in int4 (group 128, zeros) and
-// mxfp4, 17 launches each, in graphs with the weights out of the caches: the launch
-// it picks takes 3% longer than the fastest of the 17 on average (at most 16%).
-// E.g. one row of 4096 x 4096 5.2 us with four slices of one tile a wave, 5.7 with eight;
+// split adds its partials and the reduce launch.  Fitted to 30 dense shapes (M = 1, 4, 16; K
+// and N from 1024 to 14336, int4 in groups of 128 with zeros), 10 launches each, in graphs with
+// the weights out of the caches: the launch it picks takes 1% longer than the fastest of the
+// ten on average (at most 8%).
+// E.g. one row of 4096 x 4096 5.1 us with four slices of one tile a wave, 5.6 with eight;
 // 16 rows of 14336 x 4096 16 us in the split it picks, 25 in one.  Up to 400 rows it
 // also decides against the tiled kernel (figures there).
 struct W4Shape {
@@ -345,8 +345,8 @@ static double w4_cost(const W4Cfg &c, int64_t rows, int64_t C, int64_t M, int64_
     const double lds = (double)std::max<int64_t>(std::min<int64_t>(M, 16 * c.mt) * (c.seg * 256 + 16), (int64_t)waves * c.nt * c.mt * 1024);
     const double fit = std::max(1.0, std::min(std::floor(163840.0 / lds), std::floor(20.0 / waves)));
     const double rounds = std::ceil(ctas / 256.0), turns = std::ceil(rounds / fit);
-    double us = 2.1 + rounds * (0.0176 * 0.25 * (double)(rows * span) + 0.0356 * (double)(per * span) + 0.175 + 0.059 * waves);
-    us += turns * (0.1115 * (double)((c.seg + c.wk - 1) / c.wk * segs * c.nt * c.mt) + 1.12 * (double)(segs - 1));
+    double us = 1.5 + 0.2 * waves + rounds * (0.0176 * 0.25 * (double)(rows * span) + 0.0356 * (double)(per * span) + 0.175 + 0.03 * waves);
+    us += turns * (0.13 * (double)((c.seg + c.wk - 1) / c.wk * segs * c.nt * c.mt) + 1.12 * (double)(segs - 1));
     if (c.ksplit > 1) us += 2.5 + 2.0e-6 * (double)(c.ksplit * M * N);
     return us;
 }
