@@ -2,6 +2,7 @@
 // plans and launches.  Declarations, argument meanings and error behaviour: r9k.h.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdio>
 #include <cstdlib>
@@ -109,16 +110,24 @@ int r9k_pack_weight_w4(const uint8_t *wq, const void *s, const uint8_t *z, int64
 struct W4Plan {
     W4TiledCfg tiled;
     W4Cfg cfg;
-    size_t bytes;
+    bool tile[2];  // the tiled kernel takes it; [1]: int4 in groups of 32
+    size_t bytes;  // of either choice, since the workspace query does not know the format
 };
 static W4Plan w4_plan_new(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
-    W4Plan w{w4_tiled_config(M, K, N, E, silu), w4_config(M, K, N, E, silu), 0};
-    // The kernel of the least estimated time (measured around it: gemm_w4_tiled.hip); a dense
-    // product's row blocks share the weight in the caches, 8% less for the streaming kernel than
-    // estimated.  Its grid holds 65535 row blocks; 2^19 rows of 2048 experts stay below.
-    if (w.tiled.on && w4_tuning().tiled[0] < 0) w.tiled.on = w.tiled.us < (E ? 1.0 : 0.92) * w.cfg.us || M >= 1 << 19;
-    const int split = w.tiled.on ? w.tiled.ksplit : w.cfg.ksplit;
-    if (split > 1) w.bytes = align_up((size_t)split * (size_t)(M * N) * sizeof(float), 256);
+    W4Plan w{w4_tiled_config(M, K, N, E, silu), w4_config(M, K, N, E, silu), {}, 0};
+    for (int fine = 0; fine < 2; ++fine) {
+        // The kernel of the least estimated time (measured around it: gemm_w4_tiled.hip).  A dense
+        // product's row blocks share the weight in the caches, 8% less for the streaming kernel than
+        // estimated; groups of 32 cost it 10% more than the tiled kernel (100 rows of 4096 x 4096:
+        // 21.6 against 20.1 us, in groups of 128 16.9 against 18.3).  Its grid holds 65535 row
+        // blocks; 2^19 rows of 2048 experts stay below.
+        const double stream = w.cfg.us * (E ? 1.0 : 0.92) * (fine ? 1.1 : 1.0);
+        bool &tile = w.tile[fine];
+        tile = w.tiled.on;
+        if (tile && w4_tuning().tiled[0] < 0) tile = w.tiled.us < stream || M >= 1 << 19;
+        const int split = tile ? w.tiled.ksplit : w.cfg.ksplit;
+        if (split > 1) w.bytes = std::max(w.bytes, align_up((size_t)split * (size_t)(M * N) * sizeof(float), 256));
+    }
     return w;
 }
 
@@ -147,7 +156,7 @@ static int run_w4(W4Args &a, int format, int group, void *workspace, size_t ws_b
     if (ws_bytes < w.bytes) return R9K_ERR_WORKSPACE;
     if (int rc = check_device()) return rc;
     a.part = (float *)workspace;
-    return launch_result(w.tiled.on ? launch_gemm_w4_tiled(a, format, group, w.tiled, s)
+    return launch_result(w.tile[format == R9K_W4_INT && group == 32] ? launch_gemm_w4_tiled(a, format, group, w.tiled, s)
                                     : launch_gemm_w4(a, format, group, w.cfg, s));
 }
 
