@@ -330,14 +330,16 @@ __global__ __launch_bounds__(512) void k_gemm_w4(W4Args p) {
 // split adds its partials and the reduce launch.  Fitted to 30 dense shapes (M = 1, 4, 16; K
 // and N from 1024 to 14336, int4 in groups of 128 with zeros), 10 launches each, in graphs with
 // the weights out of the caches: the launch it picks takes 1% longer than the fastest of the
-// ten on average (at most 8%).
+// ten on average (at most 8%).  Experts, whose turns begin with the search for their rows
+// and whose bytes hide behind other CTAs' starts: 15 shapes (8 to 128 experts, up to 8 rows each, int4 and mxfp4,
+// 128 to 1536 wide), 11 launches each, 1% (at most 11%).
 // E.g. one row of 4096 x 4096 5.1 us with four slices of one tile a wave, 5.6 with eight;
 // 16 rows of 14336 x 4096 16 us in the split it picks, 25 in one.  Up to 400 rows it
 // also decides against the tiled kernel (figures there).
 struct W4Shape {
     int nt, wn, wk;
 };
-static double w4_cost(const W4Cfg &c, int64_t rows, int64_t C, int64_t M, int64_t N, double items) {
+static double w4_cost(const W4Cfg &c, int64_t rows, int64_t C, int64_t M, int64_t N, int64_t E, double items) {
     const int waves = c.wn * c.wk;
     const int64_t span = (C + c.ksplit - 1) / c.ksplit, segs = (span + c.seg - 1) / c.seg;
     const int64_t tiles = N / 16, per = (int64_t)c.nt * c.wn;
@@ -345,6 +347,9 @@ static double w4_cost(const W4Cfg &c, int64_t rows, int64_t C, int64_t M, int64_
     const double lds = (double)std::max<int64_t>(std::min<int64_t>(M, 16 * c.mt) * (c.seg * 256 + 16), (int64_t)waves * c.nt * c.mt * 1024);
     const double fit = std::max(1.0, std::min(std::floor(163840.0 / lds), std::floor(20.0 / waves)));
     const double rounds = std::ceil(ctas / 256.0), turns = std::ceil(rounds / fit);
+    if (E)
+        return 0.9 + 0.28 * waves + rounds * (0.0189 * 0.25 * (double)(rows * span) + 0.0108 * (double)(per * span) + 0.015 * waves) +
+               turns * (0.22 * (double)((c.seg + c.wk - 1) / c.wk * segs * c.nt * c.mt) + 1.12 * (double)(segs - 1) + 3.55);
     double us = 1.5 + 0.2 * waves + rounds * (0.0176 * 0.25 * (double)(rows * span) + 0.0356 * (double)(per * span) + 0.175 + 0.03 * waves);
     us += turns * (0.13 * (double)((c.seg + c.wk - 1) / c.wk * segs * c.nt * c.mt) + 1.12 * (double)(segs - 1));
     if (c.ksplit > 1) us += 2.5 + 2.0e-6 * (double)(c.ksplit * M * N);
@@ -393,7 +398,7 @@ W4Cfg w4_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
             const int64_t segs = (span + fit - 1) / fit;
             c.seg = (int)((span + segs - 1) / segs);
             c.wk = (int)std::min<int64_t>(sh.wk, c.seg);
-            const double us = w4_cost(c, rows, C, M, N, items);
+            const double us = w4_cost(c, rows, C, M, N, E, items);
             if (best.us == 0.0 || us < best.us) {
                 best = c;
                 best.us = us;
