@@ -18,11 +18,11 @@
 // their sums are added through LDS in ascending order.
 //
 // Bound by the packed weights' bytes, each read once (per 16 or 32 rows), and below a few
-// MB by launch and latency: one row of 4096 x 14336 in int4 (groups of 128, zeros) 10 us
-// (2.9 TB/s, 70 vector instructions a chunk and wave beside the loads; a plain read of as
+// MB by launch and latency: one row of 4096 x 14336 in int4 (groups of 128, zeros) 9.9 us
+// (3.1 TB/s, 70 vector instructions a chunk and wave beside the loads; a plain read of as
 // many bytes takes 6.0 us, with as many instructions 7.8), 16 rows of 14336 x 4096 in
-// mxfp4 13.6 us (2.3 TB/s, the reduce launch 4 of them), 16 tokens' top 8 of 128 experts,
-// 2048 -> 2 x 768 in int4, 33 us (4.1 TB/s).  K slices inside a CTA fill the chip where
+// mxfp4 14 us (2.3 TB/s, the reduce launch 4 of them), 16 tokens' top 8 of 128 experts,
+// 2048 -> 2 x 768 in int4, 34 us (4.0 TB/s).  K slices inside a CTA fill the chip where
 // there are few columns without partials in memory; a persistent loop over tiles was
 // slower than a CTA a tile (its prologue hides behind other CTAs' streams).
 //

@@ -20,8 +20,8 @@
 //   mxfp4: the scale is in the converted fragment (a power of two, exact) and the
 //   matrix instruction accumulates through all of K.
 // What bounds it, 4096 x 4096 x 12288: int4 in groups of 128 with zeros 414 us (996
-// TFLOP/s; a bf16 library product 328 us) with the matrix cores busy 43% of the cycles and
-// the vector units 53%: decoding is 7 instructions for 8 codes once per four row tiles,
+// TFLOP/s; a bf16 library product 328 us) with the matrix cores busy 44% of the cycles and
+// the vector units 51%: decoding is 7 instructions for 8 codes once per four row tiles,
 // promotion 4 for every 16 x 16 x 128, and a 16 x 16 x 32 MFMA hides two vector
 // instructions.  Groups of 64 477 us, of 32 591 (the promotions double and quadruple);
 // mxfp4, with nothing to promote, 305 us (1350 TFLOP/s).  Measured and not taken:
