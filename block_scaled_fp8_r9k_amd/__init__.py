@@ -556,14 +556,14 @@ def gemm_w4(a, wp, sp, zp=None, c=None, workspace=None, stream=None) -> torch.Te
     # The checks of a well-formed call with its output and workspace given, in one
     # expression (a decode call's host time counts: 1.2 us less than one by one); any
     # other call goes through the checks that name what is wrong.
-    dev = _cur_device() if a.is_cuda else -1
+    dev = _dev(a, "a")  # a host tensor's index is -1: never compared with another's
     if c is not None and a.dtype in BF16 and c.dtype in BF16 and wp.dtype in U8 and len(a.shape) == len(sp.shape) == 2:
         M, K = a.shape
         N, groups = sp.shape
         if (wp.shape == (N, K // 2) and c.shape == (M, N) and M and groups and K % (2 * groups) == 0
                 and sp.dtype in _W4_SCALES and a.is_contiguous() and wp.is_contiguous() and sp.is_contiguous()
                 and c.is_contiguous()
-                and a.get_device() == wp.get_device() == sp.get_device() == c.get_device() == dev
+                and wp.get_device() == sp.get_device() == c.get_device() == dev
                 and (zp is None or (zp.dtype in U8 and zp.shape == (N, groups) and zp.is_contiguous()
                                     and zp.get_device() == dev))):
             need = gemm_w4_workspace(M, K, N)
@@ -574,7 +574,6 @@ def gemm_w4(a, wp, sp, zp=None, c=None, workspace=None, stream=None) -> torch.Te
             if rc:
                 _check(rc, "r9k_gemm_w4")
             return c
-    dev = _dev(a, "a")
     w, s, z, fmt, K, group = _w4_format(wp, sp, zp, dev, 2)
     M, N = a.shape[0], wp.shape[0]
     pa = _addr(a, BF16, "a", dev, (M, K))

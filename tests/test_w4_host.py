@@ -271,3 +271,29 @@ def test_plans_of_drawn_shapes(L):
         per = 4 * M * N
         assert any(need == (per * s + 255) // 256 * 256 for s in range(2, 9)) or need == 0, (M, K, N, need)
         assert _ws(L.r9k_gemm_w4_workspace, M, K, N) == (0, need)
+
+
+@pytest.mark.parametrize("c", [False, True])
+@pytest.mark.parametrize("workspace", [False, True])
+def test_gemm_refuses_host_tensors_in_every_form(monkeypatch, c, workspace):
+    """All operands on the host, with and without the output and the workspace: refused, and no call is made with a
+    host address (the library is replaced by one that counts its calls)."""
+    import torch
+    import block_scaled_fp8_r9k_amd as r9k
+    calls = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: calls.append(name) or 0
+    monkeypatch.setattr(r9k, "lib", Lib)
+    monkeypatch.setattr(r9k, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(r9k, "gemm_w4_workspace", lambda M, K, N: 0)
+    bf, u8 = torch.bfloat16, torch.uint8
+    a, wp, sp, zp = torch.zeros((1, 128), dtype=bf), torch.zeros((16, 64), dtype=u8), torch.zeros((16, 1), dtype=bf), None
+    kw = dict(c=torch.zeros((1, 16), dtype=bf)) if c else {}
+    if workspace:
+        kw["workspace"] = torch.zeros(256, dtype=u8)
+    for zp in (None, torch.zeros((16, 1), dtype=u8)):
+        with pytest.raises(ValueError, match="current device"):
+            r9k.gemm_w4(a, wp, sp, zp, **kw)
+    assert not calls
