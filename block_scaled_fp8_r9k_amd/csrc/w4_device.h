@@ -146,24 +146,26 @@ __device__ __forceinline__ uint32_t w4_lds_addr(const uint8_t *p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)p;
 }
 // The global address is a wave-uniform base (SGPRs) plus a 32-bit lane offset;
-// the LDS address goes in M0, which the compiler sets from the operand.
+// the LDS address goes in M0, which the compiler sets from the operand.  A load needs one
+// wait state after the write of M0, which the compiler does not keep for inline asm: each
+// load brings its own.
 __device__ __forceinline__ void w4_load16(const void *base, uint32_t off, uint32_t l_addr) {
-    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(l_addr) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(l_addr) : "memory");
 }
 // The same with a 64-bit address in each lane.
 __device__ __forceinline__ void w4_load16(const void *p, uint32_t l_addr) {
-    asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(l_addr) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(l_addr) : "memory");
 }
 // The same for the first n lanes (n >= 1, the same in all lanes).  Called where the whole
 // wave is enabled; the mask is set and lifted here and not by a branch, so that no later
-// MFMA can be moved under it.
+// MFMA can be moved under it.  (Setting the mask is the wait state after the write of M0.)
 __device__ __forceinline__ void w4_load16_first(const void *p, uint32_t l_addr, int n) {
     const uint64_t mask = n >= 64 ? ~0ull : (1ull << n) - 1;
     asm volatile("s_mov_b64 exec, %1\n\tglobal_load_lds_dwordx4 %0, off\n\ts_mov_b64 exec, -1" ::"v"(p), "s"(mask), "{m0}"(l_addr)
                  : "memory");
 }
 __device__ __forceinline__ void w4_load4(const void *p, uint32_t l_addr) {
-    asm volatile("global_load_lds_dword %0, off" ::"v"(p), "{m0}"(l_addr) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(l_addr) : "memory");
 }
 
 // wait until at most VM of this wave's vector-memory instructions are in flight
