@@ -594,8 +594,8 @@ def moe_gemm_w4(x, offsets, wp, sp, zp=None, src=None, topk: int = 1, act: str =
                 stream=None) -> torch.Tensor:
     """The experts' products on sorted rows (r9k_moe_gemm_w4): offsets [E+1] and src [R] from moe_permute, (wp, sp,
     zp) the packed weights [E,N,K/2] -> [R,N] bf16, or with act="silu_mul" [R,N/2].  Without src, x [R,K] holds the
-    sorted rows; with it, x [T,K] the tokens' rows and row r reads x[src[r] // topk].  Rows from offsets[E] on are
-    not written."""
+    sorted rows; with it, x [T,K] the tokens' rows and row r reads x[src[r] // topk], topk as in the sort (R more than
+    T * topk is refused).  Rows from offsets[E] on are not written."""
     dev = _dev(x, "x")
     w, s, z, fmt, K, group = _w4_format(wp, sp, zp, dev, 3)
     if act not in _ACTS:

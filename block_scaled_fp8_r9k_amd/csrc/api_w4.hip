@@ -190,8 +190,8 @@ int r9k_moe_gemm_w4(const uint16_t *a, int64_t arows, const int32_t *src, int64_
                     int format, int group, int64_t N, int act, uint16_t *c, void *stream) {
     if (!a || !offsets || !wp || !sp || !c) return R9K_ERR_NULLPTR;
     const bool silu = act == R9K_ACT_SILU_MUL;
-    if (!w4_moe_shape(arows, E, R, K, N, silu) || topk < 1 || topk > MAX_DIM || (!src && arows < R))
-        return R9K_ERR_SHAPE;
+    if (!w4_moe_shape(arows, E, R, K, N, silu) || topk < 1 || topk > MAX_DIM || R > arows * (src ? topk : 1))
+        return R9K_ERR_SHAPE;  // more rows than there are slots (or, without an index, rows of a)
     if (!w4_known(format, group, zp != nullptr) || (act != R9K_ACT_NONE && !silu)) return R9K_ERR_ARG;
     if (!aligned16(a) || !aligned16(src) || !aligned16(offsets) || !aligned16(wp) || !aligned16(sp) ||
         !aligned16(zp) || !aligned16(c))

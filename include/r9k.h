@@ -464,7 +464,7 @@ int r9k_gemm_w4(const uint16_t *a, int64_t M, int64_t K, const uint8_t *wp, cons
  * [0, R], and an index outside a reads row 0.
  * Errors: NULLPTR (a, offsets, wp, sp, c); SHAPE if R < 0, arows < 1 (with R > 0), E
  * < 1 or > 2048, topk < 1, K not a positive multiple of 128, N of 16 (of 32 with
- * silu), or without src arows < R; ARG for an unknown format, group or act, zeros with
+ * silu), R > arows * topk with src, or R > arows without; ARG for an unknown format, group or act, zeros with
  * R9K_W4_MXFP4, or c overlapping a; ALIGN; DEVICE; LAUNCH.  R = 0 launches nothing. */
 #define R9K_ACT_NONE 0
 #define R9K_ACT_SILU_MUL 1

@@ -297,3 +297,17 @@ def test_gemm_refuses_host_tensors_in_every_form(monkeypatch, c, workspace):
         with pytest.raises(ValueError, match="current device"):
             r9k.gemm_w4(a, wp, sp, zp, **kw)
     assert not calls
+
+
+def test_moe_gemm_refuses_an_index_that_does_not_go_with_the_rows(L):
+    """src numbers slots of arows tokens with topk each: more rows than slots cannot be such an index (topk left at 1
+    with a top-8 sort would read row 0 for most of them)."""
+    F = c_void_p(6 << 32)
+
+    def call(arows, topk, R, src=B, act=1):
+        return L.r9k_moe_gemm_w4(A, arows, src, topk, C, 4, R, 256, D, E16, NUL, INT, 128, 64, act, F, S)
+    for arows, topk, R in ((8, 1, 16), (8, 2, 17), (16, 8, 129), (1, 1, 2), (8, 1, 1 << 30)):
+        assert call(arows, topk, R) == -2 and call(arows, topk, R, act=0) == -2
+    if not _gpu_present():  # every slot, or some of them, is an index
+        for arows, topk, R in ((8, 2, 16), (8, 2, 9), (16, 8, 128), (1 << 20, 1 << 20, 1 << 20)):
+            assert call(arows, topk, R) == -4
