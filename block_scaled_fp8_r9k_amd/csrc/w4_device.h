@@ -4,7 +4,7 @@
 //   int4   codes q = 0..15, value (q - z) * s: s bf16 per group of 32, 64 or 128
 //          along K, z a zero point 0..15 per group (8 where none are given);
 //   mxfp4  codes e2m1 (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives), value
-//          v * 2^(e - 127), e a byte per group of 32.
+//          v * 2^(e - 127), e a byte per group of 32 (255: NaN).
 // Packed layout (r9k_pack_weight_w4), for 16-row tile t = n / 16 and chunk
 // c = k / 128 (C = K / 128 chunks): the 1 KiB block at (t * C + c) * 1024 holds
 // at 16 * l the 16 bytes that MFMA lane l (row l % 16, quarter q = l / 16)
@@ -44,7 +44,8 @@ __device__ __forceinline__ w4_v8bf w4_int_frag(uint32_t x) {
 }
 
 // Eight e2m1 codes (one packed word) times the group's scale -> eight bf16.
-// Two significant bits times a power of two: exact in bf16.
+// Two significant bits times a power of two: exact in bf16, infinite from 2^128 on.  The
+// converter takes the scale's exponent field alone: e = 0, 0.0f here, is 2^-127, and 255 NaN.
 __device__ __forceinline__ w4_v8bf w4_fp4_frag(uint32_t x, float scale) {
     const w4_v4u u = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 0)),
                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 1)),

@@ -396,7 +396,8 @@ int r9k_moe_ws_offset(int64_t T, int64_t H, int64_t E, int64_t I, int64_t topk, 
  *                 = 32, 64 or 128 values along K.  z: a zero point 0..15 per group
  *                 (uint8_t), or none, which means 8.
  *   R9K_W4_MXFP4  codes e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 the sign); value
- *                 v * 2^(s - 127).  s: uint8_t, one per 32 values, 1..254; no zeros.
+ *                 v * 2^(s - 127).  s: uint8_t, one per 32 values; 255 makes the group
+ *                 NaN, and a value of 2^128 or more counts as an infinity; no zeros.
  * Row-major: wq [N][K/2], s [N][K/group], z [N][K/group].  K is a multiple of
  * 128, N of 16.  The products read a packed copy (r9k_pack_weight_w4), in which
  * the codes, scales and zeros keep their sizes and values. */

@@ -1,0 +1,60 @@
+"""4-bit weights at the ends of their formats' ranges: scale bytes, infinities and NaN."""
+import pytest
+import torch
+
+from tests import w4_ref as ref
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def r9k():
+    import block_scaled_fp8_r9k_amd as m
+    assert torch.cuda.is_available()
+    m.lib()
+    return m
+
+
+def _mxfp4(N, K, byte):
+    """Row n of the weight holds code n % 16 everywhere, with the scale byte `byte` in every group."""
+    code = (torch.arange(N) % 16).to(torch.uint8)
+    return (code | code << 4)[:, None].expand(N, K // 2).contiguous(), torch.full((N, K // 32), byte, dtype=torch.uint8)
+
+
+E2M1 = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=ref.F64)
+
+
+@pytest.mark.parametrize("M", [1, 20, 150, 1100])
+@pytest.mark.parametrize("byte", [0, 1, 2, 127, 252, 253, 254])
+def test_mxfp4_every_code_at_the_ends(r9k, M, byte):
+    """One activation a row is not zero, so the product is one value of the weight times a power of two: exact.  From
+    2^128 on a value is an infinity, and times the row's zeros NaN."""
+    say("mxfp4 byte", byte, M)
+    N, K = 32, 256
+    wq, s = _mxfp4(N, K, byte)
+    p = r9k.pack_weight_w4(wq.cuda(), s.cuda())
+    scale = 2.0 ** 100 if byte < 100 else 1.0 if byte < 200 else 2.0 ** -100
+    a = torch.zeros((M, K), dtype=torch.bfloat16)
+    a[torch.arange(M), (torch.arange(M) * 37) % K] = scale
+    got = r9k.gemm_w4(a.cuda(), *p).cpu().to(ref.F64)
+    code = torch.arange(N) % 16
+    value = E2M1[code % 8] * torch.where(code >= 8, -1.0, 1.0) * 2.0 ** (byte - 127)
+    finite = value.abs() < 2.0 ** 128
+    assert torch.equal(got[:, finite], (value * scale)[finite].expand(M, -1))
+    assert torch.all(torch.isnan(got[:, ~finite]))
+
+
+@pytest.mark.parametrize("M", [1, 20, 150, 1100])
+def test_mxfp4_byte_255_is_nan(r9k, M):
+    """The format's NaN scale: its rows of the weight are NaN, the others are to the bit what they are without it."""
+    say("mxfp4 byte 255", M)
+    N, K = 48, 256
+    wq, s = _mxfp4(N, K, 120)
+    a = torch.randn((M, K), generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).cuda()
+    fine = r9k.gemm_w4(a, *r9k.pack_weight_w4(wq.cuda(), s.cuda()))
+    s[5, 3] = s[16, 0] = 255
+    got = r9k.gemm_w4(a, *r9k.pack_weight_w4(wq.cuda(), s.cuda()))
+    keep = torch.ones(N, dtype=torch.bool)
+    keep[[5, 16]] = False
+    assert torch.all(torch.isnan(got.cpu()[:, ~keep])) and torch.equal(got.cpu()[:, keep], fine.cpu()[:, keep])
