@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "r9k.h"
@@ -76,9 +77,27 @@ static bool w4_shape(int64_t N, int64_t K, int64_t nmul) {
            N <= (int64_t(1) << 46) / K;
 }
 
-static bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+// Bytes that a call reads or writes.  Its CTAs read while others write, so an output
+// (a workspace too) may lie on no input and on no other output.
+struct Span {
+    const void *p;
+    int64_t n;
+};
+static bool overlap(const Span &a, const Span &b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return a.p && b.p && a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
+}
+static bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span &i : ins)
+            if (overlap(*o, i)) return true;
+        for (auto q = outs.begin(); q != o; ++q)
+            if (overlap(*o, *q)) return true;
+    }
+    return false;
+}
+static int64_t w4_scale_bytes(int64_t N, int64_t K, int format, int group) {
+    return N * (K / group) * (format == R9K_W4_INT ? 2 : 1);
 }
 
 int r9k_quant_weight_w4(const uint16_t *w, int64_t N, int64_t K, int format, int group, uint8_t *wq, void *s,
@@ -87,6 +106,8 @@ int r9k_quant_weight_w4(const uint16_t *w, int64_t N, int64_t K, int format, int
     if (!w4_shape(N, K, 16) || N * K / 8 / 256 >= MAX_BLOCKS) return R9K_ERR_SHAPE;
     if (!w4_known(format, group, z != nullptr)) return R9K_ERR_ARG;
     if (!aligned16(w) || !aligned16(wq) || !aligned16(s) || !aligned16(z)) return R9K_ERR_ALIGN;
+    if (clash({{wq, N * K / 2}, {s, w4_scale_bytes(N, K, format, group)}, {z, N * (K / group)}}, {{w, 2 * N * K}}))
+        return R9K_ERR_ARG;
     if (int rc = check_device()) return rc;
     return launch_result(launch_quant_weight_w4(w, N, K, format, group, wq, s, z, (hipStream_t)stream));
 }
@@ -98,9 +119,8 @@ int r9k_pack_weight_w4(const uint8_t *wq, const void *s, const uint8_t *z, int64
     if (!w4_known(format, group, z != nullptr) || (z == nullptr) != (zp == nullptr)) return R9K_ERR_ARG;
     if (!aligned16(wq) || !aligned16(s) || !aligned16(z) || !aligned16(wp) || !aligned16(sp) || !aligned16(zp))
         return R9K_ERR_ALIGN;
-    const int64_t ng = N * (K / group), sb = ng * (format == R9K_W4_INT ? 2 : 1);
-    if (overlap(wq, N * K / 2, wp, N * K / 2) || overlap(s, sb, sp, sb) || (z && overlap(z, ng, zp, ng)))
-        return R9K_ERR_ARG;  // in place is not supported
+    const int64_t cb = N * K / 2, sb = w4_scale_bytes(N, K, format, group), zb = N * (K / group);
+    if (clash({{wp, cb}, {sp, sb}, {zp, zb}}, {{wq, cb}, {s, sb}, {z, zb}})) return R9K_ERR_ARG;  // in place too
     if (int rc = check_device()) return rc;
     return launch_result(launch_pack_weight_w4(wq, s, z, N, K, format, group, wp, sp, zp, (hipStream_t)stream));
 }
@@ -154,6 +174,11 @@ static int run_w4(W4Args &a, int format, int group, void *workspace, size_t ws_b
     const W4Plan &w = w4_plan(a.M, a.K, a.N, a.offsets ? a.E : 0, a.silu != 0);
     if (w.bytes && !workspace) return R9K_ERR_NULLPTR;
     if (ws_bytes < w.bytes) return R9K_ERR_WORKSPACE;
+    // (what a dense product reads: a split, which alone takes a workspace, is none of the experts')
+    if (w.bytes && clash({{workspace, (int64_t)w.bytes}},
+                         {{a.a, 2 * a.M * a.K}, {a.wp, a.N * a.K / 2}, {a.sp, w4_scale_bytes(a.N, a.K, format, group)},
+                          {a.zp, a.N * (a.K / group)}, {a.c, 2 * a.M * a.N}}))
+        return R9K_ERR_ARG;
     if (int rc = check_device()) return rc;
     a.part = (float *)workspace;
     return launch_result(w.tile[format == R9K_W4_INT && group == 32] ? launch_gemm_w4_tiled(a, format, group, w.tiled, s)
@@ -174,7 +199,9 @@ int r9k_gemm_w4(const uint16_t *a, int64_t M, int64_t K, const uint8_t *wp, cons
     if (!w4_known(format, group, zp != nullptr)) return R9K_ERR_ARG;
     if (!aligned16(a) || !aligned16(wp) || !aligned16(sp) || !aligned16(zp) || !aligned16(c) || !aligned16(workspace))
         return R9K_ERR_ALIGN;
-    if (overlap(a, 2 * M * K, c, 2 * M * N)) return R9K_ERR_ARG;
+    if (clash({{c, 2 * M * N}}, {{a, 2 * M * K}, {wp, N * K / 2}, {sp, w4_scale_bytes(N, K, format, group)},
+                                 {zp, N * (K / group)}}))
+        return R9K_ERR_ARG;
     if (M == 0) return R9K_OK;
     W4Args w{a, wp, sp, zp, c, M, K, N, nullptr, nullptr, 1, 1, M, 0, nullptr};
     return run_w4(w, format, group, workspace, ws_bytes, (hipStream_t)stream);
@@ -196,7 +223,10 @@ int r9k_moe_gemm_w4(const uint16_t *a, int64_t arows, const int32_t *src, int64_
     if (!aligned16(a) || !aligned16(src) || !aligned16(offsets) || !aligned16(wp) || !aligned16(sp) ||
         !aligned16(zp) || !aligned16(c))
         return R9K_ERR_ALIGN;
-    if (overlap(a, 2 * arows * K, c, (silu ? 1 : 2) * R * N)) return R9K_ERR_ARG;
+    if (clash({{c, (silu ? 1 : 2) * R * N}},
+              {{a, 2 * arows * K}, {src, 4 * R}, {offsets, 4 * (E + 1)}, {wp, E * N * K / 2},
+               {sp, E * w4_scale_bytes(N, K, format, group)}, {zp, E * N * (K / group)}}))
+        return R9K_ERR_ARG;
     if (R == 0) return R9K_OK;
     W4Args w{a, wp, sp, zp, c, R, K, N, offsets, src, E, topk, arows, silu ? 1 : 0, nullptr};
     return run_w4(w, format, group, nullptr, 0, (hipStream_t)stream);
@@ -239,12 +269,11 @@ int r9k_moe_permute(const void *x, int dtype, int64_t T, int64_t H, const int32_
     if (!aligned16(x) || !aligned16(xs) || !aligned16(topk_ids) || !aligned16(src) || !aligned16(pos) ||
         !aligned16(offsets) || !aligned16(workspace))
         return R9K_ERR_ALIGN;
-    if (x && overlap(x, T * rb, xs, T * topk * rb)) return R9K_ERR_ARG;
-    const int64_t slots = 4 * T * topk;  // bytes of an index; a slot's row depends on every id
-    if (overlap(topk_ids, slots, src, slots) || overlap(topk_ids, slots, pos, slots) ||
-        overlap(topk_ids, slots, offsets, 4 * (E + 1)))
-        return R9K_ERR_ARG;
     const size_t need = moe_sort_workspace(T * topk, E);
+    const int64_t slots = 4 * T * topk;  // bytes of an index
+    if (clash({{xs, T * topk * rb}, {src, slots}, {pos, slots}, {offsets, 4 * (E + 1)}, {workspace, (int64_t)need}},
+              {{x, T * rb}, {topk_ids, slots}}))
+        return R9K_ERR_ARG;
     if (need && !workspace) return R9K_ERR_NULLPTR;
     if (ws_bytes < need) return R9K_ERR_WORKSPACE;
     if (int rc = check_device()) return rc;
@@ -260,7 +289,7 @@ static int run_unpermute(const void *y, int dtype, int64_t T, int64_t H, const i
     const int64_t rb = row_bytes(dtype, H);
     if (!rb) return R9K_ERR_SHAPE;
     if (!aligned16(y) || !aligned16(pos) || !aligned16(w) || !aligned16(out)) return R9K_ERR_ALIGN;
-    if (overlap(y, T * topk * rb, out, T * rb)) return R9K_ERR_ARG;
+    if (clash({{out, T * rb}}, {{y, T * topk * rb}, {pos, 4 * T * topk}, {w, 4 * T * topk}})) return R9K_ERR_ARG;
     if (T == 0) return R9K_OK;
     if (int rc = check_device()) return rc;
     return launch_result(
@@ -286,9 +315,8 @@ int r9k_moe_unpermute_backward(const void *gout, const void *y, int dtype, int64
     if (!rb) return R9K_ERR_SHAPE;
     if (!aligned16(gout) || !aligned16(y) || !aligned16(pos) || !aligned16(w) || !aligned16(gy) || !aligned16(gw))
         return R9K_ERR_ALIGN;
-    const int64_t slots = 4 * T * topk;  // bytes of gw
-    if (overlap(y, T * topk * rb, gy, T * topk * rb) || overlap(gout, T * rb, gy, T * topk * rb) ||
-        overlap(y, T * topk * rb, gw, slots) || overlap(gout, T * rb, gw, slots) || overlap(w, slots, gw, slots))
+    const int64_t slots = 4 * T * topk;  // bytes of pos, w and gw
+    if (clash({{gy, T * topk * rb}, {gw, slots}}, {{gout, T * rb}, {y, T * topk * rb}, {pos, slots}, {w, slots}}))
         return R9K_ERR_ARG;
     if (T == 0) return R9K_OK;
     if (int rc = check_device()) return rc;

@@ -400,7 +400,9 @@ int r9k_moe_ws_offset(int64_t T, int64_t H, int64_t E, int64_t I, int64_t topk, 
  *                 NaN, and a value of 2^128 or more counts as an infinity; no zeros.
  * Row-major: wq [N][K/2], s [N][K/group], z [N][K/group].  K is a multiple of
  * 128, N of 16.  The products read a packed copy (r9k_pack_weight_w4), in which
- * the codes, scales and zeros keep their sizes and values. */
+ * the codes, scales and zeros keep their sizes and values.
+ * In these calls and those of the sorted rows below, no output and no workspace may
+ * overlap an input, another output or the workspace: ARG. */
 #define R9K_W4_INT 0
 #define R9K_W4_MXFP4 1
 
@@ -413,7 +415,7 @@ int r9k_moe_ws_offset(int64_t T, int64_t H, int64_t E, int64_t I, int64_t topk, 
  *                        q = e2m1(w / 2^(s - 127)), ties to the even code, saturating.
  *   w [N][K] bf16 -> wq, s, z as above.
  * Errors: NULLPTR; SHAPE if N is not a positive multiple of 16 or K of 128, or N * K is 2^35 or more; ARG for
- * an unknown format, a group the format does not have, or zeros with R9K_W4_MXFP4;
+ * an unknown format, a group the format does not have, zeros with R9K_W4_MXFP4, or an overlap;
  * ALIGN; DEVICE; LAUNCH. */
 int r9k_quant_weight_w4(const uint16_t *w, int64_t N, int64_t K, int format, int group, uint8_t *wq, void *s,
                         uint8_t *z, void *stream);
@@ -424,7 +426,7 @@ int r9k_quant_weight_w4(const uint16_t *w, int64_t N, int64_t K, int format, int
  * j = 0..3) the codes of row 16 t + l % 16, k = 128 c + 32 j + 8 (l / 16) + 0..7;
  * the byte order inside and that of sp and zp are the library's own.  Experts'
  * weights [E][N][K/2] are packed as one weight of E * N rows.
- * Errors: as r9k_quant_weight_w4, SHAPE from N * K = 2^37 on; ARG also if an output overlaps its input, or
+ * Errors: as r9k_quant_weight_w4, SHAPE from N * K = 2^37 on; ARG also if
  * zp is given without z or z without zp. */
 int r9k_pack_weight_w4(const uint8_t *wq, const void *s, const uint8_t *z, int64_t N, int64_t K, int format,
                        int group, uint8_t *wp, void *sp, uint8_t *zp, void *stream);
@@ -439,12 +441,12 @@ int r9k_gemm_w4_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes);
  *   c[m][n] = bf16( sum_k a[m][k] * value(n, k) ),
  * any number of rows.  The activations are used as given and the weight's values
  * exactly: products, group sums and their scaling are fp32.
- *   a [M][K] bf16 -> c [M][N] bf16 (not overlapping an input).
+ *   a [M][K] bf16 -> c [M][N] bf16.
  * An infinity or NaN among a row's activations leaves that row of c without a
  * finite value (NaN in places where the formula has an infinity) and no other row.
  * Errors: NULLPTR (a, wp, sp, c, or a workspace where one is needed); SHAPE if
  * M < 0, K is not a positive multiple of 128 or N of 16; ARG for an unknown
- * format, a group the format does not have, zeros with R9K_W4_MXFP4, or c overlapping a; ALIGN;
+ * format, a group the format does not have, zeros with R9K_W4_MXFP4, or an overlap; ALIGN;
  * WORKSPACE; DEVICE; LAUNCH.  M = 0 launches nothing. */
 int r9k_gemm_w4(const uint16_t *a, int64_t M, int64_t K, const uint8_t *wp, const void *sp, const uint8_t *zp,
                 int format, int group, int64_t N, uint16_t *c, void *workspace, size_t ws_bytes, void *stream);
@@ -466,7 +468,7 @@ int r9k_gemm_w4(const uint16_t *a, int64_t M, int64_t K, const uint8_t *wp, cons
  * Errors: NULLPTR (a, offsets, wp, sp, c); SHAPE if R < 0, arows < 1 (with R > 0), E
  * < 1 or > 2048, topk < 1, K not a positive multiple of 128, N of 16 (of 32 with
  * silu), R > arows * topk with src, or R > arows without; ARG for an unknown format, group or act, zeros with
- * R9K_W4_MXFP4, or c overlapping a; ALIGN; DEVICE; LAUNCH.  R = 0 launches nothing. */
+ * R9K_W4_MXFP4, or an overlap; ALIGN; DEVICE; LAUNCH.  R = 0 launches nothing. */
 #define R9K_ACT_NONE 0
 #define R9K_ACT_SILU_MUL 1
 int r9k_moe_gemm_w4(const uint16_t *a, int64_t arows, const int32_t *src, int64_t topk, const int32_t *offsets,
@@ -498,7 +500,7 @@ int r9k_moe_permute_workspace(int64_t T, int64_t E, int64_t topk, size_t *bytes)
  *   [T][topk], offsets [E+1] int32.
  * Errors: NULLPTR (one of x and xs alone included); SHAPE if T < 0 or >= 2^24, topk < 1 or > 64, E < 1
  * or > 2048, or a row is not a positive multiple of 16 bytes; ARG for an unknown
- * dtype, xs overlapping x, or an index overlapping the ids; ALIGN; WORKSPACE; DEVICE; LAUNCH.  T = 0 writes the
+ * dtype, or an overlap; ALIGN; WORKSPACE; DEVICE; LAUNCH.  T = 0 writes the
  * offsets (zeros) and nothing else. */
 int r9k_moe_permute(const void *x, int dtype, int64_t T, int64_t H, const int32_t *topk_ids, int64_t topk, int64_t E,
                     void *xs, int32_t *src, int32_t *pos, int32_t *offsets, void *workspace, size_t ws_bytes,
@@ -516,8 +518,7 @@ int r9k_moe_permute_backward(const void *gxs, int dtype, int64_t T, int64_t H, c
  * fp32, rounded once; 0 for a token with none.  w NULL: weights 1.
  *   y [T*topk][H], pos [T][topk] int32, w [T][topk] fp32 -> out [T][H].
  * A position outside [0, T*topk) counts as a dropped slot.
- * Errors: NULLPTR; SHAPE as r9k_moe_permute; ARG for an unknown dtype or out
- * overlapping y; ALIGN; DEVICE; LAUNCH.  T = 0 launches nothing. */
+ * Errors: NULLPTR; SHAPE as r9k_moe_permute; ARG for an unknown dtype or an overlap; ALIGN; DEVICE; LAUNCH.  T = 0 launches nothing. */
 int r9k_moe_unpermute(const void *y, int dtype, int64_t T, int64_t H, const int32_t *pos, const float *w,
                       int64_t topk, void *out, void *stream);
 
@@ -527,8 +528,7 @@ int r9k_moe_unpermute(const void *y, int dtype, int64_t T, int64_t H, const int3
  *   dropped slot.
  *   gout [T][H], y [T*topk][H], pos, w as above -> gy [T*topk][H], gw [T][topk] fp32.
  * The kept slots' positions are distinct, as r9k_moe_permute writes them.
- * Errors: as r9k_moe_unpermute, ARG for gy overlapping gout or y, or gw overlapping
- * gout, y or w. */
+ * Errors: as r9k_moe_unpermute. */
 int r9k_moe_unpermute_backward(const void *gout, const void *y, int dtype, int64_t T, int64_t H, const int32_t *pos,
                                const float *w, int64_t topk, void *gy, float *gw, void *stream);
 

@@ -311,3 +311,64 @@ def test_moe_gemm_refuses_an_index_that_does_not_go_with_the_rows(L):
     if not _gpu_present():  # every slot, or some of them, is an index
         for arows, topk, R in ((8, 2, 16), (8, 2, 9), (16, 8, 128), (1 << 20, 1 << 20, 1 << 20)):
             assert call(arows, topk, R) == -4
+
+
+def _clashes(f, args, sizes, outs, ins):
+    """Places every output of a call on the first and on the last 16 bytes of every input and of every other output
+    and yields (what, code).  sizes: bytes by argument index; args: pointers far apart."""
+    for o in outs:
+        for i in ins + [x for x in outs if x != o]:
+            for at in (args[i].value, args[i].value + (sizes[i] - 1) // 16 * 16, args[i].value - (sizes[o] - 1) // 16 * 16):
+                x = list(args)
+                x[o] = c_void_p(at)
+                yield f"argument {o} on argument {i}", f(*x)
+
+
+def test_every_output_on_every_input_and_output(L):
+    """Every call: outputs and workspaces on top of any input or of each other are refused, whole or by their ends."""
+    P = [c_void_p(i << 33) for i in range(1, 14)]
+    N, K, M, E, R, T, H, k = 64, 256, 40, 3, 24, 512, 64, 6
+    wq, s2, z = N * K // 2, N * K // 64 * 2, N * K // 64
+    cases = [
+        (L.r9k_quant_weight_w4, [P[0], N, K, INT, 64, P[1], P[2], P[3], S], {0: 2 * N * K, 5: wq, 6: s2, 7: z}, [5, 6, 7], [0]),
+        (L.r9k_pack_weight_w4, [P[0], P[1], P[2], N, K, INT, 64, P[3], P[4], P[5], S],
+         {0: wq, 1: s2, 2: z, 7: wq, 8: s2, 9: z}, [7, 8, 9], [0, 1, 2]),
+        (L.r9k_gemm_w4, [P[0], M, K, P[1], P[2], P[3], INT, 64, N, P[4], P[5], 1 << 40, S],
+         {0: 2 * M * K, 3: wq, 4: s2, 5: z, 9: 2 * M * N}, [9], [0, 3, 4, 5]),
+        (L.r9k_moe_gemm_w4, [P[0], 8, P[1], 3, P[2], E, R, K, P[3], P[4], P[5], INT, 64, N, 1, P[6], S],
+         {0: 2 * 8 * K, 2: 4 * R, 4: 4 * (E + 1), 8: E * wq, 9: E * s2, 10: E * z, 15: R * N}, [15], [0, 2, 4, 8, 9, 10]),
+        (L.r9k_moe_permute, [P[0], 1, T, H, P[1], k, 8, P[2], P[3], P[4], P[5], P[6], 1 << 40, S],
+         {0: 4 * T * H, 4: 4 * T * k, 7: 4 * T * k * H, 8: 4 * T * k, 9: 4 * T * k, 10: 36,
+          11: _ws(L.r9k_moe_permute_workspace, T, 8, k)[1]}, [7, 8, 9, 10, 11], [0, 4]),
+        (L.r9k_moe_unpermute, [P[0], 0, T, H, P[1], P[2], k, P[3], S],
+         {0: 2 * T * k * H, 4: 4 * T * k, 5: 4 * T * k, 7: 2 * T * H}, [7], [0, 4, 5]),
+        (L.r9k_moe_permute_backward, [P[0], 0, T, H, P[1], k, P[2], S], {0: 2 * T * k * H, 4: 4 * T * k, 6: 2 * T * H}, [6], [0, 4]),
+        (L.r9k_moe_unpermute_backward, [P[0], P[1], 0, T, H, P[2], P[3], k, P[4], P[5], S],
+         {0: 2 * T * H, 1: 2 * T * k * H, 5: 4 * T * k, 6: 4 * T * k, 8: 2 * T * k * H, 9: 4 * T * k}, [8, 9], [0, 1, 5, 6]),
+    ]
+    for f, args, sizes, outs, ins in cases:
+        assert sizes.get(11) is None or sizes[11] > 0
+        for what, rc in _clashes(f, args, sizes, outs, ins):
+            assert rc == -7, (f.__name__, what, rc)
+    # a product that splits K: its workspace against everything
+    M, K, N = 1, 14336, 1024
+    need = _ws(L.r9k_gemm_w4_workspace, M, K, N)[1]
+    if need:
+        args = [P[0], M, K, P[1], P[2], P[3], INT, 128, N, P[4], P[5], need, S]
+        sizes = {0: 2 * M * K, 3: N * K // 2, 4: N * K // 64, 5: N * K // 128, 9: 2 * M * N, 10: need}
+        for what, rc in _clashes(L.r9k_gemm_w4, args, sizes, [9, 10], [0, 3, 4, 5]):
+            assert rc == -7, (what, rc)
+
+
+@pytest.mark.skipif(_gpu_present(), reason="valid arguments would reach a real device")
+def test_neighbours_do_not_overlap(L):
+    """Outputs that end where an input begins, and empty ones anywhere, are fine."""
+    N, K, M = 16, 128, 1
+    base = 1 << 33
+    at = lambda off: c_void_p(base + off)
+    # a [1, 128] 256 bytes, wp 1024, sp 32, c 32
+    assert L.r9k_gemm_w4(at(0), M, K, at(256), at(1280), NUL, INT, 128, N, at(1312), NUL, 0, S) == -4
+    assert L.r9k_gemm_w4(at(32), M, K, at(288), at(1312), NUL, INT, 128, N, at(0), NUL, 0, S) == -4
+    assert L.r9k_gemm_w4(at(0), 0, K, at(256), at(1280), NUL, INT, 128, N, at(512), NUL, 0, S) == 0
+    assert L.r9k_moe_unpermute(at(0), 0, 0, 64, at(0), at(0), 2, at(0), S) == 0
+    assert L.r9k_moe_permute(NUL, 0, 0, 64, at(0), 2, 8, NUL, at(0), at(0), at(0), NUL, 0, S) == -4
