@@ -358,11 +358,16 @@ static double w4_cost(const W4Cfg &c, int64_t rows, int64_t C, int64_t M, int64_
 
 // Row blocks of RB rows that uniform routing of M rows to E experts makes: the experts with
 // more than 0, RB, 2 RB, ... rows, their counts taken as normal with the mean's variance.
+// Counts four deviations and more below the mean are passed by every expert; where the
+// deviation is a block or more, a last block is as likely to hold any number of rows
+// (both within 2e-5 of the whole sum), so that no plan takes more than a few steps.
 double w4_expert_blocks(int64_t M, int64_t E, int64_t RB) {
-    const double mean = (double)M / (double)E;
-    double blocks = (double)E * (1.0 - std::pow(1.0 - 1.0 / (double)E, (double)M));
-    for (int64_t j = RB; (double)j < mean + 4.0 * std::sqrt(mean) + 1.0; j += RB)
-        blocks += (double)E * 0.5 * std::erfc(((double)j + 0.5 - mean) / std::sqrt(2.0 * mean));
+    const double mean = (double)M / (double)E, sd = std::sqrt(mean), rb = (double)RB;
+    if (sd >= rb) return (double)E * (mean / rb + 0.5 - 0.5 / rb);
+    const double sure = std::max(0.0, std::floor((mean - 4.0 * sd) / rb));
+    double blocks = (double)E * (1.0 - std::pow(1.0 - 1.0 / (double)E, (double)M) + sure);
+    for (double j = rb * (sure + 1.0); j < mean + 4.0 * sd + 1.0; j += rb)
+        blocks += (double)E * 0.5 * std::erfc((j + 0.5 - mean) / std::sqrt(2.0 * mean));
     return blocks;
 }
 

@@ -372,3 +372,21 @@ def test_neighbours_do_not_overlap(L):
     assert L.r9k_gemm_w4(at(0), 0, K, at(256), at(1280), NUL, INT, 128, N, at(512), NUL, 0, S) == 0
     assert L.r9k_moe_unpermute(at(0), 0, 0, 64, at(0), at(0), 2, at(0), S) == 0
     assert L.r9k_moe_permute(NUL, 0, 0, 64, at(0), 2, 8, NUL, at(0), at(0), at(0), NUL, 0, S) == -4
+
+
+@pytest.mark.skipif(_gpu_present(), reason="valid arguments would reach a real device")
+def test_planning_does_not_grow_with_the_rows(L):
+    """A call's plan costs the same for a few rows and for the most (it was a step for every block of rows: half a
+    second at 2^31 - 1)."""
+    import time
+    P = [c_void_p(1 << b) for b in range(49, 56)]
+
+    def us(R, E):
+        best = 1e9
+        for i in range(5):  # a new shape each time, so that it is planned
+            t = time.perf_counter()
+            assert L.r9k_moe_gemm_w4(P[0], R, None, 1, P[1], E, R - i, 256, P[2], P[3], None, INT, 128, 64, 0, P[4], S) == -4
+            best = min(best, 1e6 * (time.perf_counter() - t))
+        return best
+    for R, E in ((1 << 17, 1), (1 << 20, 1), (1 << 24, 2), ((1 << 31) - 1, 1), ((1 << 31) - 1, 2048)):
+        assert us(R, E) < 4 * us(16, 1) + 10, (R, E)
