@@ -23,7 +23,7 @@ from ctypes import POINTER, c_char_p, c_int, c_int64, c_size_t, c_void_p
 
 import torch
 
-ABI_VERSION = 9
+ABI_VERSION = 10
 ENGINE_AUTO, ENGINE_SKINNY, ENGINE_TILED, ENGINE_SPLITK = 0, 1, 2, 3
 TILE_AUTO, TILE_256X256, TILE_256X128, TILE_128X64, TILE_256X64 = 0, 1, 2, 3, 4
 
@@ -85,6 +85,8 @@ def lib() -> ctypes.CDLL:
                                   c_void_p, c_void_p, c_size_t, c_void_p]
         L.r9k_moe_gemm_w4.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64,
                                       c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64, c_int, c_void_p, c_void_p]
+        L.r9k_w4_plan.argtypes = [c_int64] * 4 + [c_int] * 3 + [POINTER(c_int)]
+        L.r9k_set_w4_plan.argtypes = [c_int] * 5
         L.r9k_moe_permute_workspace.argtypes = [c_int64, c_int64, c_int64, POINTER(c_size_t)]
         L.r9k_moe_permute.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int64, c_int64, c_void_p,
                                       c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]
@@ -544,7 +546,8 @@ def pack_weight_w4(wq, s, z=None, stream=None):
 
 @functools.lru_cache(maxsize=4096)
 def gemm_w4_workspace(M: int, K: int, N: int) -> int:
-    """Workspace bytes for gemm_w4 of this shape (r9k_gemm_w4_workspace); 0 for many shapes."""
+    """Workspace bytes for gemm_w4 of this shape (r9k_gemm_w4_workspace); 0 for many shapes.  Cached; set_w4_plan,
+    which changes the answer, clears the cache."""
     b = c_size_t(0)
     _check(lib().r9k_gemm_w4_workspace(M, K, N, ctypes.byref(b)), "r9k_gemm_w4_workspace")
     return b.value
@@ -616,6 +619,24 @@ def moe_gemm_w4(x, offsets, wp, sp, zp=None, src=None, topk: int = 1, act: str =
     if rc:
         _check(rc, "r9k_moe_gemm_w4")
     return c
+
+
+W4_AUTO, W4_STREAM, W4_TILED = 0, 1, 2
+
+
+def w4_plan(M: int, K: int, N: int, E: int = 0, act: str = "none", fmt: int = W4_INT, group: int = 128) -> tuple:
+    """The launch of a 4-bit product (r9k_w4_plan): (kernel W4_STREAM or W4_TILED, column tiles a wave, waves along
+    the columns, waves along K, CTAs along K, LDS segments or 0).  E = 0: gemm_w4; else moe_gemm_w4 of M rows."""
+    plan = (c_int * 6)()
+    _check(lib().r9k_w4_plan(M, K, N, E, _ACTS[act], fmt, group, plan), "r9k_w4_plan")
+    return tuple(plan)
+
+
+def set_w4_plan(kernel: int = W4_AUTO, tiles: int = 0, waves: int = 0, slices: int = 0, ksplit: int = 0) -> None:
+    """Force the launch of later 4-bit products (r9k_set_w4_plan; 0: the planner's).  A forced split changes the
+    workspace a shape needs, so the cached workspace sizes are dropped."""
+    _check(lib().r9k_set_w4_plan(kernel, tiles, waves, slices, ksplit), "r9k_set_w4_plan")
+    gemm_w4_workspace.cache_clear()
 
 
 # ------------------------------------------- rows sorted by expert ----

@@ -16,7 +16,7 @@
 using namespace r9k;
 
 namespace r9k {
-const W4Tuning &w4_tuning() {
+W4Tuning &w4_tuning() {
     static W4Tuning t{{0, 0, 0, 0}, {-1, 0, 0}};
     static std::once_flag once;
     std::call_once(once, [] {
@@ -151,11 +151,14 @@ static W4Plan w4_plan_new(int64_t M, int64_t K, int64_t N, int64_t E, bool silu)
     return w;
 }
 
-// The plan of a shape, kept for each thread's last shapes: planning takes about a
-// microsecond, a third of a launch.
+static std::atomic<int> g_plan_setting{0};  // counts the changes of the plan control
+
+// The plan of a shape under the present setting, kept for each thread's last shapes:
+// planning takes about a microsecond, a third of a launch.
 static const W4Plan &w4_plan(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
     struct Entry {
         int64_t M = -1, K, N, E;
+        int setting;
         bool silu;
         W4Plan plan;
     };
@@ -163,11 +166,16 @@ static const W4Plan &w4_plan(int64_t M, int64_t K, int64_t N, int64_t E, bool si
     const uint64_t h = ((uint64_t)M * 0x9E3779B97F4A7C15u) ^ ((uint64_t)K * 0xC2B2AE3D27D4EB4Fu) ^
                        ((uint64_t)N * 0x165667B19E3779F9u) ^ ((uint64_t)(2 * E + silu) * 0x27D4EB2F165667C5u);
     Entry &t = table[h >> 58];
-    if (t.M != M || t.K != K || t.N != N || t.E != E || t.silu != silu) {
+    const int setting = g_plan_setting.load(std::memory_order_relaxed);
+    if (t.M != M || t.K != K || t.N != N || t.E != E || t.silu != silu || t.setting != setting) {
         t.plan = w4_plan_new(M, K, N, E, silu);
-        t.M = M, t.K = K, t.N = N, t.E = E, t.silu = silu;
+        t.M = M, t.K = K, t.N = N, t.E = E, t.silu = silu, t.setting = setting;
     }
     return t.plan;
+}
+
+static bool w4_takes_tile(const W4Plan &w, int format, int group) {
+    return w.tile[format == R9K_W4_INT && group == 32];
 }
 
 static int run_w4(W4Args &a, int format, int group, void *workspace, size_t ws_bytes, hipStream_t s) {
@@ -181,8 +189,8 @@ static int run_w4(W4Args &a, int format, int group, void *workspace, size_t ws_b
         return R9K_ERR_ARG;
     if (int rc = check_device()) return rc;
     a.part = (float *)workspace;
-    return launch_result(w.tile[format == R9K_W4_INT && group == 32] ? launch_gemm_w4_tiled(a, format, group, w.tiled, s)
-                                    : launch_gemm_w4(a, format, group, w.cfg, s));
+    return launch_result(w4_takes_tile(w, format, group) ? launch_gemm_w4_tiled(a, format, group, w.tiled, s)
+                                                         : launch_gemm_w4(a, format, group, w.cfg, s));
 }
 
 int r9k_gemm_w4_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes) {
@@ -230,6 +238,39 @@ int r9k_moe_gemm_w4(const uint16_t *a, int64_t arows, const int32_t *src, int64_
     if (R == 0) return R9K_OK;
     W4Args w{a, wp, sp, zp, c, R, K, N, offsets, src, E, topk, arows, silu ? 1 : 0, nullptr};
     return run_w4(w, format, group, nullptr, 0, (hipStream_t)stream);
+}
+
+int r9k_w4_plan(int64_t M, int64_t K, int64_t N, int64_t E, int act, int format, int group, int *plan) {
+    if (!plan) return R9K_ERR_NULLPTR;
+    const bool silu = act == R9K_ACT_SILU_MUL;
+    if (E < 0 || (E ? !w4_moe_shape(M, E, M, K, N, silu) : M < 0 || M > MAX_DIM || !w4_shape(N, K, 16) || N > MAX_DIM))
+        return R9K_ERR_SHAPE;
+    if (!w4_known(format, group, false) || (act != R9K_ACT_NONE && !(silu && E))) return R9K_ERR_ARG;
+    std::fill(plan, plan + R9K_W4_PLAN_INTS, 0);
+    if (M == 0) return R9K_OK;
+    const W4Plan &w = w4_plan(M, K, N, E, silu);
+    const int tiled[] = {R9K_W4_TILED, w.tiled.tn, 4, 1, w.tiled.ksplit, 0};
+    const int stream[] = {R9K_W4_STREAM, w.cfg.nt, w.cfg.wn, w.cfg.wk, w.cfg.ksplit, w4_segments(w.cfg, K, format, group)};
+    std::copy_n(w4_takes_tile(w, format, group) ? tiled : stream, R9K_W4_PLAN_INTS, plan);
+    return R9K_OK;
+}
+
+int r9k_set_w4_plan(int kernel, int tiles, int waves, int slices, int ksplit) {
+    const bool shape = tiles || waves || slices;
+    if (ksplit < 0) return R9K_ERR_ARG;
+    W4Tuning t{{0, 0, 0, 0}, {-1, 0, 0}};
+    if (kernel == R9K_W4_STREAM) {
+        if (shape ? !w4_stream_shape(tiles, waves, slices) : ksplit != 0) return R9K_ERR_ARG;
+        t = W4Tuning{{tiles, waves, slices, ksplit}, {0, 0, 0}};
+    } else if (kernel == R9K_W4_TILED) {
+        if (waves || slices || (tiles != 0 && tiles != 1 && tiles != 2 && tiles != 4)) return R9K_ERR_ARG;
+        t = W4Tuning{{0, 0, 0, 0}, {1, tiles, ksplit}};
+    } else if (kernel != R9K_W4_AUTO || shape || ksplit) {
+        return R9K_ERR_ARG;
+    }
+    w4_tuning() = t;
+    ++g_plan_setting;
+    return R9K_OK;
 }
 
 // ---- rows sorted by expert -----------------------------------------------------

@@ -339,6 +339,13 @@ __global__ __launch_bounds__(512) void k_gemm_w4(W4Args p) {
 struct W4Shape {
     int nt, wn, wk;
 };
+static constexpr W4Shape W4_SHAPES[] = {{1, 1, 4}, {1, 1, 8}, {1, 2, 2}, {1, 2, 4}, {1, 4, 2}, {2, 1, 2},
+                                        {2, 1, 4}, {2, 1, 8}, {2, 2, 2}, {2, 2, 4}, {2, 4, 2}};
+bool w4_stream_shape(int nt, int wn, int wk) {
+    for (const W4Shape &s : W4_SHAPES)
+        if (s.nt == nt && s.wn == wn && s.wk == wk) return true;
+    return false;
+}
 static double w4_cost(const W4Cfg &c, int64_t rows, int64_t C, int64_t M, int64_t N, int64_t E, double items) {
     const int waves = c.wn * c.wk;
     const int64_t span = (C + c.ksplit - 1) / c.ksplit, segs = (span + c.seg - 1) / c.seg;
@@ -372,8 +379,6 @@ double w4_expert_blocks(int64_t M, int64_t E, int64_t RB) {
 }
 
 W4Cfg w4_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
-    static constexpr W4Shape shapes[] = {{1, 1, 4}, {1, 1, 8}, {1, 2, 2}, {1, 2, 4}, {1, 4, 2}, {2, 1, 2},
-                                         {2, 1, 4}, {2, 1, 8}, {2, 2, 2}, {2, 2, 4}, {2, 4, 2}};
     const int64_t C = K / 128;
     W4Cfg best{};
     // one row tile up to 16 rows; experts up to 12 on average, where few have more than 16 (2048
@@ -386,9 +391,8 @@ W4Cfg w4_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
     const int64_t fit = std::max<int64_t>(1, (W4_LDS / most - 16) / 256);  // chunks whose rows fit LDS
     const int *tune = w4_tuning().stream;
     const W4Shape wish{std::max(tune[0], silu ? 2 : 1), tune[1], tune[2]};
-    bool force = false;
-    for (const W4Shape &sh : shapes) force |= tune[0] && sh.nt == wish.nt && sh.wn == wish.wn && sh.wk == wish.wk;
-    for (const W4Shape &sh : shapes) {
+    const bool force = tune[0] && w4_stream_shape(wish.nt, wish.wn, wish.wk);
+    for (const W4Shape &sh : W4_SHAPES) {
         if (force && (sh.nt != wish.nt || sh.wn != wish.wn || sh.wk != wish.wk)) continue;
         if (silu && sh.nt == 1) continue;
         for (int ks = 1; ks <= (E ? 1 : 4); ks *= 2) {
@@ -414,12 +418,18 @@ W4Cfg w4_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
 }
 
 // chunks ahead: as many registers as two waves a SIMD leave, scales included
-template <int FMT, int GRP, int NT>
-constexpr int W4_AHEAD = (GRP == 32 && FMT == W4_INT ? 4 : 8) / NT;
+constexpr int w4_ahead(int fmt, int grp, int nt) { return (grp == 32 && fmt == W4_INT ? 4 : 8) / nt; }
+
+int w4_segments(const W4Cfg &c, int64_t K, int fmt, int grp) {
+    // whole: one segment, the same in every split, and slices that are loaded whole
+    const int64_t C = K / 128, span = (C + c.ksplit - 1) / c.ksplit;
+    const bool whole = c.seg >= span && C % span == 0 && (c.seg + c.wk - 1) / c.wk <= w4_ahead(fmt, grp, c.nt);
+    return whole ? 0 : (int)((span + c.seg - 1) / c.seg);
+}
 
 template <int FMT, int GRP, int MT, int NT, bool LONG>
 static hipError_t launch_one(W4Args a, const W4Cfg &c, hipStream_t s) {
-    auto kernel = k_gemm_w4<FMT, GRP, MT, NT, W4_AHEAD<FMT, GRP, NT>, LONG>;
+    auto kernel = k_gemm_w4<FMT, GRP, MT, NT, w4_ahead(FMT, GRP, NT), LONG>;
     // the dynamic LDS limit is a per-device function attribute: set it once per device
     static std::once_flag once[64];
     static hipError_t attr_err[64];
@@ -452,10 +462,8 @@ static hipError_t launch_one(W4Args a, const W4Cfg &c, hipStream_t s) {
 
 template <int FMT, int GRP, int MT, int NT>
 static hipError_t launch_nt(const W4Args &a, const W4Cfg &c, hipStream_t s) {
-    // one segment, the same in every split, and slices that are loaded whole
-    const int64_t C = a.K / 128, span = (C + c.ksplit - 1) / c.ksplit;
-    const bool whole = c.seg >= span && C % span == 0 && (c.seg + c.wk - 1) / c.wk <= W4_AHEAD<FMT, GRP, NT>;
-    return whole ? launch_one<FMT, GRP, MT, NT, false>(a, c, s) : launch_one<FMT, GRP, MT, NT, true>(a, c, s);
+    return w4_segments(c, a.K, FMT, GRP) == 0 ? launch_one<FMT, GRP, MT, NT, false>(a, c, s)
+                                              : launch_one<FMT, GRP, MT, NT, true>(a, c, s);
 }
 
 template <int FMT, int GRP, int MT>

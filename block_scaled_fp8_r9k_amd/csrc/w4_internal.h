@@ -7,14 +7,15 @@
 
 namespace r9k {
 
-// Tuning overrides, read from the environment once per process (as struct Tuning's):
+// Tuning overrides: r9k_set_w4_plan's, before its first call the environment's, read
+// once per process (as struct Tuning's):
 //   R9K_W4=nt,wn,wk[,ks]            streaming kernel: column tiles a wave, waves along columns, K slices, K split
 //   R9K_W4_TILED=on[,tn[,ks]]       tiled kernel: 0 never, 1 always; column tiles a wave, K split
 struct W4Tuning {
     int stream[4];  // 0: the planner's
     int tiled[3];   // -1: the planner's
 };
-const W4Tuning &w4_tuning();
+W4Tuning &w4_tuning();
 
 // ---- 4-bit weights (w4_weight.hip, gemm_w4.hip) ----
 // fmt: W4_INT or W4_MXFP4; grp: values a scale covers; the packed layout is in w4_device.h
@@ -49,6 +50,9 @@ struct W4Cfg {
 };
 double w4_expert_blocks(int64_t M, int64_t E, int64_t RB);  // row blocks that uniform routing makes
 W4Cfg w4_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu);
+bool w4_stream_shape(int nt, int wn, int wk);  // one that the streaming kernel has
+// segments in which a CTA's activation rows go through LDS; 0: slices loaded whole
+int w4_segments(const W4Cfg &c, int64_t K, int fmt, int grp);
 struct W4TiledCfg {
     bool on;     // false: the weight-streaming kernel takes the shape whatever the estimates
     int tn;      // column tiles a wave (4 waves along the columns)

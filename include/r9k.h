@@ -60,7 +60,7 @@ extern "C" {
 #pragma GCC visibility push(default)
 #endif
 
-#define R9K_ABI_VERSION 9
+#define R9K_ABI_VERSION 10
 
 /* Return codes: 0 or negative, as the pages' kernels return them (release
  * v0.3.0, its validation record: a test failing "with the kernel's -7").
@@ -77,7 +77,8 @@ extern "C" {
 /* The ABI version this library implements (R9K_ABI_VERSION; 4 added the MoE
  * routing and the shared-expert fold, 5 the bf16-activation variant, 6 the
  * mid-width kernel in the plan query, 7 the allocation-free GEMM entry point, 8 the tiled-plan
- * control and R9K_ENGINE_SPLITK, 9 the 4-bit weights and the rows sorted by expert).  Callers refuse
+ * control and R9K_ENGINE_SPLITK, 9 the 4-bit weights and the rows sorted by expert, 10 their plan
+ * query and control).  Callers refuse
  * a library whose version differs from the header they were built against:
  * the convention of the pages' plugin, which refuses an older libr9k.so
  * (release v0.2.2, "Upgrading").  Host only; cannot fail. */
@@ -474,6 +475,37 @@ int r9k_gemm_w4(const uint16_t *a, int64_t M, int64_t K, const uint8_t *wp, cons
 int r9k_moe_gemm_w4(const uint16_t *a, int64_t arows, const int32_t *src, int64_t topk, const int32_t *offsets,
                     int64_t E, int64_t R, int64_t K, const uint8_t *wp, const void *sp, const uint8_t *zp,
                     int format, int group, int64_t N, int act, uint16_t *c, void *stream);
+
+/* Which launch a 4-bit product takes (host only), as r9k_gemm_fp8_block_plan
+ * tells it of the fp8 products.  E = 0: r9k_gemm_w4 of M rows; E >= 1: r9k_moe_gemm_w4
+ * of R = M rows.  plan holds R9K_W4_PLAN_INTS values:
+ *   [0] the kernel: R9K_W4_STREAM (weights streamed into registers) or R9K_W4_TILED
+ *       (tiles staged through LDS); 0 for M = 0, and the rest too;
+ *   [1] column tiles of 16 a wave, [2] waves along the columns, [3] waves along K,
+ *   [4] CTAs along K (above 1: partial sums in the workspace, and a second launch);
+ *   [5] streaming kernel: segments in which a CTA's activation rows go through LDS, 0
+ *       where every wave loads its slice of the weight at once.
+ * Errors: NULLPTR; SHAPE as for the call; ARG for an unknown format, group or act, or
+ * an act with E = 0. */
+#define R9K_W4_AUTO 0
+#define R9K_W4_STREAM 1
+#define R9K_W4_TILED 2
+#define R9K_W4_PLAN_INTS 6
+int r9k_w4_plan(int64_t M, int64_t K, int64_t N, int64_t E, int act, int format, int group, int *plan);
+
+/* Plan control of the 4-bit products, for tuning and tests: later calls take this
+ * kernel (R9K_W4_AUTO with all else 0: the planner's choice), with `tiles` column tiles
+ * a wave, `waves` along the columns, `slices` waves along K and `ksplit` CTAs along K, 0
+ * for the planner's.  R9K_W4_STREAM takes the three of its shape together (1 1 4, 1 1 8,
+ * 1 2 2, 1 2 4, 1 4 2, or 2 and 1 2, 1 4, 1 8, 2 2, 2 4, 4 2; with silu always 2 tiles)
+ * and a split only with them; R9K_W4_TILED takes tiles of 1, 2 or 4 and its own four
+ * waves (waves = slices = 0).  Splits are clamped to K / 128 and dense; experts run one
+ * tile a wave on the streaming kernel.  The environment variables R9K_W4 (nt,wn,wk,ks)
+ * and R9K_W4_TILED (on,tn,ks) give the initial values.  The setting is process-wide,
+ * changes the workspace a shape needs (query again after a change), and must change only
+ * while no 4-bit product is being issued.
+ * Errors: ARG for an unknown kernel or a shape that it does not have. */
+int r9k_set_w4_plan(int kernel, int tiles, int waves, int slices, int ksplit);
 
 /* ------------------------------------------------------------------------ */
 /* Rows sorted by expert, and back                                           */

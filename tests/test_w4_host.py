@@ -390,3 +390,98 @@ def test_planning_does_not_grow_with_the_rows(L):
         return best
     for R, E in ((1 << 17, 1), (1 << 20, 1), (1 << 24, 2), ((1 << 31) - 1, 1), ((1 << 31) - 1, 2048)):
         assert us(R, E) < 4 * us(16, 1) + 10, (R, E)
+
+
+FORMS = [(INT, 32), (INT, 64), (INT, 128), (MX, 32)]
+
+
+@pytest.fixture
+def plans():
+    import block_scaled_fp8_r9k_amd as r9k
+    yield r9k
+    r9k.set_w4_plan()
+
+
+def test_plan_query_and_control_checks(L, plans):
+    out = (ctypes.c_int * 6)()
+    assert L.r9k_w4_plan(1, 128, 16, 0, 0, INT, 128, None) == -1
+    for M, K, N, E in ((-1, 128, 16, 0), (1, 100, 16, 0), (1, 128, 8, 0), (1, 128, 16, -1), (1, 128, 16, 2049)):
+        assert L.r9k_w4_plan(M, K, N, E, 0, INT, 128, out) == -2
+    assert L.r9k_w4_plan(1, 128, 16, 4, 1, INT, 128, out) == -2        # silu needs whole tiles in either half
+    for act, fmt, g in ((1, INT, 128), (2, INT, 128), (0, 2, 32), (0, INT, 16), (0, MX, 64)):
+        assert L.r9k_w4_plan(1, 128, 32, 0, act, fmt, g, out) == -7    # an act with a dense product, unknown ones
+    assert L.r9k_w4_plan(0, 128, 16, 0, 0, INT, 128, out) == 0 and list(out) == [0] * 6
+    for bad in ((3, 0, 0, 0, 0), (-1, 0, 0, 0, 0), (0, 1, 0, 0, 0), (0, 0, 0, 0, 2), (1, 1, 1, 1, 0), (1, 2, 0, 0, 0),
+                (1, 0, 0, 0, 2), (1, 3, 1, 4, 0), (2, 3, 0, 0, 0), (2, 2, 1, 0, 0), (2, 2, 0, 1, 0), (2, 2, 0, 0, -1)):
+        assert L.r9k_set_w4_plan(*bad) == -7, bad
+
+
+def test_control_is_followed_and_lifted(L, plans):
+    """A forced launch is the one planned, the workspace query follows it, and the planner's choice comes back; the
+    calls of one thread see a change at once."""
+    shape = (100, 4096, 4096)
+    auto, ws = plans.w4_plan(*shape, group=32), plans.gemm_w4_workspace(*shape)
+    plans.set_w4_plan(plans.W4_TILED, 4, 0, 0, 8)
+    assert plans.w4_plan(*shape, group=32) == (plans.W4_TILED, 4, 4, 1, 8, 0)
+    assert plans.gemm_w4_workspace(*shape) == 8 * 4 * 100 * 4096
+    assert plans.w4_plan(100, 256, 4096)[4] == 2                       # the split clamped to K / 128
+    assert plans.w4_plan(64, 4096, 4096, 8) == (plans.W4_TILED, 4, 4, 1, 1, 0)  # experts take none
+    plans.set_w4_plan(plans.W4_TILED, 1)
+    assert plans.w4_plan(64, 4096, 4096, 8)[0] == plans.W4_STREAM      # nor one tile a wave
+    plans.set_w4_plan(plans.W4_STREAM, 1, 2, 4, 3)
+    assert plans.w4_plan(*shape)[:5] == (plans.W4_STREAM, 1, 2, 4, 3)
+    assert plans.w4_plan(64, 4096, 4096, 8, "silu_mul")[:5] == (plans.W4_STREAM, 2, 2, 4, 1)
+    plans.set_w4_plan()
+    assert plans.w4_plan(*shape, group=32) == auto and plans.gemm_w4_workspace(*shape) == ws
+
+
+def test_forced_cases_reach_every_launch(plans):
+    """The cases that the GPU tests run, on the CPU: each is planned as it is forced, and together they reach every
+    instance of either kernel: one and two row tiles, one and two column tiles, slices loaded whole and streamed in
+    one and in several segments, with a split and without."""
+    from tests.w4_plans import STREAM_CASES, STREAM_EXPERTS, STREAM_SHAPES, TILED_CASES, TILED_EXPERT_COUNTS
+    every = {(mt, nt, seg) for mt in (1, 2) for nt in (1, 2) for seg in (0, 1, 2)}
+    for fmt, group in FORMS:
+        seen = set()
+        for M, K, N, ks in STREAM_CASES:
+            for sh in STREAM_SHAPES:
+                plans.set_w4_plan(plans.W4_STREAM, *sh, ks)
+                p = plans.w4_plan(M, K, N, fmt=fmt, group=group)
+                assert p[:3] == (plans.W4_STREAM, *sh[:2]) and p[4] == ks, (M, K, N, sh, p)
+                seen.add((1 if M <= 16 else 2, p[1], min(p[5], 2), ks > 1))
+        assert seen == {(*x, split) for x in every for split in (False, True)}
+        for act in ("none", "silu_mul"):
+            seen = set()
+            for counts, K, N, topk in STREAM_EXPERTS:
+                R = -(-(sum(counts) + 2) // topk) * topk
+                for sh in STREAM_SHAPES:
+                    if act == "none" or sh[0] == 2:
+                        plans.set_w4_plan(plans.W4_STREAM, *sh)
+                        p = plans.w4_plan(R, K, N, len(counts), act, fmt, group)
+                        assert p[:3] == (plans.W4_STREAM, *sh[:2])
+                        seen.add((1 if R <= 12 * len(counts) else 2, p[1], min(p[5], 2)))
+            assert seen == {x for x in every if act == "none" or x[1] == 2}
+        live = set()
+        for M, K, N, splits in TILED_CASES:
+            live.add((min(M, 64) + 15) // 16)
+            for tn in (1, 2, 4):
+                for ks in splits:
+                    plans.set_w4_plan(plans.W4_TILED, tn, 0, 0, ks)
+                    assert plans.w4_plan(M, K, N, fmt=fmt, group=group) == (plans.W4_TILED, tn, 4, 1, ks, 0)
+        assert live == {1, 2, 3, 4}
+    assert {(min(c, 64) + 15) // 16 for c in TILED_EXPERT_COUNTS} == {0, 1, 2, 3, 4}
+
+
+def test_planned_launches(plans):
+    """The kernel and the shape that the planner picks for sizes in use: a change of its constants shows here."""
+    S, T = plans.W4_STREAM, plans.W4_TILED
+    for args, kw, want in (
+            ((1, 512, 1024), {}, (S, 1, 1, 4, 1, 0)),
+            ((1, 4096, 14336), {}, (S, 1, 1, 4, 1, 0)),
+            ((16, 14336, 4096), dict(fmt=MX, group=32), (S, 1, 4, 2, 4, 1)),
+            ((100, 4096, 4096), dict(group=32), (T, 2, 4, 1, 4, 0)),
+            ((4096, 4096, 12288), {}, (T, 4, 4, 1, 1, 0)),
+            ((33, 14336, 2048), {}, (T, 1, 4, 1, 8, 0)),
+            ((128, 2048, 1536, 128, "silu_mul"), {}, (S, 2, 4, 2, 1, 1)),
+            ((16384, 768, 2048, 128), dict(fmt=MX, group=32), (T, 4, 4, 1, 1, 0))):
+        assert plans.w4_plan(*args, **kw) == want, (args, kw, plans.w4_plan(*args, **kw))
