@@ -40,7 +40,8 @@ __global__ __launch_bounds__(256) void k_quant_weight_w4(const uint16_t *__restr
     const int64_t g = id * 8 / grp;
     uint32_t code[8];
     if (FMT == W4_INT) {
-        const float num = z_out ? fmaxf(hi - lo, 1e-10f) / 15.0f : fmaxf(amax, 1e-10f) / 7.0f;
+        // (the range of the halves: hi - lo may pass fp32's largest value)
+        const float num = z_out ? fmaxf(0.5f * hi - 0.5f * lo, 0.5e-10f) / 15.0f * 2.0f : fmaxf(amax, 1e-10f) / 7.0f;
         const uint32_t sb = bf16_rne(num);
         const float s = __uint_as_float(sb << 16);
         const float z = z_out ? fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f) : 8.0f;

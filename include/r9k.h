@@ -410,7 +410,8 @@ int r9k_moe_ws_offset(int64_t T, int64_t H, int64_t E, int64_t I, int64_t topk, 
 /* Group quantisation of bf16 weights at load time, in fp32, ties to even:
  *   R9K_W4_INT, z NULL:  s = bf16(max(amax, 1e-10f) / 7), q = clamp(rint(w / s) + 8, 0, 15);
  *   R9K_W4_INT, z given: lo = min(0, min w), hi = max(0, max w),
- *                        s = bf16(max(hi - lo, 1e-10f) / 15), z = clamp(rint(-lo / s), 0, 15),
+ *                        s = bf16(max(hi - lo, 1e-10f) / 15), also where hi - lo passes fp32's
+ *                        largest value, z = clamp(rint(-lo / s), 0, 15),
  *                        q = clamp(rint(w / s) + z, 0, 15);
  *   R9K_W4_MXFP4:        s = clamp(exponent field of amax - 2, 1, 254),
  *                        q = e2m1(w / 2^(s - 127)), ties to the even code, saturating.

@@ -1,4 +1,5 @@
 """4-bit weights at the ends of their formats' ranges: scale bytes, infinities and NaN."""
+import numpy as np
 import pytest
 import torch
 
@@ -58,3 +59,29 @@ def test_mxfp4_byte_255_is_nan(r9k, M):
     keep = torch.ones(N, dtype=torch.bool)
     keep[[5, 16]] = False
     assert torch.all(torch.isnan(got.cpu()[:, ~keep])) and torch.equal(got.cpu()[:, keep], fine.cpu()[:, keep])
+
+
+def test_quantiser_at_the_widest_ranges(r9k):
+    """Groups that reach from one end of bf16 to the other: hi - lo passes fp32's largest value, the scale does not.
+    Bit for bit the rule, with the difference taken of the halves (a power of two: exact)."""
+    say("quant_weight_w4 wide")
+    top = torch.finfo(torch.bfloat16).max
+    w = (torch.rand((16, 256), generator=torch.Generator().manual_seed(3)) * 2 - 1)
+    w = (w * torch.linspace(0.4, 1, 16)[:, None] * top).to(torch.bfloat16)
+    w[0, 0], w[0, 1], w[1] = top, -top, 0
+    for group in (32, 64, 128):
+        q, s, z = r9k.quant_weight_w4(w.cuda(), group, r9k.W4_INT, True)
+        g = w.float().numpy().reshape(16, -1, group)
+        f32 = np.float32
+        lo, hi = np.minimum(g.min(2), f32(0)), np.maximum(g.max(2), f32(0))
+        want_s = torch.from_numpy(np.maximum(hi * f32(0.5) - lo * f32(0.5), f32(0.5e-10)) / f32(15) * f32(2)).to(torch.bfloat16)
+        ss = want_s.float().numpy()
+        want_z = np.clip(np.rint(-lo / ss), 0, 15)
+        want_q = np.clip(np.rint(g / ss[..., None]) + want_z[..., None], 0, 15).reshape(16, -1)
+        assert torch.equal(s.cpu(), want_s)
+        assert np.array_equal(z.cpu().numpy(), want_z) and np.array_equal(ref.codes_of(q).numpy(), want_q)
+        value, _ = ref.dequant(q, s, z, group)
+        # half a step of rounding, half of the zero point's, and the codes that the range's ends are clamped to
+        # (the scale's own rounding, 2^-8 of 15 steps)
+        step = s.cpu().to(ref.F64).repeat_interleave(group, 1)
+        assert torch.all((value - w.to(ref.F64)).abs() <= (1 + 15 * 2.0 ** -8) * step)
