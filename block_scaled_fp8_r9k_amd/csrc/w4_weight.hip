@@ -13,6 +13,7 @@ namespace r9k {
 //          q = clamp(rint(w / s) + z, 0, 15)
 //   mxfp4  e = clamp(exponent of amax - 2, 2^-126 .. 2^127) biased by 127 in a byte,
 //          q = e2m1(w / 2^e), ties to the even code, saturating at 6
+// A group with an infinity or a NaN takes the scale NaN (255 in mxfp4), so that it shows.
 // fp32 arithmetic, ties to even in rint; s is bf16 because that is how 4-bit
 // checkpoints hold it, and the codes are taken against the rounded s.
 template <int FMT>
@@ -25,24 +26,28 @@ __global__ __launch_bounds__(256) void k_quant_weight_w4(const uint16_t *__restr
     const float f[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
                         bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
     float lo = 0.0f, hi = 0.0f;  // the range always holds 0
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         lo = fminf(lo, f[i]);
         hi = fmaxf(hi, f[i]);
+        bad |= (__float_as_uint(f[i]) & 0x7F800000u) == 0x7F800000u;
     }
+    if (bad) hi = __uint_as_float(0x7F800000u);  // fmaxf passes over a NaN
     const int lanes = grp / 8;  // 4, 8 or 16
     for (int d = 1; d < lanes; d <<= 1) {
         lo = fminf(lo, __shfl_xor(lo, d, 64));
         hi = fmaxf(hi, __shfl_xor(hi, d, 64));
     }
     const float amax = fmaxf(-lo, hi);
+    bad = amax == __uint_as_float(0x7F800000u);  // any of the group
     const bool first = live && (threadIdx.x & (lanes - 1)) == 0;
     const int64_t g = id * 8 / grp;
     uint32_t code[8];
     if (FMT == W4_INT) {
         // (the range of the halves: hi - lo may pass fp32's largest value)
         const float num = z_out ? fmaxf(0.5f * hi - 0.5f * lo, 0.5e-10f) / 15.0f * 2.0f : fmaxf(amax, 1e-10f) / 7.0f;
-        const uint32_t sb = bf16_rne(num);
+        const uint32_t sb = bad ? 0x7FC0u : bf16_rne(num);
         const float s = __uint_as_float(sb << 16);
         const float z = z_out ? fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f) : 8.0f;
         if (first) {
@@ -53,7 +58,7 @@ __global__ __launch_bounds__(256) void k_quant_weight_w4(const uint16_t *__restr
         for (int i = 0; i < 8; ++i) code[i] = (uint32_t)fminf(fmaxf(rintf(f[i] / s) + z, 0.0f), 15.0f);
     } else {
         const int ex = (int)(__float_as_uint(amax) >> 23);  // biased exponent; 0 for zero and subnormals
-        const int e = min(max(ex - 2, 1), 254);
+        const int e = bad ? 255 : min(max(ex - 2, 1), 254);
         if (first) ((uint8_t *)s_out)[g] = (uint8_t)e;
         // 2^(127 - e) as two factors, each a normal number
         const float r1 = __uint_as_float((uint32_t)(127 + (127 - e) / 2) << 23);

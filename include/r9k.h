@@ -415,6 +415,7 @@ int r9k_moe_ws_offset(int64_t T, int64_t H, int64_t E, int64_t I, int64_t topk, 
  *                        q = clamp(rint(w / s) + z, 0, 15);
  *   R9K_W4_MXFP4:        s = clamp(exponent field of amax - 2, 1, 254),
  *                        q = e2m1(w / 2^(s - 127)), ties to the even code, saturating.
+ * A group that holds an infinity or a NaN gets the scale NaN (255 with R9K_W4_MXFP4).
  *   w [N][K] bf16 -> wq, s, z as above.
  * Errors: NULLPTR; SHAPE if N is not a positive multiple of 16 or K of 128, or N * K is 2^35 or more; ARG for
  * an unknown format, a group the format does not have, zeros with R9K_W4_MXFP4, or an overlap;

@@ -85,3 +85,38 @@ def test_quantiser_at_the_widest_ranges(r9k):
         # (the scale's own rounding, 2^-8 of 15 steps)
         step = s.cpu().to(ref.F64).repeat_interleave(group, 1)
         assert torch.all((value - w.to(ref.F64)).abs() <= (1 + 15 * 2.0 ** -8) * step)
+
+
+@pytest.mark.parametrize("fmt,group,zeros", [("int4", 32, False), ("int4", 64, True), ("int4", 128, True), ("mxfp4", 32, False)])
+def test_quantiser_keeps_what_is_not_finite(r9k, fmt, group, zeros):
+    """A group with an infinity or a NaN has no finite value; every other group is to the bit what it is without it;
+    and the product's columns show both."""
+    say("quant_weight_w4 non-finite", fmt, group, zeros)
+    N, K = 48, 512
+    code = r9k.W4_INT if fmt == "int4" else r9k.W4_MXFP4
+    w = (torch.randn((N, K), generator=torch.Generator().manual_seed(group)) * 0.02).to(torch.bfloat16)
+    bad = w.clone()
+    where = [(0, 0, float("nan")), (5, K - 1, float("inf")), (6, 100, -float("inf")), (47, 300, float("nan"))]
+    for n, k, v in where:
+        bad[n, k] = v
+    fine, got = r9k.quant_weight_w4(w.cuda(), group, code, zeros), r9k.quant_weight_w4(bad.cuda(), group, code, zeros)
+    groups = torch.zeros((N, K // group), dtype=torch.bool)
+    for n, k, _ in where:
+        groups[n, k // group] = True
+    s = got[1].cpu()
+    assert torch.equal(s == 255 if fmt == "mxfp4" else torch.isnan(s), groups)
+    assert torch.equal(s[~groups], fine[1].cpu()[~groups])
+    each = groups.repeat_interleave(group, 1)
+    assert torch.equal(ref.codes_of(got[0])[~each], ref.codes_of(fine[0])[~each])
+    if zeros:
+        assert torch.equal(got[2].cpu()[~groups], fine[2].cpu()[~groups])
+    rows = groups.any(1)
+    for M in (3, 90):
+        a = torch.randn((M, K), generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).cuda()
+        for plan in ((), (r9k.W4_TILED, 1), (r9k.W4_TILED, 4)):
+            r9k.set_w4_plan(*plan)
+            try:
+                c, d = r9k.gemm_w4(a, *r9k.pack_weight_w4(*fine)).cpu(), r9k.gemm_w4(a, *r9k.pack_weight_w4(*got)).cpu()
+            finally:
+                r9k.set_w4_plan()
+            assert torch.all(torch.isnan(d[:, rows])) and torch.equal(d[:, ~rows], c[:, ~rows])
