@@ -655,6 +655,7 @@ def moe_permute(x, topk_ids, E: int, xs=None, src=None, pos=None, offsets=None, 
     dev = _dev(topk_ids, "topk_ids")
     T, topk = topk_ids.shape
     R = T * topk
+    need = moe_permute_workspace(T, E, topk)  # refuses counts that no output could be made for
     pi = _addr(topk_ids, I32, "topk_ids", dev)
     px = pxs = None
     H = dt = 0
@@ -686,7 +687,7 @@ def moe_permute(x, topk_ids, E: int, xs=None, src=None, pos=None, offsets=None, 
     if T == 0:  # no slots (empty tensors have no device address to pass): the call sees only the offsets
         px = pxs = None
         pi = psrc = ppos = poff
-    pw, nb, _keep = _scratch(workspace, moe_permute_workspace(T, E, topk), dev, stream)
+    pw, nb, _keep = _scratch(workspace, need, dev, stream)
     rc = lib().r9k_moe_permute(px, dt, T, H, pi, topk, E, pxs, psrc, ppos, poff, pw, nb, _raw(stream, dev))
     if rc:
         _check(rc, "r9k_moe_permute")

@@ -485,3 +485,20 @@ def test_planned_launches(plans):
             ((128, 2048, 1536, 128, "silu_mul"), {}, (S, 2, 4, 2, 1, 1)),
             ((16384, 768, 2048, 128), dict(fmt=MX, group=32), (T, 4, 4, 1, 1, 0))):
         assert plans.w4_plan(*args, **kw) == want, (args, kw, plans.w4_plan(*args, **kw))
+
+
+@pytest.fixture
+def on_host(monkeypatch):
+    """The binding with host tensors let through its device check, and no call that reaches the library's launches."""
+    import block_scaled_fp8_r9k_amd as r9k
+    monkeypatch.setattr(r9k, "_dev", lambda t, name: -1)
+    monkeypatch.setattr(r9k, "_raw", lambda stream, dev: 0)
+    return r9k
+
+
+def test_permute_refuses_expert_counts_before_it_allocates(on_host):
+    import torch
+    for E in (0, -1, -5, 2049, 1 << 40):
+        with pytest.raises(on_host.R9kError) as e:
+            on_host.moe_permute(None, torch.zeros((2, 2), dtype=torch.int32), E)
+        assert e.value.code == -2, E
