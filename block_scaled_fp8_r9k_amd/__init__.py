@@ -508,7 +508,7 @@ def _w4_format(wp, sp, zp, dev: int, dims: int = 0):
         raise ValueError(f"scales {tuple(ss)} do not go with 4-bit codes {tuple(ws)}"
                          + (f" of {dims} sizes" if dims else ""))
     K, groups = 2 * ws[-1], ss[-1]
-    if not groups or K % groups:
+    if not K or not groups or K % groups:
         raise ValueError(f"{groups} scales a row do not divide K = {K}")
     return (_addr(wp, U8, "codes", dev), _addr(sp, _W4_SCALES, "scales", dev),
             None if zp is None else _addr(zp, U8, "zeros", dev, ss), _W4_SCALES[sp.dtype], K, K // groups)
@@ -519,7 +519,7 @@ def quant_weight_w4(w: torch.Tensor, group: int = 128, fmt: int = W4_INT, zeros:
     W4_INT: scales bf16, zero points u8 when `zeros` (else 8 is meant); W4_MXFP4: group 32, scales u8 (e8m0)."""
     dev = _dev(w, "w")
     K, rows = w.shape[-1], w.numel() // max(w.shape[-1], 1)
-    if group <= 0 or K % group:
+    if not K or group <= 0 or K % group:
         raise ValueError(f"K = {K} is not whole groups of {group}")
     lead = w.shape[:-1]
     wq = _new((*lead, K // 2), torch.uint8, dev, stream)

@@ -502,3 +502,19 @@ def test_permute_refuses_expert_counts_before_it_allocates(on_host):
         with pytest.raises(on_host.R9kError) as e:
             on_host.moe_permute(None, torch.zeros((2, 2), dtype=torch.int32), E)
         assert e.value.code == -2, E
+
+
+def test_weights_without_columns_are_refused(on_host):
+    """Codes of no columns with scales of some: a refusal of their shape, in every call that takes a weight."""
+    import torch
+    bf, u8 = torch.bfloat16, torch.uint8
+    for lead in ((16,), (2, 16)):
+        wq, s = torch.zeros((*lead, 0), dtype=u8), torch.zeros((*lead, 2), dtype=bf)
+        with pytest.raises(ValueError, match="K = 0"):
+            on_host.pack_weight_w4(wq, s)
+    with pytest.raises(ValueError, match="K = 0"):
+        on_host.gemm_w4(torch.zeros((1, 0), dtype=bf), torch.zeros((16, 0), dtype=u8), torch.zeros((16, 2), dtype=bf))
+    with pytest.raises(ValueError, match="K = 0"):
+        on_host.moe_gemm_w4(torch.zeros((1, 0), dtype=bf), torch.zeros(3, dtype=torch.int32), wq, s)
+    with pytest.raises(ValueError, match="K = 0"):
+        on_host.quant_weight_w4(torch.zeros((16, 0), dtype=bf))
