@@ -740,8 +740,10 @@ def moe_unpermute(y, pos, w=None, out=None, stream=None) -> torch.Tensor:
 
 def moe_unpermute_backward(gout, y, pos, w, gy=None, gw=None, stream=None):
     """Gradient of moe_unpermute: gout [T,H], y [T*topk,H], pos and w [T,topk] -> (gy [T*topk,H], gw [T,topk] fp32).
-    Rows of gy that no slot fills are not written."""
+    Rows of gy that no slot fills are not written.  The gradient of moe_unpermute without weights takes ones."""
     dev = _dev(y, "y")
+    if w is None:
+        raise TypeError("w: the weights are needed (ones for a moe_unpermute without them)")
     T, topk, H, ppos, py = _sorted_rows(y, pos, dev, "y")
     pg = _addr(gout, (y.dtype,), "gout", dev, (T, H))
     pw = _addr(w, F32, "w", dev, (T, topk))

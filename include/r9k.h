@@ -446,7 +446,8 @@ int r9k_gemm_w4_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes);
  * exactly: products, group sums and their scaling are fp32.
  *   a [M][K] bf16 -> c [M][N] bf16.
  * An infinity or NaN among a row's activations leaves that row of c without a
- * finite value (NaN in places where the formula has an infinity) and no other row.
+ * finite value (NaN in places where the formula has an infinity) and no other row; with
+ * R9K_W4_INT so does a group whose sum of a * q or z * a passes fp32's largest value.
  * Errors: NULLPTR (a, wp, sp, c, or a workspace where one is needed); SHAPE if
  * M < 0, K is not a positive multiple of 128 or N of 16; ARG for an unknown
  * format, a group the format does not have, zeros with R9K_W4_MXFP4, or an overlap; ALIGN;
@@ -561,7 +562,8 @@ int r9k_moe_unpermute(const void *y, int dtype, int64_t T, int64_t H, const int3
  *   as they were), gw[t][j] = sum_h gout[t][h] * y[pos[t][j]][h] in fp32, 0 for a
  *   dropped slot.
  *   gout [T][H], y [T*topk][H], pos, w as above -> gy [T*topk][H], gw [T][topk] fp32.
- * The kept slots' positions are distinct, as r9k_moe_permute writes them.
+ * The kept slots' positions are distinct, as r9k_moe_permute writes them.  w is needed:
+ * ones for the gradient of r9k_moe_unpermute with w NULL.
  * Errors: as r9k_moe_unpermute. */
 int r9k_moe_unpermute_backward(const void *gout, const void *y, int dtype, int64_t T, int64_t H, const int32_t *pos,
                                const float *w, int64_t topk, void *gy, float *gw, void *stream);

@@ -518,3 +518,11 @@ def test_weights_without_columns_are_refused(on_host):
         on_host.moe_gemm_w4(torch.zeros((1, 0), dtype=bf), torch.zeros(3, dtype=torch.int32), wq, s)
     with pytest.raises(ValueError, match="K = 0"):
         on_host.quant_weight_w4(torch.zeros((16, 0), dtype=bf))
+
+
+def test_unpermute_backward_without_weights_is_refused(on_host):
+    """moe_unpermute takes no weights to mean 1; its gradient has a result for them and needs them."""
+    import torch
+    y, pos, g = torch.zeros((4, 64)), torch.zeros((2, 2), dtype=torch.int32), torch.zeros((2, 64))
+    with pytest.raises(TypeError, match="w: .*ones"):
+        on_host.moe_unpermute_backward(g, y, pos, None)
