@@ -18,11 +18,12 @@
 // their sums are added through LDS in ascending order.
 //
 // Bound by the packed weights' bytes, each read once (per 16 or 32 rows), and below a few
-// MB by launch and latency: one row of 4096 x 14336 in int4 (groups of 128, zeros) 9.9 us
-// (3.1 TB/s, 70 vector instructions a chunk and wave beside the loads; a plain read of as
-// many bytes takes 6.0 us, with as many instructions 7.8), 16 rows of 14336 x 4096 in
-// mxfp4 14 us (2.3 TB/s, the reduce launch 4 of them), 16 tokens' top 8 of 128 experts,
-// 2048 -> 2 x 768 in int4, 34 us (4.0 TB/s).  K slices inside a CTA fill the chip where
+// MB by launch and latency.  In graphs, weights from memory: one row of 4096 x 14336 in
+// int4 (groups of 128, zeros) 9.9 us (3.1 TB/s, 70 vector instructions a chunk and wave
+// beside the loads; a plain read of as many bytes takes 6.0 us, with as many instructions
+// 7.8; weights in the caches 8.1), in groups of 64 11.1, of 32 13.8, in mxfp4 8.3; 16 rows
+// of 14336 x 4096 in mxfp4 13.6 us (2.3 TB/s, the reduce launch 4 of them); 16 tokens' top 8
+// of 128 experts, 2048 -> 2 x 768 in int4, 34 us (3.9 TB/s).  K slices inside a CTA fill the chip where
 // there are few columns without partials in memory; a persistent loop over tiles was
 // slower than a CTA a tile (its prologue hides behind other CTAs' streams).
 //
@@ -330,9 +331,12 @@ __global__ __launch_bounds__(512) void k_gemm_w4(W4Args p) {
 // split adds its partials and the reduce launch.  Fitted to 30 dense shapes (M = 1, 4, 16; K
 // and N from 1024 to 14336, int4 in groups of 128 with zeros), 10 launches each, in graphs with
 // the weights out of the caches: the launch it picks takes 1% longer than the fastest of the
-// ten on average (at most 8%).  Experts, whose turns begin with the search for their rows
+// ten on average (at most 8%).  Groups of 32, of which a wave loads half as many chunks
+// ahead, were not fitted: over 12 other shapes 11% behind the fastest (at most 40%: 16 rows of
+// 4096 x 4096 11.2 us, eight slices 8.0), the other formats within 1% (5%).  Experts, whose turns begin with the search for their rows
 // and whose bytes hide behind other CTAs' starts: 15 shapes (8 to 128 experts, up to 8 rows each, int4 and mxfp4,
-// 128 to 1536 wide), 11 launches each, 1% (at most 11%).
+// 128 to 1536 wide), 11 launches each, 1% (at most 11%); over 48 other shapes, up to 8 rows an
+// expert in every format, 9% (at most 47%: 64 rows of 8 experts, 4096 -> 2 x 1024).
 // E.g. one row of 4096 x 4096 5.1 us with four slices of one tile a wave, 5.6 with eight;
 // 16 rows of 14336 x 4096 16 us in the split it picks, 25 in one.  Up to 400 rows it
 // also decides against the tiled kernel (figures there).

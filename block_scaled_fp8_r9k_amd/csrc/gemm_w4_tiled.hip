@@ -19,12 +19,12 @@
 //   row tile w (an MFMA with ones for weights) and leaves them, split, in LDS.
 //   mxfp4: the scale is in the converted fragment (a power of two, exact) and the
 //   matrix instruction accumulates through all of K.
-// What bounds it, 4096 x 4096 x 12288: int4 in groups of 128 with zeros 414 us (996
-// TFLOP/s; a bf16 library product 328 us) with the matrix cores busy 44% of the cycles and
-// the vector units 51%: decoding is 7 instructions for 8 codes once per four row tiles,
+// What bounds it, 4096 x 4096 x 12288: int4 in groups of 128 with zeros 412-444 us by the
+// card's clock (928 to 1000 TFLOP/s; a bf16 library product 328 us) with the matrix cores
+// busy 44% of the cycles and the vector units 50%: decoding is 7 instructions for 8 codes once per four row tiles,
 // promotion 4 for every 16 x 16 x 128, and a 16 x 16 x 32 MFMA hides two vector
-// instructions.  Groups of 64 477 us, of 32 591 (the promotions double and quadruple);
-// mxfp4, with nothing to promote, 305 us (1350 TFLOP/s).  Measured and not taken:
+// instructions.  Where that takes 444 us, groups of 64 take 484, of 32 608 (the promotions
+// double and quadruple); mxfp4, with nothing to promote, 322 us (1283 TFLOP/s).  Measured and not taken:
 // 32 x 32 x 16 MFMA (492 us: two product chains a wave instead of sixteen), 128 rows a CTA
 // (its registers leave one CTA a compute unit), the zero points' sums in a launch of their own.
 // A rows are 256 bytes in LDS; 16-byte piece p of row r lies at piece p ^ (r % 16),
@@ -420,7 +420,9 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_gemm_w4_tiled(W4Args p) {
 // tiles, 514 with 2.
 // The streaming kernel takes what it is estimated to do sooner, always up to 32 rows.  Both
 // timed on 90 shapes (33 to 400 rows dense, 3 to 250 rows an expert, 8 to 128 experts), the
-// pick was 2% behind the faster on average, 17% at most.  E.g. (streaming, tiled; us)
+// pick was 2% behind the faster on average, 17% at most; against every launch of both, over 96
+// dense shapes of 33 to 400 rows in every format 3% (at most 25%), over 64 of 16 to 128 rows an
+// expert 4% (at most 46%).  E.g. (streaming, tiled; us)
 //   64 rows, int4      1024 x 4096  5.7, 9.6   4096 x 4096  13.7, 14.6   4096 x 14336  24.1, 23.8
 //   400 rows, int4     1024 x 4096  11.6, 12.5  4096 x 4096  43.6, 31.7
 //   2048 -> 2 x 768 of 128 experts, int4, rows an expert   8: 50, 58   16: 82, 62   32: 120, 70

@@ -10,8 +10,8 @@
 // All of it is bound by the rows' bytes: each token row is read once, each sorted
 // row read or written once, in 16-byte pieces.  A large copy reaches 4.99 TB/s here
 // (reads from the caches count on top).  Rows of 2048 bf16, 8192 tokens, top 8 of 128:
-// permute 63 us (4.8 TB/s: 46 us of rows behind 13 us of sorting), unpermute 46 us (6.6
-// TB/s), its gradient 114 us (5.0 TB/s); 4096 rows of 4096 fp32, top 2: 42, 31 and 61 us
+// permute 63 us (4.8 TB/s; with a quarter of the slots dropped 59 us, 46 of them for the
+// rows behind 13 of sorting), unpermute 46 us (6.6 TB/s), its gradient 114 us (5.0 TB/s); 4096 rows of 4096 fp32, top 2: 42, 31 and 61 us
 // (4.8, 6.5, 5.5 TB/s).  16 tokens: 3.6, 3.3 and 6.6 us, a launch and the loads' latencies.
 #include <algorithm>
 
