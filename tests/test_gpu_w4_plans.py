@@ -245,3 +245,46 @@ def test_forced_plans_in_graphs(r9k):
             r9k.gemm_w4(a, *p)
         torch.cuda.synchronize()
         assert all(torch.equal(out, eager) for _, out, eager in graphs)
+
+
+@pytest.mark.parametrize("kernel,shape,split", [("tiled", (4, 0, 0), 1), ("stream", (1, 4, 2), 1), ("tiled", (2, 0, 0), 2),
+                                                ("stream", (1, 1, 4), 2)])
+@pytest.mark.parametrize("M,K,N", [(140000, 256, 16400), (140000, 16384, 16)])
+def test_far_dense_rows(r9k, kernel, shape, split, M, K, N):
+    """Outputs, partial sums or activations past 4 GiB: rows from either end and the middle, the columns' ends."""
+    say("far dense", kernel, shape, split, M, K, N)
+    w = weight((N,), K, "int4", 128, True, 7)
+    p = packed(r9k, w)
+    a = torch.randn((M, K), generator=torch.Generator(device="cuda").manual_seed(M + K), device="cuda", dtype=torch.bfloat16)
+    with forced(r9k, r9k.W4_TILED if kernel == "tiled" else r9k.W4_STREAM, *shape, split):
+        assert r9k.w4_plan(M, K, N)[4] == split
+        c = r9k.gemm_w4(a, *p)
+    rows = torch.tensor([0, 1, 31, 64, 65535, 65536, 131071, 131072, M - 65, M - 17, M - 1])
+    cols = torch.unique(torch.cat((torch.arange(0, 16), torch.arange(N - 16, N))))
+    want, before = ref.product(a[rows.cuda()], *(t[cols] for t in w), 128)
+    got = c[rows.cuda()][:, cols.cuda()].cpu().to(ref.F64)
+    assert torch.all((got - want).abs() <= ref.bf16_bound(want, before))
+
+
+def test_two_threads_on_two_streams(r9k):
+    """Two threads call products of their own shapes, formats and streams at the same time: each result is to the bit
+    what it is alone."""
+    import threading
+    say("two threads")
+    jobs = []
+    for i, (M, K, N, fmt, group, zeros) in enumerate([(3, 4096, 512, "int4", 64, True), (150, 1024, 1040, "mxfp4", 32, False)]):
+        p, a = packed(r9k, weight((N,), K, fmt, group, zeros, i)), acts(M, K, i).cuda()
+        jobs.append((a, p, r9k.gemm_w4(a, *p), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(a, p, want, stream):
+        outs = [r9k.gemm_w4(a, *p, stream=stream) for _ in range(50)]
+        stream.synchronize()
+        wrong.extend(1 for c in outs if not torch.equal(c, want))
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not wrong and not any(t.is_alive() for t in threads)
