@@ -13,6 +13,7 @@ Tensor conventions (all contiguous, on the current CUDA/HIP device):
   scales, weights  torch.float32;  expert ids torch.int32
   4-bit weights    torch.uint8, two codes to a byte; their scales torch.bfloat16
                    (int4) or torch.uint8 (mxfp4), their zero points torch.uint8
+  8-bit integers   torch.int8; a float32 scale per row (token or output channel)
 """
 from __future__ import annotations
 
@@ -23,7 +24,7 @@ from ctypes import POINTER, c_char_p, c_int, c_int64, c_size_t, c_void_p
 
 import torch
 
-ABI_VERSION = 10
+ABI_VERSION = 11
 ENGINE_AUTO, ENGINE_SKINNY, ENGINE_TILED, ENGINE_SPLITK = 0, 1, 2, 3
 TILE_AUTO, TILE_256X256, TILE_256X128, TILE_128X64, TILE_256X64 = 0, 1, 2, 3, 4
 
@@ -96,6 +97,18 @@ def lib() -> ctypes.CDLL:
                                         c_void_p]
         L.r9k_moe_unpermute_backward.argtypes = [c_void_p, c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p,
                                                  c_int64, c_void_p, c_void_p, c_void_p]
+        L.r9k_quant_i8.argtypes = [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p]
+        L.r9k_pack_weight_i8.argtypes = [c_void_p, c_int64, c_int64, c_void_p, c_void_p]
+        L.r9k_gemm_i8_workspace.argtypes = [c_int64, c_int64, c_int64, POINTER(c_size_t)]
+        L.r9k_gemm_i8.argtypes = L.r9k_gemm_fp8_block.argtypes
+        L.r9k_gemm_i8_qa.argtypes = L.r9k_gemm_fp8_block_qa.argtypes
+        L.r9k_moe_gemm_i8.argtypes = [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64,
+                                      c_void_p, c_void_p, c_int64, c_int, c_void_p, c_void_p]
+        L.r9k_moe_balance_loss_workspace.argtypes = [c_int64, c_int64, c_int64, POINTER(c_size_t)]
+        L.r9k_moe_balance_loss.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int64] + [c_void_p] * 5 + [
+            c_size_t, c_void_p]
+        L.r9k_moe_balance_loss_backward.argtypes = [c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64] + [c_void_p] * 7
+        L.r9k_moe_route_backward.argtypes = [c_void_p] * 3 + [c_int64] * 3 + [c_void_p] * 2
         v = L.r9k_abi_version()
         if v != ABI_VERSION:
             raise ImportError(f"libr9k.so has ABI version {v}, this binding needs {ABI_VERSION}")
@@ -755,3 +768,202 @@ def moe_unpermute_backward(gout, y, pos, w, gy=None, gw=None, stream=None):
         if rc:
             _check(rc, "r9k_moe_unpermute_backward")
     return gy, gw
+
+
+# ------------------------------------------ products in 8-bit integers ----
+
+I8 = (torch.int8,)
+
+
+def quant_i8(x: torch.Tensor, q=None, s=None, stream=None):
+    """Rows to signed bytes with a scale each (r9k_quant_i8): x [..., K] bf16 -> (codes [..., K] int8, scales [...] fp32).
+    Activations per token; a weight [..., N, K] per output channel, at load time."""
+    dev = _dev(x, "x")
+    px = _addr(x, BF16, "x", dev)
+    if x.dim() < 1:
+        raise ValueError("x has no rows")
+    if q is None:
+        q = _new(x.shape, torch.int8, dev, stream)
+    if s is None:
+        s = _new(x.shape[:-1], torch.float32, dev, stream)
+    pq, ps = _addr(q, I8, "q", dev, x.shape), _addr(s, F32, "s", dev, x.shape[:-1])
+    if s.numel():
+        rc = lib().r9k_quant_i8(px, s.numel(), x.shape[-1], pq, ps, _raw(stream, dev))
+        if rc:
+            _check(rc, "r9k_quant_i8")
+    return q, s
+
+
+def pack_weight_i8(wq: torch.Tensor, stream=None) -> torch.Tensor:
+    """The packed copy that the products read (r9k_pack_weight_i8): codes [..., N, K] int8 -> the same shape.  Experts'
+    weights [E, N, K] pack as one.  Once, at load time; the scales stay as they are."""
+    dev = _dev(wq, "wq")
+    if wq.dim() < 2 or wq.shape[-2] % 16 or not wq.numel():
+        raise ValueError(f"wq: shape {tuple(wq.shape)}; its rows must be a multiple of 16")
+    p = _addr(wq, I8, "wq", dev)
+    wp = _new(wq.shape, torch.int8, dev, stream)
+    K = wq.shape[-1]
+    _check(lib().r9k_pack_weight_i8(p, wq.numel() // K, K, wp.data_ptr(), _raw(stream, dev)), "r9k_pack_weight_i8")
+    return wp
+
+
+@functools.lru_cache(maxsize=4096)
+def gemm_i8_workspace(M: int, K: int, N: int) -> int:
+    """Workspace bytes for gemm_i8 and gemm_i8_qa of this shape (r9k_gemm_i8_workspace)."""
+    b = c_size_t(0)
+    _check(lib().r9k_gemm_i8_workspace(M, K, N, ctypes.byref(b)), "r9k_gemm_i8_workspace")
+    return b.value
+
+
+def _i8_product(x, wp, ws, c, dev: int, stream):
+    if x.dim() != 2 or wp.dim() != 2 or not wp.numel():
+        raise ValueError(f"activations {tuple(x.shape)} and weight {tuple(wp.shape)} need two sizes each, the weight some values")
+    (M, K), N = x.shape, wp.shape[0]
+    pw, ps = _addr(wp, I8, "wp", dev, (N, K)), _addr(ws, F32, "ws", dev, (N,))
+    if c is None:
+        c = _new((M, N), torch.bfloat16, dev, stream)
+    return M, K, N, pw, ps, c, _addr(c, BF16, "c", dev, (M, N))
+
+
+def gemm_i8(aq, as_, wp, ws, c=None, workspace=None, stream=None) -> torch.Tensor:
+    """The product of int8 codes (r9k_gemm_i8): aq [M,K], as_ [M], wp [N,K] from pack_weight_i8, ws [N] -> C [M,N] bf16."""
+    dev = _dev(aq, "aq")
+    M, K, N, pw, ps, c, pc = _i8_product(aq, wp, ws, c, dev, stream)
+    pa, pas = _addr(aq, I8, "aq", dev), _addr(as_, F32, "as", dev, (M,))
+    if M == 0:  # an empty batch: nothing to compute (an empty tensor has no device address to pass)
+        return c
+    pws, nb, _keep = _scratch(workspace, gemm_i8_workspace(M, K, N), dev, stream)
+    rc = lib().r9k_gemm_i8(pa, pas, M, K, pw, ps, N, pc, pws, nb, _raw(stream, dev))
+    if rc:
+        _check(rc, "r9k_gemm_i8")
+    return c
+
+
+def gemm_i8_qa(a, wp, ws, c=None, workspace=None, stream=None) -> torch.Tensor:
+    """The product with the activations quantised in the call (r9k_gemm_i8_qa): a [M,K] bf16, (wp, ws) as for gemm_i8
+    -> C [M,N] bf16, the bits of quant_i8 and gemm_i8."""
+    dev = _dev(a, "a")
+    M, K, N, pw, ps, c, pc = _i8_product(a, wp, ws, c, dev, stream)
+    pa = _addr(a, BF16, "a", dev)
+    if M == 0:
+        return c
+    pws, nb, _keep = _scratch(workspace, gemm_i8_workspace(M, K, N), dev, stream)
+    rc = lib().r9k_gemm_i8_qa(pa, M, K, pw, ps, N, pc, pws, nb, _raw(stream, dev))
+    if rc:
+        _check(rc, "r9k_gemm_i8_qa")
+    return c
+
+
+def moe_gemm_i8(xq, xs, offsets, wp, ws, src=None, topk: int = 1, act: str = "none", c=None,
+                stream=None) -> torch.Tensor:
+    """The experts' products on sorted rows, in int8 codes (r9k_moe_gemm_i8): xq [rows,K] and xs [rows] from quant_i8,
+    offsets [E+1] and src [R] from moe_permute, wp [E,N,K] from pack_weight_i8, ws [E,N] -> [R,N] bf16, or with
+    act="silu_mul" [R,N/2].  Without src, xq holds the sorted rows; with it the tokens' rows, and row r reads
+    xq[src[r] // topk], topk as in the sort.  Rows from offsets[E] on are not written."""
+    dev = _dev(xq, "xq")
+    if act not in _ACTS:
+        raise ValueError(f"act {act!r} not in {tuple(_ACTS)}")
+    if xq.dim() != 2 or wp.dim() != 3 or not wp.numel():
+        raise ValueError(f"activations {tuple(xq.shape)} need two sizes, the experts' weight {tuple(wp.shape)} three and "
+                         "some values")
+    (rows, K), (E, N) = xq.shape, wp.shape[:2]
+    px, pxs = _addr(xq, I8, "xq", dev), _addr(xs, F32, "xs", dev, (rows,))
+    pw, ps = _addr(wp, I8, "wp", dev, (E, N, K)), _addr(ws, F32, "ws", dev, (E, N))
+    po = _addr(offsets, I32, "offsets", dev, (E + 1,))
+    pi = None if src is None else _addr(src, I32, "src", dev)
+    R = rows if src is None else src.numel()
+    out = (R, N if act == "none" else N // 2)
+    if c is None:
+        c = _new(out, torch.bfloat16, dev, stream)
+    pc = _addr(c, BF16, "c", dev, out)
+    if R == 0:
+        return c
+    rc = lib().r9k_moe_gemm_i8(px, pxs, rows, pi, topk, po, E, R, K, pw, ps, N, _ACTS[act], pc, _raw(stream, dev))
+    if rc:
+        _check(rc, "r9k_moe_gemm_i8")
+    return c
+
+
+# --------------------------------------------------- the router in training ----
+
+MASK = (torch.bool, torch.uint8)
+
+
+@functools.lru_cache(maxsize=1024)
+def moe_balance_loss_workspace(T: int, E: int, topk: int) -> int:
+    b = c_size_t(0)
+    _check(lib().r9k_moe_balance_loss_workspace(T, E, topk, ctypes.byref(b)), "r9k_moe_balance_loss_workspace")
+    return b.value
+
+
+def moe_balance_loss(logits, topk_ids, mask=None, loss=None, counts=None, psum=None, workspace=None, stream=None):
+    """The load balance loss of a routed batch (r9k_moe_balance_loss): logits [T,E] fp32 or bf16, ids [T,topk] int32, mask
+    [T] bool (None: every token counts) -> (loss [] fp32, counts [E+1] int32: the slots of each expert and last the tokens
+    counted, psum [E] fp32)."""
+    dev = _dev(logits, "logits")
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError(f"logits {tuple(logits.shape)} and ids {tuple(topk_ids.shape)} need two sizes each")
+    (T, E), topk = logits.shape, topk_ids.shape[1]
+    need = moe_balance_loss_workspace(T, E, topk)  # refuses sizes that no output could be made for
+    pl = _addr(logits, _ROWS, "logits", dev)
+    pi = _addr(topk_ids, I32, "topk_ids", dev, (T, topk))
+    pm = None if mask is None else _addr(mask, MASK, "mask", dev, (T,))
+    if loss is None:
+        loss = _new((), torch.float32, dev, stream)
+    if counts is None:
+        counts = _new(E + 1, torch.int32, dev, stream)
+    if psum is None:
+        psum = _new(E, torch.float32, dev, stream)
+    po, pc, pp = _addr(loss, F32, "loss", dev, ()), _addr(counts, I32, "counts", dev, (E + 1,)), _addr(psum, F32, "psum", dev, (E,))
+    pw, nb, keep = _scratch(workspace, need, dev, stream)
+    if T == 0:  # no rows to read (empty tensors have no device address to pass)
+        pl = pi = pw
+        pm = None
+    rc = lib().r9k_moe_balance_loss(pl, _ROWS[logits.dtype], T, E, pi, topk, pm, po, pc, pp, pw, nb, _raw(stream, dev))
+    if rc:
+        _check(rc, "r9k_moe_balance_loss")
+    return loss, counts, psum
+
+
+def moe_balance_loss_backward(gloss, logits, counts, topk: int, mask=None, route=None, glogits=None,
+                              stream=None) -> torch.Tensor:
+    """The gradient of moe_balance_loss for the logits (r9k_moe_balance_loss_backward): gloss [] fp32, logits and mask as in
+    the forward call, counts [E+1] from it (or their sum over ranks) -> glogits [T,E] of the logits' type.  route = (gw, ids,
+    w), each [T,topk]: the gradient of moe_route_backward is added in the same pass."""
+    dev = _dev(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits {tuple(logits.shape)} need two sizes")
+    T, E = logits.shape
+    pl = _addr(logits, _ROWS, "logits", dev)
+    pg, pc = _addr(gloss, F32, "gloss", dev, ()), _addr(counts, I32, "counts", dev, (E + 1,))
+    pm = None if mask is None else _addr(mask, MASK, "mask", dev, (T,))
+    pgw = pi = pw = None
+    if route is not None:
+        gw, ids, w = route
+        pgw, pi = _addr(gw, F32, "gw", dev, (T, topk)), _addr(ids, I32, "ids", dev, (T, topk))
+        pw = _addr(w, F32, "w", dev, (T, topk))
+    glogits, po = _out(glogits, (T, E), logits, "glogits", dev, stream)
+    if T:
+        rc = lib().r9k_moe_balance_loss_backward(pg, pl, _ROWS[logits.dtype], T, E, topk, pc, pm, pgw, pi, pw, po,
+                                                 _raw(stream, dev))
+        if rc:
+            _check(rc, "r9k_moe_balance_loss_backward")
+    return glogits
+
+
+def moe_route_backward(gw, topk_ids, topk_w, E: int, glogits=None, stream=None) -> torch.Tensor:
+    """The gradient of moe_route for the logits (r9k_moe_route_backward): gw, ids and weights [T,topk] -> glogits [T,E] fp32,
+    zero outside a token's experts."""
+    dev = _dev(gw, "gw")
+    if gw.dim() != 2:
+        raise ValueError(f"gw {tuple(gw.shape)} needs two sizes")
+    T, topk = gw.shape
+    if not 1 <= E <= 65536:  # before an output of that many columns is made
+        _check(-2, "r9k_moe_route_backward")
+    pg, pi, pw = _addr(gw, F32, "gw", dev), _addr(topk_ids, I32, "ids", dev, (T, topk)), _addr(topk_w, F32, "w", dev, (T, topk))
+    glogits, po = _out(glogits, (T, E), gw, "glogits", dev, stream)
+    if T:
+        rc = lib().r9k_moe_route_backward(pg, pi, pw, T, E, topk, po, _raw(stream, dev))
+        if rc:
+            _check(rc, "r9k_moe_route_backward")
+    return glogits

@@ -1,0 +1,191 @@
+// The C ABI of the 8-bit integer products and of the router's training operators: argument
+// checks, plans and launches.  Declarations, argument meanings and error behaviour: r9k.h.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "api_checks.h"
+#include "i8_internal.h"
+
+using namespace r9k;
+
+extern "C" {
+
+// ---- products -------------------------------------------------------------------
+
+static bool i8_k(int64_t K) { return K > 0 && K % 128 == 0 && K < int64_t(1) << 17; }
+static bool i8_shape(int64_t N, int64_t K, int64_t nmul) { return N > 0 && N % nmul == 0 && N <= MAX_DIM && i8_k(K); }
+
+int r9k_quant_i8(const uint16_t *x, int64_t rows, int64_t K, int8_t *q, float *s, void *stream) {
+    if (!x || !q || !s) return R9K_ERR_NULLPTR;
+    if (rows < 0 || rows >= 128 * MAX_DIM || !i8_k(K)) return R9K_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(s)) return R9K_ERR_ALIGN;
+    if (clash({{q, rows * K}, {s, 4 * rows}}, {{x, 2 * rows * K}})) return R9K_ERR_ARG;
+    if (rows == 0) return R9K_OK;
+    if (int rc = check_device()) return rc;
+    return launch_result(launch_quant_i8(x, rows, K, q, s, (hipStream_t)stream));
+}
+
+int r9k_pack_weight_i8(const int8_t *wq, int64_t N, int64_t K, int8_t *wp, void *stream) {
+    if (!wq || !wp) return R9K_ERR_NULLPTR;
+    if (N <= 0 || N % 16 || !i8_k(K) || N >= (int64_t(1) << 36) / K) return R9K_ERR_SHAPE;
+    if (!aligned16(wq) || !aligned16(wp)) return R9K_ERR_ALIGN;
+    if (clash({{wp, N * K}}, {{wq, N * K}})) return R9K_ERR_ARG;
+    if (int rc = check_device()) return rc;
+    return launch_result(launch_pack_weight((const uint8_t *)wq, N, K, (uint8_t *)wp, (hipStream_t)stream));
+}
+
+// The workspace: the codes and scales of a call that quantises, then a split's sums
+struct I8Layout {
+    size_t scales, part, total;
+};
+static I8Layout i8_layout(int64_t M, int64_t K, int64_t N, const I8Cfg &c) {
+    I8Layout l;
+    l.scales = align_up((size_t)(M * K), 256);
+    l.part = l.scales + align_up((size_t)M * 4, 256);
+    l.total = l.part + (c.ksplit > 1 ? align_up((size_t)c.ksplit * (size_t)(M * N) * 4, 256) : 0);
+    return l;
+}
+
+int r9k_gemm_i8_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes) {
+    if (!bytes) return R9K_ERR_NULLPTR;
+    if (M < 0 || M > MAX_DIM || !i8_shape(N, K, 16)) return R9K_ERR_SHAPE;
+    *bytes = M ? i8_layout(M, K, N, i8_config(M, K, N, 0, false)).total : 0;
+    return R9K_OK;
+}
+
+static int run_gemm_i8(const uint16_t *a, const int8_t *aq, const float *as, int64_t M, int64_t K, const int8_t *wp,
+                       const float *ws, int64_t N, uint16_t *c, void *workspace, size_t ws_bytes, hipStream_t s) {
+    if (!(a ? (const void *)a : (const void *)aq) || (!a && !as) || !wp || !ws || !c) return R9K_ERR_NULLPTR;
+    if (M < 0 || M > MAX_DIM || !i8_shape(N, K, 16)) return R9K_ERR_SHAPE;
+    if (!aligned16(a) || !aligned16(aq) || !aligned16(as) || !aligned16(wp) || !aligned16(ws) || !aligned16(c) ||
+        !aligned16(workspace))
+        return R9K_ERR_ALIGN;
+    if (M == 0) return R9K_OK;
+    const I8Cfg cfg = i8_config(M, K, N, 0, false);
+    const I8Layout l = i8_layout(M, K, N, cfg);
+    const bool need = a || cfg.ksplit > 1;
+    if (need && !workspace) return R9K_ERR_NULLPTR;
+    if (need && ws_bytes < l.total) return R9K_ERR_WORKSPACE;
+    if (clash({{c, 2 * M * N}, {need ? workspace : nullptr, (int64_t)l.total}},
+              {{a, 2 * M * K}, {aq, M * K}, {as, 4 * M}, {wp, N * K}, {ws, 4 * N}}))
+        return R9K_ERR_ARG;
+    if (int rc = check_device()) return rc;
+    uint8_t *w = (uint8_t *)workspace;
+    if (a) {
+        aq = (const int8_t *)w;
+        as = (const float *)(w + l.scales);
+        const hipError_t err = launch_quant_i8(a, M, K, (int8_t *)w, (float *)(w + l.scales), s);
+        if (err != hipSuccess) return launch_result(err);
+    }
+    I8Args g{aq, as, wp, ws, c, M, K, N, nullptr, nullptr, 1, 1, M, 0, need ? (int32_t *)(w + l.part) : nullptr};
+    return launch_result(launch_gemm_i8(g, cfg, s));
+}
+
+int r9k_gemm_i8(const int8_t *aq, const float *as, int64_t M, int64_t K, const int8_t *wp, const float *ws, int64_t N,
+                uint16_t *c, void *workspace, size_t ws_bytes, void *stream) {
+    return run_gemm_i8(nullptr, aq, as, M, K, wp, ws, N, c, workspace, ws_bytes, (hipStream_t)stream);
+}
+
+int r9k_gemm_i8_qa(const uint16_t *a, int64_t M, int64_t K, const int8_t *wp, const float *ws, int64_t N, uint16_t *c,
+                   void *workspace, size_t ws_bytes, void *stream) {
+    if (!a) return R9K_ERR_NULLPTR;
+    return run_gemm_i8(a, nullptr, nullptr, M, K, wp, ws, N, c, workspace, ws_bytes, (hipStream_t)stream);
+}
+
+int r9k_moe_gemm_i8(const int8_t *aq, const float *as, int64_t arows, const int32_t *src, int64_t topk,
+                    const int32_t *offsets, int64_t E, int64_t R, int64_t K, const int8_t *wp, const float *ws,
+                    int64_t N, int act, uint16_t *c, void *stream) {
+    if (!aq || !as || !offsets || !wp || !ws || !c) return R9K_ERR_NULLPTR;
+    const bool silu = act == R9K_ACT_SILU_MUL;
+    if (R < 0 || R >= 128 * MAX_DIM || E < 1 || E > MOE_MAX_E || arows < 0 || arows >= 128 * MAX_DIM ||
+        !i8_shape(N, K, silu ? 32 : 16) || (R > 0 && arows < 1) || topk < 1 || topk > MAX_DIM ||
+        R > arows * (src ? topk : 1))
+        return R9K_ERR_SHAPE;
+    if (act != R9K_ACT_NONE && !silu) return R9K_ERR_ARG;
+    if (!aligned16(aq) || !aligned16(as) || !aligned16(src) || !aligned16(offsets) || !aligned16(wp) ||
+        !aligned16(ws) || !aligned16(c))
+        return R9K_ERR_ALIGN;
+    if (clash({{c, (silu ? 1 : 2) * R * N}},
+              {{aq, arows * K}, {as, 4 * arows}, {src, 4 * R}, {offsets, 4 * (E + 1)}, {wp, E * N * K}, {ws, 4 * E * N}}))
+        return R9K_ERR_ARG;
+    if (R == 0) return R9K_OK;
+    if (int rc = check_device()) return rc;
+    I8Args g{aq, as, wp, ws, c, R, K, N, offsets, src, E, topk, arows, silu ? 1 : 0, nullptr};
+    return launch_result(launch_gemm_i8(g, i8_config(R, K, N, E, silu), (hipStream_t)stream));
+}
+
+// ---- the router ------------------------------------------------------------------
+
+static int check_router_shape(int64_t T, int64_t E, int64_t topk, int64_t most) {
+    return T < 0 || T >= MAX_BLOCKS || E < 1 || E > most || topk < 1 || topk > 64 ? R9K_ERR_SHAPE : R9K_OK;
+}
+static size_t balance_counts_at(int64_t T, int64_t E) { return align_up((size_t)balance_parts(T, E) * E * 4, 256); }
+static size_t balance_bytes(int64_t T, int64_t E) {
+    return balance_counts_at(T, E) + align_up((size_t)balance_parts(T, E) * (E + 1) * 4, 256);
+}
+
+int r9k_moe_balance_loss_workspace(int64_t T, int64_t E, int64_t topk, size_t *bytes) {
+    if (!bytes) return R9K_ERR_NULLPTR;
+    if (int rc = check_router_shape(T, E, topk, MOE_MAX_E)) return rc;
+    *bytes = balance_bytes(T, E);
+    return R9K_OK;
+}
+
+int r9k_moe_balance_loss(const void *logits, int dtype, int64_t T, int64_t E, const int32_t *topk_ids, int64_t topk,
+                         const uint8_t *mask, float *loss, int32_t *counts, float *psum, void *workspace,
+                         size_t ws_bytes, void *stream) {
+    if (!logits || !topk_ids || !loss || !counts || !psum) return R9K_ERR_NULLPTR;
+    if (int rc = check_router_shape(T, E, topk, MOE_MAX_E)) return rc;
+    if (dtype != R9K_BF16 && dtype != R9K_F32) return R9K_ERR_ARG;
+    if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(mask) || !aligned16(loss) || !aligned16(counts) ||
+        !aligned16(psum) || !aligned16(workspace))
+        return R9K_ERR_ALIGN;
+    const size_t need = balance_bytes(T, E);
+    if (clash({{loss, 4}, {counts, 4 * (E + 1)}, {psum, 4 * E}, {workspace, (int64_t)need}},
+              {{logits, T * E * (dtype == R9K_F32 ? 4 : 2)}, {topk_ids, 4 * T * topk}, {mask, T}}))
+        return R9K_ERR_ARG;
+    if (need && !workspace) return R9K_ERR_NULLPTR;
+    if (ws_bytes < need) return R9K_ERR_WORKSPACE;
+    if (int rc = check_device()) return rc;
+    uint8_t *w = (uint8_t *)workspace;
+    const BalanceArgs a{logits, dtype == R9K_F32, T, E, topk, topk_ids, mask, loss, counts, psum, (float *)w,
+                        (int32_t *)(w + balance_counts_at(T, E))};
+    return launch_result(launch_balance_loss(a, (hipStream_t)stream));
+}
+
+int r9k_moe_balance_loss_backward(const float *gloss, const void *logits, int dtype, int64_t T, int64_t E, int64_t topk,
+                                  const int32_t *counts, const uint8_t *mask, const float *gw, const int32_t *topk_ids,
+                                  const float *topk_w, void *glogits, void *stream) {
+    if (!gloss || !logits || !counts || !glogits || (gw == nullptr) != (topk_ids == nullptr) ||
+        (gw == nullptr) != (topk_w == nullptr))
+        return R9K_ERR_NULLPTR;
+    if (int rc = check_router_shape(T, E, topk, MOE_MAX_E)) return rc;
+    if (dtype != R9K_BF16 && dtype != R9K_F32) return R9K_ERR_ARG;
+    if (!aligned16(gloss) || !aligned16(logits) || !aligned16(counts) || !aligned16(mask) || !aligned16(gw) ||
+        !aligned16(topk_ids) || !aligned16(topk_w) || !aligned16(glogits))
+        return R9K_ERR_ALIGN;
+    const int64_t rows = T * E * (dtype == R9K_F32 ? 4 : 2), slots = 4 * T * topk;
+    if (clash({{glogits, rows}}, {{gloss, 4}, {logits, rows}, {counts, 4 * (E + 1)}, {mask, T}, {gw, slots},
+                                  {topk_ids, slots}, {topk_w, slots}}))
+        return R9K_ERR_ARG;
+    if (T == 0) return R9K_OK;
+    if (int rc = check_device()) return rc;
+    const RouterGradArgs a{gw, topk_ids, topk_w, T, E, topk, gloss, logits, dtype == R9K_F32, counts, mask, glogits};
+    return launch_result(launch_router_backward(a, (hipStream_t)stream));
+}
+
+int r9k_moe_route_backward(const float *gw, const int32_t *topk_ids, const float *topk_w, int64_t T, int64_t E,
+                           int64_t topk, float *glogits, void *stream) {
+    if (!gw || !topk_ids || !topk_w || !glogits) return R9K_ERR_NULLPTR;
+    if (int rc = check_router_shape(T, E, topk, 65536)) return rc;
+    if (!aligned16(gw) || !aligned16(topk_ids) || !aligned16(topk_w) || !aligned16(glogits)) return R9K_ERR_ALIGN;
+    const int64_t slots = 4 * T * topk;
+    if (clash({{glogits, 4 * T * E}}, {{gw, slots}, {topk_ids, slots}, {topk_w, slots}})) return R9K_ERR_ARG;
+    if (T == 0) return R9K_OK;
+    if (int rc = check_device()) return rc;
+    const RouterGradArgs a{gw, topk_ids, topk_w, T, E, topk, nullptr, nullptr, true, nullptr, nullptr, glogits};
+    return launch_result(launch_router_backward(a, (hipStream_t)stream));
+}
+
+}  // extern "C"

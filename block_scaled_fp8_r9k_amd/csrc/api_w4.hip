@@ -10,7 +10,7 @@
 #include <initializer_list>
 #include <mutex>
 
-#include "r9k.h"
+#include "api_checks.h"
 #include "w4_internal.h"
 
 using namespace r9k;
@@ -28,41 +28,6 @@ W4Tuning &w4_tuning() {
 }
 }  // namespace r9k
 
-namespace {
-
-// Device check, cached per device id: 1 = gfx950, 2 = not usable.
-constexpr int MAX_DEV = 64;
-std::atomic<int> g_dev_ok[MAX_DEV];
-
-int check_device() {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) {
-        (void)hipGetLastError();
-        return R9K_ERR_DEVICE;
-    }
-    const int st = dev < MAX_DEV ? g_dev_ok[dev].load() : 0;
-    if (st) return st == 1 ? R9K_OK : R9K_ERR_DEVICE;
-    hipDeviceProp_t prop;
-    const bool ok = hipGetDeviceProperties(&prop, dev) == hipSuccess && strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    (void)hipGetLastError();
-    if (dev < MAX_DEV) g_dev_ok[dev] = ok ? 1 : 2;
-    return ok ? R9K_OK : R9K_ERR_DEVICE;
-}
-
-inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-inline int launch_result(hipError_t e) { return e == hipSuccess ? R9K_OK : R9K_ERR_LAUNCH; }
-
-constexpr int64_t MAX_DIM = int64_t(1) << 24;
-
-// Blocks of 256 threads in a launch: the runtime refuses 2^32 threads and more
-constexpr int64_t MAX_BLOCKS = int64_t(1) << 24;
-
-// Experts that the sort and the expert products take: the sort keeps four counters an
-// expert in a CTA's LDS
-constexpr int64_t MOE_MAX_E = 2048;
-
-}  // namespace
-
 extern "C" {
 
 // ---- 4-bit weights ------------------------------------------------------------
@@ -77,25 +42,6 @@ static bool w4_shape(int64_t N, int64_t K, int64_t nmul) {
            N <= (int64_t(1) << 46) / K;
 }
 
-// Bytes that a call reads or writes.  Its CTAs read while others write, so an output
-// (a workspace too) may lie on no input and on no other output.
-struct Span {
-    const void *p;
-    int64_t n;
-};
-static bool overlap(const Span &a, const Span &b) {
-    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-    return a.p && b.p && a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
-}
-static bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
-    for (auto o = outs.begin(); o != outs.end(); ++o) {
-        for (const Span &i : ins)
-            if (overlap(*o, i)) return true;
-        for (auto q = outs.begin(); q != o; ++q)
-            if (overlap(*o, *q)) return true;
-    }
-    return false;
-}
 static int64_t w4_scale_bytes(int64_t N, int64_t K, int format, int group) {
     return N * (K / group) * (format == R9K_W4_INT ? 2 : 1);
 }

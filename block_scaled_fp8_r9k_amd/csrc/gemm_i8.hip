@@ -1,0 +1,218 @@
+// Products in 8-bit integers, few rows: the weight-streaming kernel.
+//
+//   c[m][n] = bf16( (sum_k aq[m][k] * wq[n][k]) * as[m] * ws[n] )
+//
+// with the sum in 32-bit integers, exact: no split of K and no order of the sum changes a
+// bit of the output, which is rounded where the sum becomes fp32, at each scale and at the end.
+//
+// C^T = W A^T: a wave takes NT column tiles of 16 (rows of W) and MT row tiles of 16 (rows
+// of A) and streams its K slice of both into registers as fragments of
+// v_mfma_i32_16x16x64_i8, D chunks of 128 K ahead.  The CTA's waves hold consecutive K
+// slices of the same tiles; their sums meet in LDS.  Rows of the block that are not there
+// repeat its last row and are not stored.
+//
+// For expert products the rows are ranges of `offsets`, one per expert; a CTA finds its
+// expert and row block there, and may read its activation rows through the sort's index.
+// With silu the first half of a wave's tiles are gate columns, the second half the up
+// columns that belong to them.
+#include <algorithm>
+
+#include "i8_device.h"
+#include "i8_internal.h"
+
+namespace r9k {
+
+template <int MT, int NT, int D>
+__global__ __launch_bounds__(512) void k_gemm_i8(I8Args p) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
+    const int nw = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = 1 << p.wnl, ct = wave & (wn - 1), slice = wave >> p.wnl, wk = nw >> p.wnl;
+    const int C = (int)(p.K / 128), tiles = (int)(p.N / 16);
+    const int bx = blockIdx.x, item = blockIdx.y, ks = blockIdx.z;
+
+    // rows [r0, r1) of this CTA, of expert e
+    int e = 0, r0, r1;
+    if (p.offsets) {
+        int a0, a1;
+        if (!w4_find_block(p.offsets, (int)p.E, (int)p.M, 16 * MT, item, e, a0, a1)) return;
+        r0 = a0;
+        r1 = min(a1, a0 + 16 * MT);
+    } else {
+        r0 = item * 16 * MT;
+        r1 = (int)min<int64_t>(p.M, (int64_t)r0 + 16 * MT);
+    }
+    e = __builtin_amdgcn_readfirstlane(e);
+    r0 = __builtin_amdgcn_readfirstlane(r0);
+    r1 = __builtin_amdgcn_readfirstlane(r1);
+    const int rows = r1 - r0;
+
+    // the wave's column tiles; those past the last repeat it and are not stored
+    int tile[NT];
+    const int u0 = bx * wn + ct;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        tile[j] = min(u0 * NT + j, tiles - 1);
+        if constexpr (NT > 1) {
+            if (p.silu) tile[j] = min(u0 * (NT / 2) + j % (NT / 2), tiles / 2 - 1) + (j < NT / 2 ? 0 : tiles / 2);
+        }
+    }
+
+    // activation rows of the lane's row in each row tile; an index that points outside the
+    // activations means row 0
+    uint32_t aoff[MT];
+    float as[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int r = r0 + min(16 * m + l16, rows - 1);
+        uint32_t row = r;
+        if (p.src) {
+            row = w4_div_topk((uint32_t)p.src[r], (uint32_t)p.topk, p.tmagic);
+            if (row >= (uint32_t)p.arows) row = 0;
+        }
+        as[m] = p.as[row];
+        aoff[m] = (p.src ? row : row - (uint32_t)r0) * (uint32_t)p.K + 16 * q;
+    }
+
+    // this wave's chunks [cb, ce).  Weight loads past ce lie behind the descriptors' end, return
+    // zeros and move nothing, and so make no difference whatever activations meet them.
+    const int kb = ks * p.span, ke = min(C, kb + p.span);
+    const int cb = kb + slice * p.cps, ce = min(ke, cb + p.cps);
+    __amdgpu_buffer_rsrc_t wd[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+        wd[j] = __builtin_amdgcn_make_buffer_rsrc((void *)(p.wp + ((int64_t)e * tiles + tile[j]) * C * 2048), (short)0,
+                                                  ce * 2048, 0x00020000);
+    // (the block's rows, or with an index all of the activations, less than 2^32 bytes)
+    const __amdgpu_buffer_rsrc_t ad = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(p.src ? p.aq : p.aq + (int64_t)r0 * p.K), (short)0,
+        (int)((uint32_t)(p.src ? p.arows : rows) * (uint32_t)p.K), 0x00020000);
+
+    v4i acc[NT][MT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[j][m] = v4i{0, 0, 0, 0};
+    v4i wr[D][NT][2], ar[D][MT][2];
+    auto load = [&](int c, int d) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                ar[d][m][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(ad, aoff[m] + c * 128 + 64 * h, 0, 0));
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                wr[d][j][h] = __builtin_bit_cast(v4i, load_buf_nt16(wd[j], 16 * lane + c * 2048 + 1024 * h));
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(cb + d, d);
+    for (int c = cb; c < ce; c += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) acc[j][m] = i8_mfma(wr[d][j][h], ar[d][m][h], acc[j][m]);
+            load(c + d + D, d);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) i8_pin(acc[j][m]);
+
+    // the K slices' sums, in LDS; an item is one output tile of the CTA (with silu, a gate
+    // tile and its up tile)
+    v4i *red = (v4i *)lds;  // [wave][tile][row tile][lane]
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) red[((wave * NT + j) * MT + m) * 64 + lane] = acc[j][m];
+    __syncthreads();
+    const int64_t ldc = p.silu ? p.N / 2 : p.N;
+    const int nt = p.silu ? NT / 2 : NT;
+    const int otiles = p.silu ? tiles / 2 : tiles;
+    const int outs = wn * nt * MT;
+    for (int it = wave; it < outs; it += nw) {
+        const int w = it & (wn - 1), j = (it >> p.wnl) / MT, m = (it >> p.wnl) % MT;
+        auto total = [&](int jj) {
+            v4i x = red[((w * NT + jj) * MT + m) * 64 + lane];
+            for (int s = 1; s < wk; ++s) x += red[(((s * wn + w) * NT + jj) * MT + m) * 64 + lane];
+            return x;
+        };
+        const int t = (bx * wn + w) * nt + j, r = 16 * m + l16;
+        if (t >= otiles || r >= rows) continue;
+        v4i x = total(j);
+        if (p.ksplit > 1) {
+            *(v4i *)(p.part + ((int64_t)ks * p.M + r0 + r) * p.N + 16 * t + 4 * q) = x;
+            continue;
+        }
+        float a = as[0];
+#pragma unroll
+        for (int i = 1; i < MT; ++i) a = m == i ? as[i] : a;
+        const float *ws = p.ws + (int64_t)e * p.N + 16 * t + 4 * q;
+        v4f y = i8_scale(x, a, *(const float4 *)ws);
+        if (p.silu) {
+            const v4f u = i8_scale(total(j + nt), a, *(const float4 *)(ws + p.N / 2));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = w4_silu_mul(y[i], u[i]);
+        }
+        *(uint2 *)(p.c + (r0 + r) * ldc + 16 * t + 4 * q) = w4_bf16x4(y);
+    }
+}
+
+// The sums of a K split, added and scaled.
+__global__ __launch_bounds__(256) void k_i8_reduce(const int32_t *__restrict__ part, const float *__restrict__ as,
+                                                   const float *__restrict__ ws, uint16_t *__restrict__ c, int64_t M,
+                                                   int64_t N, int ksplit) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= M * N) return;
+    v4i x = *(const v4i *)(part + i);
+    for (int k = 1; k < ksplit; ++k) x += *(const v4i *)(part + k * M * N + i);
+    *(uint2 *)(c + i) = w4_bf16x4(i8_scale(x, as[i / N], *(const float4 *)(ws + i % N)));
+}
+
+I8Cfg i8_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
+    I8Cfg c{M <= (E ? 12 * E : 16) ? 1 : 2, silu ? 2 : 1, 1, 8, 1};
+    const int64_t C = K / 128, tiles = N / 16 / (silu ? 2 : 1);
+    while (c.wk > 1 && C < 2 * c.wk) c.wk /= 2;
+    const int64_t ctas = E ? tiles * E : tiles * ((M + 16 * c.mt - 1) / (16 * c.mt));
+    if (!E && ctas < 256 && C >= 64) c.ksplit = 2;
+    return c;
+}
+
+template <int MT, int NT>
+static hipError_t launch_one(I8Args a, const I8Cfg &c, hipStream_t s) {
+    constexpr int D = 4;
+    const int64_t C = a.K / 128, RB = 16 * MT;
+    const int64_t per = (int64_t)c.wn * (a.silu ? NT / 2 : NT), tiles = a.N / 16 / (a.silu ? 2 : 1);
+    const int64_t nblk = (tiles + per - 1) / per;
+    int64_t items = (a.M + RB - 1) / RB;
+    if (a.offsets) items = (a.M + std::min(a.E, a.M) * (RB - 1)) / RB;
+    a.wnl = __builtin_ctz((unsigned)c.wn);
+    a.ksplit = c.ksplit;
+    a.span = (int)((C + c.ksplit - 1) / c.ksplit);
+    a.cps = (a.span + c.wk - 1) / c.wk;
+    a.tmagic = a.topk > 1 ? (uint32_t)(((uint64_t(1) << 32) + a.topk - 1) / a.topk) : 0;
+    const size_t lds = (size_t)c.wn * c.wk * NT * MT * 1024;
+    if (nblk > 0x7fffffff / 512 || items > 65535 || lds > 64 * 1024) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_gemm_i8<MT, NT, D>), dim3((unsigned)nblk, (unsigned)items, (unsigned)c.ksplit),
+                       dim3(64 * c.wn * c.wk), lds, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_gemm_i8(const I8Args &a, const I8Cfg &c, hipStream_t s) {
+    hipError_t err;
+    if (c.mt == 1) err = c.nt == 1 ? launch_one<1, 1>(a, c, s) : launch_one<1, 2>(a, c, s);
+    else err = c.nt == 1 ? launch_one<2, 1>(a, c, s) : launch_one<2, 2>(a, c, s);
+    if (err != hipSuccess || c.ksplit == 1) return err;
+    hipLaunchKernelGGL(k_i8_reduce, dim3((unsigned)((a.M * a.N / 4 + 255) / 256)), dim3(256), 0, s, a.part, a.as, a.ws,
+                       a.c, a.M, a.N, c.ksplit);
+    return hipGetLastError();
+}
+
+}  // namespace r9k

@@ -1,0 +1,73 @@
+// Device helpers of the 8-bit integer kernels.
+//
+// Codes are signed bytes, -128 to 127; a row of activations has one fp32 scale, an
+// output channel (a row of W) one.  Packed weights (r9k_pack_weight_i8): for 16-row tile
+// t = n / 16 and chunk c = k / 128 (C = K / 128 chunks) the 2 KiB block at (t * C + c) * 2048
+// holds, at h * 1024 + 16 * l (h = 0, 1; l = 0..63), the 16 bytes that MFMA lane l
+// feeds to v_mfma_i32_16x16x64_i8 as half h of the chunk: row 16 t + l % 16, columns 128 c +
+// 64 h + 16 (l / 16) .. +15.
+#pragma once
+
+#include "r9k_device.h"
+#include "w4_device.h"
+
+namespace r9k {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+// D = W(16x64) * A(64x16) + C in 32-bit integers.  Lane l supplies row l % 16 of W and column
+// l % 16 of A (row l % 16 of the activations), K bytes 16 (l / 16) .. +15 of both; D's lane l
+// holds rows 4 (l / 16) .. +3 of column l % 16.  Sums are exact: K < 2^17 products of at most
+// 2^14 stay below 2^31.
+__device__ __forceinline__ v4i i8_mfma(v4i w, v4i a, v4i c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, a, c, 0, 0, 0);
+}
+
+// Computed where it stands, with the whole wave enabled (as pin_acc of fp32 sums)
+__device__ __forceinline__ void i8_pin(v4i &x) { asm volatile("" : "+v"(x)); }
+
+// Four sums of one row and four channels -> fp32: one rounding when the sum becomes fp32 (above
+// 2^24), one for each scale.
+__device__ __forceinline__ v4f i8_scale(v4i x, float as, float4 ws) {
+    return v4f{(float)x[0] * as * ws.x, (float)x[1] * as * ws.y, (float)x[2] * as * ws.z, (float)x[3] * as * ws.w};
+}
+
+// A row's quantisation: b = max(amax, 1e-10) from the largest bf16 bit pattern; with an infinity
+// or a NaN in the row (patterns from 0x7F80 on) the scale is NaN and the codes are 0.
+struct I8Scale {
+    float s, inv;
+    bool bad;
+};
+__device__ __forceinline__ I8Scale i8_row_scale(uint32_t amax_bits) {
+    I8Scale r;
+    r.bad = amax_bits >= 0x7F80u;
+    const float b = fmaxf(r.bad ? 0.0f : __uint_as_float(amax_bits << 16), 1e-10f);
+    r.s = r.bad ? __uint_as_float(0x7FC00000u) : b / 127.0f;
+    r.inv = r.bad ? 0.0f : 127.0f / b;
+    return r;
+}
+
+// rint(x * inv) of eight bf16, |x * inv| <= 127 (1 + 2^-23): adding 1.5 * 2^23 rounds to the
+// nearest integer, ties to even, and leaves its two's complement in the low byte.
+__device__ __forceinline__ uint32_t i8x4(float a, float b, float c, float d, float inv) {
+    const float m = 12582912.0f;
+    const uint32_t x = __float_as_uint(a * inv + m), y = __float_as_uint(b * inv + m);
+    const uint32_t z = __float_as_uint(c * inv + m), w = __float_as_uint(d * inv + m);
+    const uint32_t lo = __builtin_amdgcn_perm(y, x, 0x0C0C0400u), hi = __builtin_amdgcn_perm(w, z, 0x04000C0Cu);
+    return lo | hi;
+}
+__device__ __forceinline__ uint2 i8_quant8(uint4 v, const I8Scale &r) {
+    const uint2 o = make_uint2(i8x4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y), r.inv),
+                               i8x4(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w), r.inv));
+    return r.bad ? make_uint2(0, 0) : o;
+}
+
+// Maximum over the wave, the same in every lane.  Every lane must be active.
+__device__ __forceinline__ uint32_t max64(uint32_t v) {
+    v = max16_dpp(v);
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+    return max(max(a, b), max(c, d));
+}
+
+}  // namespace r9k

@@ -1,0 +1,67 @@
+// Host-side interfaces between the C ABI (api_i8.hip) and the kernels of the 8-bit
+// integer products and of the router's training operators.  Every launcher enqueues on
+// `stream` and returns hipGetLastError().
+#pragma once
+
+#include "r9k_internal.h"
+
+namespace r9k {
+
+// ---- 8-bit integer products (i8_quant.hip, gemm_i8.hip) ----
+hipError_t launch_quant_i8(const uint16_t *x, int64_t rows, int64_t K, int8_t *q, float *s, hipStream_t st);
+
+struct I8Args {
+    const int8_t *aq;        // activation codes [arows][K]
+    const float *as;         // their scales [arows]
+    const int8_t *wp;        // packed codes [E][N*K]
+    const float *ws;         // channel scales [E][N]
+    uint16_t *c;             // [M][N] bf16, or [M][N/2] with silu
+    int64_t M, K, N;         // M: rows of c (expert products: the most that offsets cover)
+    const int32_t *offsets;  // expert products: [E + 1] first rows; NULL for a dense product
+    const int32_t *src;      // expert products: row r reads activation row src[r] / topk; NULL: row r
+    int64_t E, topk, arows;
+    int silu;                // 1: columns [0, N/2) gate, [N/2, N) up, c = silu(gate) * up
+    int32_t *part;           // with a K split: sums [ksplit][M][N] (workspace)
+    // set by the launchers
+    int ksplit, wnl, span, cps;  // CTAs along K; log2 of the waves along the columns; chunks a split, a wave's slice
+    uint32_t tmagic;             // ceil(2^32 / topk), 0 for topk = 1
+};
+struct I8Cfg {
+    int mt;      // row tiles of 16 a CTA
+    int nt;      // column tiles a wave
+    int wn, wk;  // waves along the columns, K slices
+    int ksplit;  // CTAs along K (dense products only)
+};
+I8Cfg i8_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu);
+hipError_t launch_gemm_i8(const I8Args &a, const I8Cfg &c, hipStream_t s);
+
+// ---- the router's training operators (router.hip) ----
+struct BalanceArgs {
+    const void *logits;     // [T][E], fp32 or bf16
+    bool f32;
+    int64_t T, E, topk;
+    const int32_t *ids;     // [T][topk]
+    const uint8_t *mask;    // [T], or NULL
+    float *loss;            // [1]
+    int32_t *counts;        // [E + 1]
+    float *psum;            // [E]
+    float *part_p;          // [parts][E] (workspace)
+    int32_t *part_c;        // [parts][E + 1]
+};
+int balance_parts(int64_t T, int64_t E);
+hipError_t launch_balance_loss(const BalanceArgs &a, hipStream_t s);
+struct RouterGradArgs {
+    const float *gw;        // [T][topk], or NULL: the balance loss's part alone
+    const int32_t *ids;
+    const float *w;
+    int64_t T, E, topk;
+    const float *gloss;     // [1], or NULL: the routing weights' part alone
+    const void *logits;
+    bool f32;
+    const int32_t *counts;
+    const uint8_t *mask;
+    void *g;                // [T][E] of the logits' type
+};
+hipError_t launch_router_backward(const RouterGradArgs &a, hipStream_t s);
+
+}  // namespace r9k

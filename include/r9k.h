@@ -60,7 +60,7 @@ extern "C" {
 #pragma GCC visibility push(default)
 #endif
 
-#define R9K_ABI_VERSION 10
+#define R9K_ABI_VERSION 11
 
 /* Return codes: 0 or negative, as the pages' kernels return them (release
  * v0.3.0, its validation record: a test failing "with the kernel's -7").
@@ -78,7 +78,7 @@ extern "C" {
  * routing and the shared-expert fold, 5 the bf16-activation variant, 6 the
  * mid-width kernel in the plan query, 7 the allocation-free GEMM entry point, 8 the tiled-plan
  * control and R9K_ENGINE_SPLITK, 9 the 4-bit weights and the rows sorted by expert, 10 their plan
- * query and control).  Callers refuse
+ * query and control, 11 the 8-bit integer products and the router's training operators).  Callers refuse
  * a library whose version differs from the header they were built against:
  * the convention of the pages' plugin, which refuses an older libr9k.so
  * (release v0.2.2, "Upgrading").  Host only; cannot fail. */
@@ -567,6 +567,123 @@ int r9k_moe_unpermute(const void *y, int dtype, int64_t T, int64_t H, const int3
  * Errors: as r9k_moe_unpermute. */
 int r9k_moe_unpermute_backward(const void *gout, const void *y, int dtype, int64_t T, int64_t H, const int32_t *pos,
                                const float *w, int64_t topk, void *gy, float *gw, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Products in 8-bit integers                                                */
+/* ------------------------------------------------------------------------ */
+
+/* Codes are signed bytes (int8_t); every row of activations (token) and every
+ * output channel (row of W) has one fp32 scale.  The product
+ *   c[m][n] = bf16( fp32(sum_k aq[m][k] * wq[n][k]) * as[m] * ws[n] )
+ * sums in 32-bit integers, exactly, so every launch of a shape gives the same bits; the
+ * sum becomes fp32, is multiplied by as[m], then by ws[n], and is rounded to bf16.
+ * K is a multiple of 128 below 2^17 (with which no sum of codes -128..127 overflows),
+ * N of 16.  In these calls and the router's below, no output and no workspace may
+ * overlap an input, another output or the workspace: ARG. */
+
+/* Rows of bf16 to codes, one scale a row: activations per token, or a weight's
+ * output channels at load time.  In fp32, ties to even:
+ *   b = max(max_k |x[k]|, 1e-10f), s = b / 127, q[k] = rint(x[k] * (127 / b)).
+ * A row that holds an infinity or a NaN gets the scale NaN and codes 0, so that its
+ * product is NaN.
+ *   x [rows][K] bf16 -> q [rows][K], s [rows].
+ * Errors: NULLPTR; SHAPE if rows < 0 or >= 2^31, or K is not a positive multiple of 128 below
+ * 2^17; ALIGN; ARG for an overlap; DEVICE; LAUNCH.  rows = 0 launches nothing. */
+int r9k_quant_i8(const uint16_t *x, int64_t rows, int64_t K, int8_t *q, float *s, void *stream);
+
+/* The packed copy that the products read, in the byte order of r9k_pack_weight (N a
+ * multiple of 16 here); scales stay as they are.  Experts' weights [E][N][K] are packed
+ * as one weight of E * N rows.  Once, at load time.
+ *   wq [N][K] -> wp [N*K].
+ * Errors: NULLPTR; SHAPE if N is not a positive multiple of 16, K as above, or N * K is 2^36 or
+ * more; ALIGN; ARG for an overlap; DEVICE; LAUNCH. */
+int r9k_pack_weight_i8(const int8_t *wq, int64_t N, int64_t K, int8_t *wp, void *stream);
+
+/* Workspace bytes that r9k_gemm_i8 and r9k_gemm_i8_qa need for this shape (host
+ * only; 0 for M = 0).  Needs no initialisation; calls sharing one must not overlap in time.
+ * Errors: NULLPTR (bytes); SHAPE as for the calls. */
+int r9k_gemm_i8_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes);
+
+/* The product of codes, any number of rows.
+ *   aq [M][K], as [M], wp packed, ws [N] -> c [M][N] bf16.
+ * Errors: NULLPTR (a workspace too, where one is needed); SHAPE if M < 0 or > 2^24, K as above, or N is
+ * not a positive multiple of 16 up to 2^24; ALIGN; WORKSPACE; ARG for an overlap; DEVICE; LAUNCH.
+ * M = 0 launches nothing. */
+int r9k_gemm_i8(const int8_t *aq, const float *as, int64_t M, int64_t K, const int8_t *wp, const float *ws, int64_t N,
+                uint16_t *c, void *workspace, size_t ws_bytes, void *stream);
+
+/* r9k_quant_i8 of bf16 activations and r9k_gemm_i8 in one call, with the bits of the two.
+ *   a [M][K] bf16 -> c [M][N] bf16.
+ * Errors: as r9k_gemm_i8. */
+int r9k_gemm_i8_qa(const uint16_t *a, int64_t M, int64_t K, const int8_t *wp, const float *ws, int64_t N, uint16_t *c,
+                   void *workspace, size_t ws_bytes, void *stream);
+
+/* The experts' products on rows sorted by expert: as r9k_moe_gemm_w4, on codes.  Rows
+ * [offsets[e], offsets[e+1]) of c are the product with expert e's weight; with
+ * R9K_ACT_SILU_MUL c [R][N/2] = bf16( silu(gate) * up ), gate and up in fp32.  Activation row
+ * of row r: r (src NULL), or src[r] / topk.  Rows of c from offsets[E] on are left as they were.
+ *   aq [arows][K], as [arows], src [R] int32, offsets [E+1] int32 (device, ascending,
+ *   at most R); wp: E weights of N rows packed as one, ws [E][N] -> c.
+ * offsets and src are device data the host cannot check: offsets are held to
+ * [0, R], and an index outside a reads row 0.
+ * Errors: NULLPTR (aq, as, offsets, wp, ws, c); SHAPE if R < 0, arows < 1 (with R > 0), E < 1 or
+ * > 2048, topk < 1, K as above, N not a positive multiple of 16 (of 32 with silu), R > arows *
+ * topk with src, or R > arows without; ARG for an unknown act or an overlap; ALIGN; DEVICE;
+ * LAUNCH.  R = 0 launches nothing. */
+int r9k_moe_gemm_i8(const int8_t *aq, const float *as, int64_t arows, const int32_t *src, int64_t topk,
+                    const int32_t *offsets, int64_t E, int64_t R, int64_t K, const int8_t *wp, const float *ws,
+                    int64_t N, int act, uint16_t *c, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* The router in training                                                    */
+/* ------------------------------------------------------------------------ */
+
+/* Workspace bytes of r9k_moe_balance_loss (host only).  Needs no initialisation;
+ * calls sharing one must not overlap in time.
+ * Errors: NULLPTR (bytes); SHAPE as for the call. */
+int r9k_moe_balance_loss_workspace(int64_t T, int64_t E, int64_t topk, size_t *bytes);
+
+/* The load balance loss of a routed batch, and the experts' counts.  Over the n tokens
+ * that mask keeps (mask NULL: all), with p[t] the softmax of logits[t] over all E experts in
+ * fp32:
+ *   counts[e] = slots of kept tokens with topk_ids[t][j] = e,   counts[E] = n,
+ *   psum[e]   = sum_t p[t][e],
+ *   loss      = E / (topk * n^2) * sum_e counts[e] * psum[e]   (0 where n = 0),
+ * which is 1 where the load is even.  An id outside [0, E) counts nowhere.  A logit of -inf has
+ * p = 0, also where all of a token's are; other logits that are not finite make the loss NaN.
+ * counts and psum may be added up over ranks for the loss of the whole batch.
+ *   logits [T][E] (dtype), topk_ids [T][topk] int32, mask [T] bytes (0: left out) ->
+ *   loss [1] fp32, counts [E+1] int32, psum [E] fp32.
+ * Errors: NULLPTR (all but mask; the workspace where one is needed); SHAPE if T < 0 or >= 2^24, E
+ * < 1 or > 2048, topk < 1 or > 64; ARG for an unknown dtype or an overlap; ALIGN (mask and loss
+ * too); WORKSPACE; DEVICE; LAUNCH.  T = 0 writes zeros. */
+int r9k_moe_balance_loss(const void *logits, int dtype, int64_t T, int64_t E, const int32_t *topk_ids, int64_t topk,
+                         const uint8_t *mask, float *loss, int32_t *counts, float *psum, void *workspace,
+                         size_t ws_bytes, void *stream);
+
+/* The gradient of r9k_moe_balance_loss for the logits, times gloss (the gradient of the
+ * loss, one fp32 on the device): with f[e] = E * counts[e] / (topk * n),
+ *   g[t][i] = gloss / n * p[t][i] * (f[i] - sum_e f[e] * p[t][e]),
+ * 0 for a token that mask leaves out, and 0 where n = counts[E] = 0.  counts is the forward
+ * call's, or its sum over ranks.  With gw, topk_ids and topk_w (all three or none) the
+ * gradient of r9k_moe_route_backward is added before the one rounding to the logits' type.
+ *   logits [T][E] (dtype), counts [E+1], mask [T], gw and topk_w [T][topk] fp32, topk_ids
+ *   [T][topk] -> glogits [T][E] (dtype).
+ * Errors: NULLPTR (gloss, logits, counts, glogits; one or two of gw, topk_ids and topk_w alone);
+ * otherwise as r9k_moe_balance_loss.  T = 0 launches nothing. */
+int r9k_moe_balance_loss_backward(const float *gloss, const void *logits, int dtype, int64_t T, int64_t E, int64_t topk,
+                                  const int32_t *counts, const uint8_t *mask, const float *gw, const int32_t *topk_ids,
+                                  const float *topk_w, void *glogits, void *stream);
+
+/* The gradient of r9k_moe_route for the logits: with d[j] = topk_w[t][j] * (gw[t][j] -
+ * sum_i topk_w[t][i] * gw[t][i]),
+ *   glogits[t][e] = sum of d[j] over j with topk_ids[t][j] = e, j ascending.
+ * An id outside [0, E) takes part in the inner sum alone.
+ *   gw, topk_w [T][topk] fp32, topk_ids [T][topk] int32 -> glogits [T][E] fp32.
+ * Errors: NULLPTR; SHAPE if T < 0 or >= 2^24, E < 1 or > 65536, topk < 1 or > 64; ARG for an
+ * overlap; ALIGN; DEVICE; LAUNCH.  T = 0 launches nothing. */
+int r9k_moe_route_backward(const float *gw, const int32_t *topk_ids, const float *topk_w, int64_t T, int64_t E,
+                           int64_t topk, float *glogits, void *stream);
 
 #if defined(__GNUC__) || defined(__clang__)
 #pragma GCC visibility pop
