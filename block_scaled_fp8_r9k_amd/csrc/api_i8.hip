@@ -9,6 +9,13 @@
 
 using namespace r9k;
 
+namespace r9k {
+I8Tuning &i8_tuning() {
+    static I8Tuning t{};
+    return t;
+}
+}  // namespace r9k
+
 extern "C" {
 
 // ---- products -------------------------------------------------------------------
@@ -39,18 +46,23 @@ int r9k_pack_weight_i8(const int8_t *wq, int64_t N, int64_t K, int8_t *wp, void 
 struct I8Layout {
     size_t scales, part, total;
 };
-static I8Layout i8_layout(int64_t M, int64_t K, int64_t N, const I8Cfg &c) {
-    I8Layout l;
-    l.scales = align_up((size_t)(M * K), 256);
-    l.part = l.scales + align_up((size_t)M * 4, 256);
-    l.total = l.part + (c.ksplit > 1 ? align_up((size_t)c.ksplit * (size_t)(M * N) * 4, 256) : 0);
+static I8Layout i8_layout(int64_t M, int64_t K, int64_t N, const I8Plan &p) {
+    I8Layout l{};
+    if (!p.fused) {
+        l.scales = align_up((size_t)(M * K), 256);
+        l.part = l.scales + align_up((size_t)M * 4, 256);
+    }
+    l.total = l.part + (p.ksplit() > 1 ? align_up((size_t)p.ksplit() * (size_t)(M * N) * 4, 256) : 0);
     return l;
+}
+static hipError_t launch_i8(const I8Args &a, const I8Plan &p, hipStream_t s) {
+    return p.tile ? launch_gemm_i8_tiled(a, p.tiled, s) : launch_gemm_i8(a, p.cfg, s);
 }
 
 int r9k_gemm_i8_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes) {
     if (!bytes) return R9K_ERR_NULLPTR;
     if (M < 0 || M > MAX_DIM || !i8_shape(N, K, 16)) return R9K_ERR_SHAPE;
-    *bytes = M ? i8_layout(M, K, N, i8_config(M, K, N, 0, false)).total : 0;
+    *bytes = M ? i8_layout(M, K, N, i8_plan(M, K, N, 0, false)).total : 0;
     return R9K_OK;
 }
 
@@ -62,9 +74,9 @@ static int run_gemm_i8(const uint16_t *a, const int8_t *aq, const float *as, int
         !aligned16(workspace))
         return R9K_ERR_ALIGN;
     if (M == 0) return R9K_OK;
-    const I8Cfg cfg = i8_config(M, K, N, 0, false);
-    const I8Layout l = i8_layout(M, K, N, cfg);
-    const bool need = a || cfg.ksplit > 1;
+    const I8Plan plan = i8_plan(M, K, N, 0, false);
+    const I8Layout l = i8_layout(M, K, N, plan);
+    const bool quant = a && !plan.fused, need = quant || plan.ksplit() > 1;
     if (need && !workspace) return R9K_ERR_NULLPTR;
     if (need && ws_bytes < l.total) return R9K_ERR_WORKSPACE;
     if (clash({{c, 2 * M * N}, {need ? workspace : nullptr, (int64_t)l.total}},
@@ -72,14 +84,15 @@ static int run_gemm_i8(const uint16_t *a, const int8_t *aq, const float *as, int
         return R9K_ERR_ARG;
     if (int rc = check_device()) return rc;
     uint8_t *w = (uint8_t *)workspace;
-    if (a) {
+    if (quant) {
         aq = (const int8_t *)w;
         as = (const float *)(w + l.scales);
         const hipError_t err = launch_quant_i8(a, M, K, (int8_t *)w, (float *)(w + l.scales), s);
         if (err != hipSuccess) return launch_result(err);
     }
-    I8Args g{aq, as, wp, ws, c, M, K, N, nullptr, nullptr, 1, 1, M, 0, need ? (int32_t *)(w + l.part) : nullptr};
-    return launch_result(launch_gemm_i8(g, cfg, s));
+    I8Args g{aq, as, wp, ws, c, M, K, N, nullptr, nullptr, 1, 1, M, 0, need ? (int32_t *)(w + l.part) : nullptr,
+             quant ? nullptr : a};
+    return launch_result(launch_i8(g, plan, s));
 }
 
 int r9k_gemm_i8(const int8_t *aq, const float *as, int64_t M, int64_t K, const int8_t *wp, const float *ws, int64_t N,
@@ -111,8 +124,40 @@ int r9k_moe_gemm_i8(const int8_t *aq, const float *as, int64_t arows, const int3
         return R9K_ERR_ARG;
     if (R == 0) return R9K_OK;
     if (int rc = check_device()) return rc;
-    I8Args g{aq, as, wp, ws, c, R, K, N, offsets, src, E, topk, arows, silu ? 1 : 0, nullptr};
-    return launch_result(launch_gemm_i8(g, i8_config(R, K, N, E, silu), (hipStream_t)stream));
+    I8Args g{aq, as, wp, ws, c, R, K, N, offsets, src, E, topk, arows, silu ? 1 : 0, nullptr, nullptr};
+    return launch_result(launch_i8(g, i8_plan(R, K, N, E, silu), (hipStream_t)stream));
+}
+
+int r9k_i8_plan(int64_t M, int64_t K, int64_t N, int64_t E, int act, int *plan) {
+    if (!plan) return R9K_ERR_NULLPTR;
+    const bool silu = act == R9K_ACT_SILU_MUL;
+    if (M < 0 || E < 0 || E > MOE_MAX_E || M > (E ? 128 * MAX_DIM - 1 : MAX_DIM) || !i8_shape(N, K, silu ? 32 : 16))
+        return R9K_ERR_SHAPE;
+    if (act != R9K_ACT_NONE && !(silu && E)) return R9K_ERR_ARG;
+    std::fill(plan, plan + R9K_I8_PLAN_INTS, 0);
+    if (M == 0) return R9K_OK;
+    const I8Plan p = i8_plan(M, K, N, E, silu);
+    const int *tile = I8_TILES[p.tiled.shape];
+    const int tiled[] = {R9K_I8_TILED, tile[0], tile[1], 0, p.tiled.ksplit, 0, 0};
+    const int stream[] = {R9K_I8_STREAM, p.cfg.nt, p.cfg.wn, p.cfg.wk, p.cfg.ksplit, p.cfg.mt, p.fused};
+    std::copy_n(p.tile ? tiled : stream, R9K_I8_PLAN_INTS, plan);
+    return R9K_OK;
+}
+
+int r9k_set_i8_plan(int kernel, int a, int b, int c, int ksplit, int rows) {
+    if (ksplit < 0) return R9K_ERR_ARG;
+    const bool shape = a || b || c || rows;
+    if (kernel == R9K_I8_STREAM) {
+        if (shape ? !i8_stream_shape(rows, a, b, c) : ksplit != 0) return R9K_ERR_ARG;
+    } else if (kernel == R9K_I8_TILED) {
+        bool known = !shape;
+        for (const auto &t : I8_TILES) known |= t[0] == a && t[1] == b && !c && !rows;
+        if (!known) return R9K_ERR_ARG;
+    } else if (kernel != R9K_I8_AUTO || shape || ksplit) {
+        return R9K_ERR_ARG;
+    }
+    i8_tuning() = I8Tuning{kernel, a, b, c, rows, ksplit};
+    return R9K_OK;
 }
 
 // ---- the router ------------------------------------------------------------------

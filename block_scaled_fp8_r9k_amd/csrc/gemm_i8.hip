@@ -17,13 +17,18 @@
 // columns that belong to them.
 #include <algorithm>
 
+#include "r9k.h"
 #include "i8_device.h"
 #include "i8_internal.h"
 
 namespace r9k {
 
-template <int MT, int NT, int D>
-__global__ __launch_bounds__(512) void k_gemm_i8(I8Args p) {
+// 512-value units that a wave quantises, held in registers
+static constexpr int I8_QA_UNITS = 4;
+
+template <int MT, int NT, int D, bool LONG, bool QA>
+__global__ __launch_bounds__(MT * NT == 1 ? 1024 : 512) void k_gemm_i8(I8Args p) {
+    static_assert(!QA || MT == 1, "activations are quantised up to 16 rows");
     extern __shared__ __align__(16) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
     const int nw = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -58,26 +63,39 @@ __global__ __launch_bounds__(512) void k_gemm_i8(I8Args p) {
         }
     }
 
+    // QA: the rows are quantised here, from bf16.  A unit is 512 values of a row, one 16-byte load of a
+    // wave; the loads go out before the weights'.
+    const int segs = (int)((p.K + 511) / 512), units = QA ? rows * segs : 0, K = (int)p.K;
+    uint4 av[QA ? I8_QA_UNITS : 1];
+    if constexpr (QA) {
+#pragma unroll
+        for (int i = 0; i < I8_QA_UNITS; ++i) {
+            const int u = wave + i * nw, r = u / segs, k = (u - r * segs) * 512 + 8 * lane;
+            av[i] = u < units && k < K ? *(const uint4 *)(p.a + (int64_t)(r0 + r) * K + k) : make_uint4(0, 0, 0, 0);
+        }
+    }
     // activation rows of the lane's row in each row tile; an index that points outside the
     // activations means row 0
     uint32_t aoff[MT];
     float as[MT];
+    if constexpr (!QA) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int r = r0 + min(16 * m + l16, rows - 1);
-        uint32_t row = r;
-        if (p.src) {
-            row = w4_div_topk((uint32_t)p.src[r], (uint32_t)p.topk, p.tmagic);
-            if (row >= (uint32_t)p.arows) row = 0;
+        for (int m = 0; m < MT; ++m) {
+            const int r = r0 + min(16 * m + l16, rows - 1);
+            uint32_t row = r;
+            if (p.src) {
+                row = w4_div_topk((uint32_t)p.src[r], (uint32_t)p.topk, p.tmagic);
+                if (row >= (uint32_t)p.arows) row = 0;
+            }
+            as[m] = p.as[row];
+            aoff[m] = (p.src ? row : row - (uint32_t)r0) * (uint32_t)p.K + 16 * q;
         }
-        as[m] = p.as[row];
-        aoff[m] = (p.src ? row : row - (uint32_t)r0) * (uint32_t)p.K + 16 * q;
     }
 
     // this wave's chunks [cb, ce).  Weight loads past ce lie behind the descriptors' end, return
     // zeros and move nothing, and so make no difference whatever activations meet them.
     const int kb = ks * p.span, ke = min(C, kb + p.span);
-    const int cb = kb + slice * p.cps, ce = min(ke, cb + p.cps);
+    const int cb = kb + slice * p.cps, ce = __builtin_amdgcn_readfirstlane(min(ke, cb + p.cps));
     __amdgpu_buffer_rsrc_t wd[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -93,13 +111,15 @@ __global__ __launch_bounds__(512) void k_gemm_i8(I8Args p) {
     for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[j][m] = v4i{0, 0, 0, 0};
-    v4i wr[D][NT][2], ar[D][MT][2];
+    v4i wr[D][NT][2], ar[QA ? 1 : D][MT][2];
     auto load = [&](int c, int d) {
+        if constexpr (!QA) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                ar[d][m][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(ad, aoff[m] + c * 128 + 64 * h, 0, 0));
+                for (int h = 0; h < 2; ++h)
+                    ar[d][m][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(ad, aoff[m] + c * 128 + 64 * h, 0, 0));
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -107,18 +127,60 @@ __global__ __launch_bounds__(512) void k_gemm_i8(I8Args p) {
                 wr[d][j][h] = __builtin_bit_cast(v4i, load_buf_nt16(wd[j], 16 * lane + c * 2048 + 1024 * h));
     };
 #pragma unroll
-    for (int d = 0; d < D; ++d) load(cb + d, d);
-    for (int c = cb; c < ce; c += D) {
+    for (int d = 0; d < D; ++d) {
+        load(cb + d, d);
+        __builtin_amdgcn_sched_barrier(0);  // in the order of use
+    }
+    // QA: [rows][K] codes, rows 16 bytes apart so that a fragment read's fall on distinct banks, then the units' maxima
+    const uint8_t *al = lds;
+    if constexpr (QA) {
+        const int pitch = K + 16;
+        uint32_t *top = (uint32_t *)(lds + rows * pitch);
+        uint32_t *sums = top + units;  // the rows' scales
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) acc[j][m] = i8_mfma(wr[d][j][h], ar[d][m][h], acc[j][m]);
-            load(c + d + D, d);
+        for (int i = 0; i < I8_QA_UNITS; ++i) {
+            const uint32_t m = max64(absmax8_bits(av[i]));
+            if (wave + i * nw < units) top[wave + i * nw] = m;
         }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < I8_QA_UNITS; ++i) {
+            const int u = wave + i * nw, r = u / segs, k = (u - r * segs) * 512 + 8 * lane;
+            if (u >= units) break;
+            uint32_t m = 0;
+            for (int s = lane; s < segs; s += 64) m = max(m, top[r * segs + s]);
+            const I8Scale sc = i8_row_scale(max64(m));
+            if (k < K) *(uint2 *)(lds + r * pitch + k) = i8_quant8(av[i], sc);
+            if (u == r * segs) sums[r] = __float_as_uint(sc.s);
+        }
+        __syncthreads();
+        as[0] = __uint_as_float(sums[min(l16, rows - 1)]);
+        al = lds + min(l16, rows - 1) * pitch + 16 * q;
+    }
+    auto compute = [&](int c, int d) {
+        if constexpr (QA) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) ar[0][0][h] = *(const v4i *)(al + c * 128 + 64 * h);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) acc[j][m] = i8_mfma(wr[d][j][h], ar[QA ? 0 : d][m][h], acc[j][m]);
+    };
+    if constexpr (LONG) {
+        for (int c = cb; c < ce; c += D) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                if (c + d < ce) compute(c + d, d);
+                if (c + d + D < ce) load(c + d + D, d);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            if (cb + d < ce) compute(cb + d, d);
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -127,7 +189,8 @@ __global__ __launch_bounds__(512) void k_gemm_i8(I8Args p) {
 
     // the K slices' sums, in LDS; an item is one output tile of the CTA (with silu, a gate
     // tile and its up tile)
-    v4i *red = (v4i *)lds;  // [wave][tile][row tile][lane]
+    v4i *red = (v4i *)lds;  // [wave][tile][row tile][lane], where the codes were
+    if constexpr (QA) __syncthreads();
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -137,6 +200,11 @@ __global__ __launch_bounds__(512) void k_gemm_i8(I8Args p) {
     const int nt = p.silu ? NT / 2 : NT;
     const int otiles = p.silu ? tiles / 2 : tiles;
     const int outs = wn * nt * MT;
+    // the block's rows of c or of this split's sums, less than 2^32 bytes; a store past the last
+    // row falls behind the descriptor's end and is dropped (no lane is masked)
+    void *first = p.ksplit > 1 ? (void *)(p.part + ((int64_t)ks * p.M + r0) * p.N) : (void *)(p.c + r0 * ldc);
+    const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
+        first, (short)0, (int)((uint32_t)rows * (uint32_t)ldc * (p.ksplit > 1 ? 4u : 2u)), 0x00020000);
     for (int it = wave; it < outs; it += nw) {
         const int w = it & (wn - 1), j = (it >> p.wnl) / MT, m = (it >> p.wnl) % MT;
         auto total = [&](int jj) {
@@ -144,11 +212,12 @@ __global__ __launch_bounds__(512) void k_gemm_i8(I8Args p) {
             for (int s = 1; s < wk; ++s) x += red[(((s * wn + w) * NT + jj) * MT + m) * 64 + lane];
             return x;
         };
-        const int t = (bx * wn + w) * nt + j, r = 16 * m + l16;
-        if (t >= otiles || r >= rows) continue;
-        v4i x = total(j);
+        const int t = (bx * wn + w) * nt + j;
+        if (t >= otiles) continue;
+        const v4i x = total(j);
+        const uint32_t at = (uint32_t)(16 * m + l16) * (uint32_t)ldc + 16 * t + 4 * q;
         if (p.ksplit > 1) {
-            *(v4i *)(p.part + ((int64_t)ks * p.M + r0 + r) * p.N + 16 * t + 4 * q) = x;
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), out, 4 * at, 0, 0);
             continue;
         }
         float a = as[0];
@@ -161,7 +230,7 @@ __global__ __launch_bounds__(512) void k_gemm_i8(I8Args p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[i] = w4_silu_mul(y[i], u[i]);
         }
-        *(uint2 *)(p.c + (r0 + r) * ldc + 16 * t + 4 * q) = w4_bf16x4(y);
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(w4_v2u, w4_bf16x4(y)), out, 2 * at, 0, 0);
     }
 }
 
@@ -176,16 +245,55 @@ __global__ __launch_bounds__(256) void k_i8_reduce(const int32_t *__restrict__ p
     *(uint2 *)(c + i) = w4_bf16x4(i8_scale(x, as[i / N], *(const float4 *)(ws + i % N)));
 }
 
-I8Cfg i8_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
-    I8Cfg c{M <= (E ? 12 * E : 16) ? 1 : 2, silu ? 2 : 1, 1, 8, 1};
-    const int64_t C = K / 128, tiles = N / 16 / (silu ? 2 : 1);
-    while (c.wk > 1 && C < 2 * c.wk) c.wk /= 2;
-    const int64_t ctas = E ? tiles * E : tiles * ((M + 16 * c.mt - 1) / (16 * c.mt));
-    if (!E && ctas < 256 && C >= 64) c.ksplit = 2;
-    return c;
+hipError_t launch_i8_reduce(const I8Args &a, int ksplit, hipStream_t s) {
+    hipLaunchKernelGGL(k_i8_reduce, dim3((unsigned)((a.M * a.N / 4 + 255) / 256)), dim3(256), 0, s, a.part, a.as, a.ws,
+                       a.c, a.M, a.N, ksplit);
+    return hipGetLastError();
 }
 
-template <int MT, int NT>
+bool i8_stream_shape(int mt, int nt, int wn, int wk) {
+    const auto pow2 = [](int x, int most) { return x >= 1 && x <= most && (x & (x - 1)) == 0; };
+    return pow2(mt, 4) && pow2(nt, 2) && pow2(wn, 8) && pow2(wk, 16) && wn * wk <= (mt * nt == 1 ? 16 : 8);
+}
+
+I8Plan i8_plan(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
+    const I8Tuning &f = i8_tuning();
+    const int64_t C = K / 128;
+    I8Plan p{};
+    const double per = E ? (double)M / (double)E : (double)M;  // rows a weight
+    p.cfg = I8Cfg{per <= (E ? 12 : 16) ? 1 : per <= 32 ? 2 : 4, silu || per > 16 ? 2 : 1, 1, 8, 1};
+    if (p.cfg.mt > 1) p.cfg.wk = 4;
+    while (p.cfg.wk > 1 && C < 2 * p.cfg.wk) p.cfg.wk /= 2;
+    p.cfg.wn = std::max(1, 4 / p.cfg.wk);
+    p.tile = per > (E ? 32 : 128);
+    p.tiled = I8TiledCfg{I8_256X256, 1};
+    if (!E) {
+        const auto ctas = [&](int s) { return ((N + I8_TILES[s][0] - 1) / I8_TILES[s][0]) * ((M + I8_TILES[s][1] - 1) / I8_TILES[s][1]); };
+        if (ctas(I8_256X256) < 200) p.tiled.shape = ctas(I8_256X128) >= 200 ? I8_256X128 : I8_128X64;
+        if (p.tiled.shape == I8_128X64 && ctas(I8_128X64) < 256)
+            p.tiled.ksplit = (int)std::max<int64_t>(1, std::min<int64_t>(256 / ctas(I8_128X64), C / 4));
+    } else if (per < 192) {
+        p.tiled.shape = per > 64 ? I8_256X128 : I8_128X64;
+    }
+    if (f.kernel == R9K_I8_STREAM && f.a) {
+        p.cfg.nt = std::max(f.a, silu ? 2 : 1), p.cfg.wn = f.b, p.cfg.wk = f.c, p.cfg.mt = f.d;
+        p.tile = false;
+    }
+    if (f.kernel == R9K_I8_TILED && f.a)
+        for (int s = 0; s < I8_SHAPES; ++s)
+            if (I8_TILES[s][0] == f.a && I8_TILES[s][1] == f.b) p.tiled.shape = s;
+    if (f.kernel) p.tile = f.kernel == R9K_I8_TILED;
+    if (f.ksplit && !E && N < 1 << 22) (p.tile ? p.tiled.ksplit : p.cfg.ksplit) = (int)std::min<int64_t>(f.ksplit, C);
+    if (!p.tile) {  // no split without chunks
+        const int64_t span = (C + p.cfg.ksplit - 1) / p.cfg.ksplit;
+        p.cfg.ksplit = (int)((C + span - 1) / span);
+    }
+    const int64_t units = M * ((K + 511) / 512);
+    p.fused = !E && !p.tile && p.cfg.mt == 1 && M <= 16 && p.cfg.ksplit == 1 && units <= I8_QA_UNITS * p.cfg.wn * p.cfg.wk;
+    return p;
+}
+
+template <int MT, int NT, bool LONG, bool QA>
 static hipError_t launch_one(I8Args a, const I8Cfg &c, hipStream_t s) {
     constexpr int D = 4;
     const int64_t C = a.K / 128, RB = 16 * MT;
@@ -198,21 +306,31 @@ static hipError_t launch_one(I8Args a, const I8Cfg &c, hipStream_t s) {
     a.span = (int)((C + c.ksplit - 1) / c.ksplit);
     a.cps = (a.span + c.wk - 1) / c.wk;
     a.tmagic = a.topk > 1 ? (uint32_t)(((uint64_t(1) << 32) + a.topk - 1) / a.topk) : 0;
-    const size_t lds = (size_t)c.wn * c.wk * NT * MT * 1024;
-    if (nblk > 0x7fffffff / 512 || items > 65535 || lds > 64 * 1024) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_gemm_i8<MT, NT, D>), dim3((unsigned)nblk, (unsigned)items, (unsigned)c.ksplit),
+    size_t lds = (size_t)c.wn * c.wk * NT * MT * 1024;
+    if (QA) lds = std::max(lds, (size_t)(a.M * (a.K + 16) + a.M * ((a.K + 511) / 512) * 4 + a.M * 4));
+    if (nblk > 0x7fffffff / 1024 || items > 65535 || lds > 64 * 1024) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_gemm_i8<MT, NT, D, LONG, QA>), dim3((unsigned)nblk, (unsigned)items, (unsigned)c.ksplit),
                        dim3(64 * c.wn * c.wk), lds, s, a);
     return hipGetLastError();
 }
+template <int MT, int NT>
+static hipError_t launch_nt(const I8Args &a, const I8Cfg &c, hipStream_t s) {
+    const int64_t C = a.K / 128, span = (C + c.ksplit - 1) / c.ksplit;
+    const bool longer = (span + c.wk - 1) / c.wk > 4;
+    if constexpr (MT == 1) {
+        if (a.a) return longer ? launch_one<1, NT, true, true>(a, c, s) : launch_one<1, NT, false, true>(a, c, s);
+    }
+    return longer ? launch_one<MT, NT, true, false>(a, c, s) : launch_one<MT, NT, false, false>(a, c, s);
+}
+template <int MT>
+static hipError_t launch_mt(const I8Args &a, const I8Cfg &c, hipStream_t s) {
+    return c.nt == 1 ? launch_nt<MT, 1>(a, c, s) : launch_nt<MT, 2>(a, c, s);
+}
 
 hipError_t launch_gemm_i8(const I8Args &a, const I8Cfg &c, hipStream_t s) {
-    hipError_t err;
-    if (c.mt == 1) err = c.nt == 1 ? launch_one<1, 1>(a, c, s) : launch_one<1, 2>(a, c, s);
-    else err = c.nt == 1 ? launch_one<2, 1>(a, c, s) : launch_one<2, 2>(a, c, s);
+    const hipError_t err = c.mt == 1 ? launch_mt<1>(a, c, s) : c.mt == 2 ? launch_mt<2>(a, c, s) : launch_mt<4>(a, c, s);
     if (err != hipSuccess || c.ksplit == 1) return err;
-    hipLaunchKernelGGL(k_i8_reduce, dim3((unsigned)((a.M * a.N / 4 + 255) / 256)), dim3(256), 0, s, a.part, a.as, a.ws,
-                       a.c, a.M, a.N, c.ksplit);
-    return hipGetLastError();
+    return launch_i8_reduce(a, c.ksplit, s);
 }
 
 }  // namespace r9k

@@ -22,18 +22,42 @@ struct I8Args {
     int64_t E, topk, arows;
     int silu;                // 1: columns [0, N/2) gate, [N/2, N) up, c = silu(gate) * up
     int32_t *part;           // with a K split: sums [ksplit][M][N] (workspace)
+    const uint16_t *a;       // bf16 activations that the streaming kernel quantises itself (aq and as are not read)
     // set by the launchers
-    int ksplit, wnl, span, cps;  // CTAs along K; log2 of the waves along the columns; chunks a split, a wave's slice
-    uint32_t tmagic;             // ceil(2^32 / topk), 0 for topk = 1
+    int nblk, nrow, ksplit;  // tiled kernel: column blocks, row blocks; CTAs along K
+    int wnl, span, cps;      // streaming kernel: log2 of the waves along the columns; chunks a split, a wave's slice
+    uint32_t tmagic;         // ceil(2^32 / topk), 0 for topk = 1
 };
-struct I8Cfg {
-    int mt;      // row tiles of 16 a CTA
-    int nt;      // column tiles a wave
-    int wn, wk;  // waves along the columns, K slices
-    int ksplit;  // CTAs along K (dense products only)
+struct I8Cfg {       // the weight-streaming kernel
+    int mt;          // row tiles of 16 a CTA
+    int nt;          // column tiles a wave
+    int wn, wk;      // waves along the columns, K slices
+    int ksplit;      // CTAs along K (dense products only)
 };
-I8Cfg i8_config(int64_t M, int64_t K, int64_t N, int64_t E, bool silu);
+struct I8TiledCfg {  // the LDS-tiled kernel
+    int shape;       // I8_TILES
+    int ksplit;      // CTAs along K (dense products only)
+};
+struct I8Plan {
+    bool tile;       // the tiled kernel takes it
+    bool fused;      // bf16 activations are quantised in the streaming kernel
+    I8Cfg cfg;
+    I8TiledCfg tiled;
+    int ksplit() const { return tile ? tiled.ksplit : cfg.ksplit; }
+};
+// columns x rows of a CTA
+enum { I8_256X256, I8_256X128, I8_256X64, I8_128X128, I8_128X64, I8_128X32, I8_SHAPES };
+inline constexpr int I8_TILES[I8_SHAPES][2] = {{256, 256}, {256, 128}, {256, 64}, {128, 128}, {128, 64}, {128, 32}};
+// r9k_set_i8_plan's choice: kernel 0 (the planner's), R9K_I8_STREAM or R9K_I8_TILED, the shape (0: the planner's), the split
+struct I8Tuning {
+    int kernel, a, b, c, d, ksplit;
+};
+I8Tuning &i8_tuning();
+bool i8_stream_shape(int mt, int nt, int wn, int wk);  // one that the streaming kernel has
+I8Plan i8_plan(int64_t M, int64_t K, int64_t N, int64_t E, bool silu);
 hipError_t launch_gemm_i8(const I8Args &a, const I8Cfg &c, hipStream_t s);
+hipError_t launch_gemm_i8_tiled(const I8Args &a, const I8TiledCfg &c, hipStream_t s);
+hipError_t launch_i8_reduce(const I8Args &a, int ksplit, hipStream_t s);  // a split's sums, added and scaled
 
 // ---- the router's training operators (router.hip) ----
 struct BalanceArgs {

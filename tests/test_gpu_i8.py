@@ -207,7 +207,7 @@ def test_refusals(r9k):
             bad()
     for bad, code in ((lambda: r9k.quant_i8(torch.zeros((2, 96), dtype=torch.bfloat16, device="cuda")), -2),
                       (lambda: r9k.quant_i8(a, q=a.view(torch.int8).view(-1)[:512].view(2, 256)), -7),
-                      (lambda: r9k.gemm_i8_qa(a, p, ws, workspace=torch.empty(256, dtype=torch.uint8, device="cuda")), -6)):
+                      (lambda: r9k.gemm_i8_qa(acts(100, 256, 1).cuda(), p, ws, workspace=torch.empty(256, dtype=torch.uint8, device="cuda")), -6)):
         with pytest.raises(r9k.R9kError) as e:
             bad()
         assert e.value.code == code
