@@ -50,9 +50,10 @@ def test_workspace_queries(L):
     assert _need(L, 0, 128, 16) == (0, 0)
     for M, K, N in ((-1, 128, 16), ((1 << 24) + 1, 128, 16), (1, 64, 16), (1, 1 << 17, 16), (1, 128, 8), (1, 128, (1 << 24) + 16)):
         assert _need(L, M, K, N)[0] == -2
-    for M, K, N in ((1, 128, 16), (100, 4096, 4096), (4096, 4096, 12288)):
+    for M, K, N in ((100, 4096, 4096), (4096, 4096, 12288)):
         rc, b = _need(L, M, K, N)
         assert rc == 0 and b >= M * K + 4 * M and b % 256 == 0
+    assert _need(L, 1, 512, 1024) == (0, 0)                                     # quantised inside the product, no split
     b = c_size_t(0)
     q = L.r9k_moe_balance_loss_workspace
     assert q(1, 1, 1, None) == -1
@@ -84,7 +85,7 @@ def test_product_checks(L):
     bad[2] = 0
     assert f(*bad) == 0
     g = L.r9k_gemm_i8_qa
-    ok = [D16, 4, 256, F16, G16, 32, A16, W, big, S]
+    ok = [D16, 100, 256, F16, G16, 32, A16, W, big, S]
     for i in (0, 3, 4, 6, 7):
         bad = list(ok)
         bad[i] = NUL
@@ -92,7 +93,7 @@ def test_product_checks(L):
         bad[i] = ODD
         assert g(*bad) == -3, i
     bad = list(ok)
-    bad[8] = _need(L, 4, 256, 32)[1] - 1
+    bad[8] = _need(L, 100, 256, 32)[1] - 1
     assert g(*bad) == -6
     for i in (0, 3, 4, 6):                                                      # the workspace on a tensor
         bad = list(ok)
