@@ -938,7 +938,7 @@ def moe_balance_loss(logits, topk_ids, mask=None, loss=None, counts=None, psum=N
     po, pc, pp = _addr(loss, F32, "loss", dev, ()), _addr(counts, I32, "counts", dev, (E + 1,)), _addr(psum, F32, "psum", dev, (E,))
     pw, nb, keep = _scratch(workspace, need, dev, stream)
     if T == 0:  # no rows to read (empty tensors have no device address to pass)
-        pl = pi = pw
+        pl = pi = po
         pm = None
     rc = lib().r9k_moe_balance_loss(pl, _ROWS[logits.dtype], T, E, pi, topk, pm, po, pc, pp, pw, nb, _raw(stream, dev))
     if rc:

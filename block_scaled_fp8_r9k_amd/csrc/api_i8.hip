@@ -165,15 +165,10 @@ int r9k_set_i8_plan(int kernel, int a, int b, int c, int ksplit, int rows) {
 static int check_router_shape(int64_t T, int64_t E, int64_t topk, int64_t most) {
     return T < 0 || T >= MAX_BLOCKS || E < 1 || E > most || topk < 1 || topk > 64 ? R9K_ERR_SHAPE : R9K_OK;
 }
-static size_t balance_counts_at(int64_t T, int64_t E) { return align_up((size_t)balance_parts(T, E) * E * 4, 256); }
-static size_t balance_bytes(int64_t T, int64_t E) {
-    return balance_counts_at(T, E) + align_up((size_t)balance_parts(T, E) * (E + 1) * 4, 256);
-}
-
 int r9k_moe_balance_loss_workspace(int64_t T, int64_t E, int64_t topk, size_t *bytes) {
     if (!bytes) return R9K_ERR_NULLPTR;
     if (int rc = check_router_shape(T, E, topk, MOE_MAX_E)) return rc;
-    *bytes = balance_bytes(T, E);
+    *bytes = balance_workspace(T, E);
     return R9K_OK;
 }
 
@@ -186,17 +181,15 @@ int r9k_moe_balance_loss(const void *logits, int dtype, int64_t T, int64_t E, co
     if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(mask) || !aligned16(loss) || !aligned16(counts) ||
         !aligned16(psum) || !aligned16(workspace))
         return R9K_ERR_ALIGN;
-    const size_t need = balance_bytes(T, E);
+    const size_t need = balance_workspace(T, E);
+    if (need && !workspace) return R9K_ERR_NULLPTR;
+    if (ws_bytes < need) return R9K_ERR_WORKSPACE;
     if (clash({{loss, 4}, {counts, 4 * (E + 1)}, {psum, 4 * E}, {workspace, (int64_t)need}},
               {{logits, T * E * (dtype == R9K_F32 ? 4 : 2)}, {topk_ids, 4 * T * topk}, {mask, T}}))
         return R9K_ERR_ARG;
-    if (need && !workspace) return R9K_ERR_NULLPTR;
-    if (ws_bytes < need) return R9K_ERR_WORKSPACE;
     if (int rc = check_device()) return rc;
-    uint8_t *w = (uint8_t *)workspace;
-    const BalanceArgs a{logits, dtype == R9K_F32, T, E, topk, topk_ids, mask, loss, counts, psum, (float *)w,
-                        (int32_t *)(w + balance_counts_at(T, E))};
-    return launch_result(launch_balance_loss(a, (hipStream_t)stream));
+    const BalanceArgs a{logits, dtype == R9K_F32, T, E, topk, topk_ids, mask, loss, counts, psum};
+    return launch_result(launch_balance_loss(a, workspace, (hipStream_t)stream));
 }
 
 int r9k_moe_balance_loss_backward(const float *gloss, const void *logits, int dtype, int64_t T, int64_t E, int64_t topk,

@@ -69,11 +69,13 @@ struct BalanceArgs {
     float *loss;            // [1]
     int32_t *counts;        // [E + 1]
     float *psum;            // [E]
-    float *part_p;          // [parts][E] (workspace)
-    int32_t *part_c;        // [parts][E + 1]
+    // set by the launcher, in the workspace
+    float *part_p;          // the parts' sums
+    int32_t *part_c, *part_n, *ticket;
+    double *dots;
 };
-int balance_parts(int64_t T, int64_t E);
-hipError_t launch_balance_loss(const BalanceArgs &a, hipStream_t s);
+size_t balance_workspace(int64_t T, int64_t E);
+hipError_t launch_balance_loss(BalanceArgs a, void *workspace, hipStream_t s);
 struct RouterGradArgs {
     const float *gw;        // [T][topk], or NULL: the balance loss's part alone
     const int32_t *ids;

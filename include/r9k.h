@@ -677,7 +677,8 @@ int r9k_moe_balance_loss_workspace(int64_t T, int64_t E, int64_t topk, size_t *b
  *   psum[e]   = sum_t p[t][e],
  *   loss      = E / (topk * n^2) * sum_e counts[e] * psum[e]   (0 where n = 0),
  * which is 1 where the load is even.  An id outside [0, E) counts nowhere.  A logit of -inf has
- * p = 0, also where all of a token's are; other logits that are not finite make the loss NaN.
+ * p = 0, also where all of a token's are, and a p below 2^-126 may count as 0; other logits that are
+ * not finite make the loss NaN.
  * counts and psum may be added up over ranks for the loss of the whole batch.
  *   logits [T][E] (dtype), topk_ids [T][topk] int32, mask [T] bytes (0: left out) ->
  *   loss [1] fp32, counts [E+1] int32, psum [E] fp32.

@@ -43,16 +43,16 @@ def probs(logits):
     """Softmax in 64 bits (0 for a logit of -inf, also where all are), and a bound on the error of its fp32 value: the
     difference d to the maximum is off by u d and so, with one more, is exp, of the value; exp, the division and the product by
     8 u together; the sum of E terms by at most E u of itself and by its terms' own errors (depth-weighted, at most the
-    largest d that matters, 104: exp is below fp32's smallest value from there on, 2^-148 with the sum)."""
+    largest d that matters, 88: exp is below fp32's smallest normal value, 2^-126, from there on and may count as 0)."""
     x = logits.to(F64)
     mx = x.amax(1, keepdim=True)
     e = torch.where(x == -float("inf"), torch.zeros_like(x), torch.exp(x - mx))
     s = e.sum(1, keepdim=True)
     one = torch.where(s == 0, torch.ones_like(s), s)
-    d = torch.where(torch.isfinite(x), mx - x, torch.zeros_like(x)).clamp_max(104.0)
+    d = torch.where(torch.isfinite(x), mx - x, torch.zeros_like(x)).clamp_max(88.0)
     p = e / one
     mean = (p * d).sum(1, keepdim=True)
-    return p, p * (2 * (d + mean) + x.shape[1] + 8) * U + 2.0 ** -148
+    return p, p * (2 * (d + mean) + x.shape[1] + 8) * U + 2.0 ** -126
 
 
 def balance(logits, ids, mask=None):

@@ -20,7 +20,7 @@ def r9k():
     return m
 
 
-SHAPES = [(1, 1, 1), (1, 8, 2), (3, 2, 2), (5, 7, 3), (64, 8, 2), (100, 128, 8), (257, 60, 4), (1000, 256, 8), (333, 129, 5),
+SHAPES = [(1, 1, 1), (8193, 3, 1), (300, 520, 33), (1, 8, 2), (3, 2, 2), (5, 7, 3), (64, 8, 2), (100, 128, 8), (257, 60, 4), (1000, 256, 8), (333, 129, 5),
           (77, 512, 10), (50, 1000, 6), (130, 2048, 8), (31, 2047, 64), (2100, 16, 4), (9000, 64, 6), (40000, 10, 2)]
 
 
@@ -237,7 +237,7 @@ def test_refusals(r9k):
     big = torch.zeros((2, 4096)).cuda()
     for bad, code in ((lambda: r9k.moe_balance_loss(big, ids[:2]), -2),
                       (lambda: r9k.moe_balance_loss(x, torch.zeros((20, 65), dtype=torch.int32).cuda()), -2),
-                      (lambda: r9k.moe_balance_loss(x, ids, workspace=torch.empty(16, dtype=torch.uint8).cuda()), -6),
+                      (lambda: r9k.moe_balance_loss(*on_gpu(*batch(2100, 16, 2, "plain")[:2]), workspace=torch.empty(16, dtype=torch.uint8).cuda()), -6),
                       (lambda: r9k.moe_balance_loss_backward(gl, x, counts, 2, glogits=x), -7),     # in place
                       (lambda: r9k.moe_balance_loss_backward(gl, x, counts, 0), -2),
                       (lambda: r9k.moe_route_backward(gw, ids, w, 2, glogits=gw), -7),

@@ -60,6 +60,7 @@ def test_workspace_queries(L):
     for T, E, k in ((-1, 8, 2), (1 << 24, 8, 2), (8, 0, 2), (8, 2049, 2), (8, 8, 0), (8, 8, 65)):
         assert q(T, E, k, ctypes.byref(b)) == -2
     assert q((1 << 24) - 1, 2048, 64, ctypes.byref(b)) == 0 and 0 < b.value < 1 << 24
+    assert q(64, 8, 2, ctypes.byref(b)) == 0 and b.value == 0                   # one launch
 
 
 def test_product_checks(L):
@@ -140,7 +141,7 @@ def test_router_checks(L):
     big = 1 << 38
     f = L.r9k_moe_balance_loss
     V = [c_void_p(i << 40) for i in range(1, 9)]
-    ok = [V[0], 1, 20, 16, V[1], 2, V[2], V[3], V[4], V[5], V[6], big, S]
+    ok = [V[0], 1, 2000, 16, V[1], 2, V[2], V[3], V[4], V[5], V[6], big, S]
     for i in (0, 4, 7, 8, 9, 10):
         bad = list(ok)
         bad[i] = NUL
