@@ -2,14 +2,19 @@
 //
 // The same sums as the weight-streaming kernel (gemm_i8.hip), for row counts at which the
 // matrix instructions and not the weight bytes set the time.  C^T = W A^T: WN x WM waves,
-// each TN column tiles by TM row tiles of 16; per chunk of 128 K a stage in LDS holds the W
-// tile in packed order ([column tile][half][lane][16 bytes]) and the A tile (rows of 128
-// bytes), moved there straight from memory, NST - 1 chunks ahead.  Integer sums need no
-// promotion, so between the matrix instructions there are only the fragments' LDS reads.
-// 16-byte piece c of row r of the A tile lies at piece c ^ ((r >> 1) & 7), so that the 16
+// each TN column tiles by TM row tiles of 16; per half chunk of 64 K a stage in LDS holds the W
+// tile in packed order ([column tile][lane][16 bytes]) and the A tile (rows of 64
+// bytes), moved there straight from memory, NST - 1 stages ahead.  Integer sums need no
+// promotion, so between the matrix instructions there are only the fragments' LDS reads, in
+// a fixed order: a step multiplies one W fragment with the stage's TM A fragments, and asks for the W
+// fragment of two steps later and, spread over the stage, for the A fragments of the next.  The stage that
+// these come from has landed for every wave since the barrier before, so that no step waits for LDS
+// after a barrier.
+// 16-byte piece c of row r of the A tile lies at piece c ^ ((r >> 2) & 3), so that the 16
 // rows of a fragment read fall on distinct banks.
 #include <algorithm>
 #include <mutex>
+#include <utility>
 
 #include "i8_device.h"
 #include "i8_internal.h"
@@ -22,18 +27,27 @@ struct I8Tile {
     static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, NST = NST_;
     static constexpr int NW = WN * WM, THREADS = 64 * NW;
     static constexpr int BN = WN * TN * 16, BM = WM * TM * 16;  // output columns and rows of a CTA
-    static constexpr int WBYTES = BN * 128, ABYTES = BM * 128, STAGE = WBYTES + ABYTES;
-    static constexpr int WLOADS = BN / 8 / NW, ALOADS = BM / 8 / NW, LOADS = WLOADS + ALOADS;  // 1 KiB loads a wave
+    static constexpr int WBYTES = BN * 64, ABYTES = BM * 64, STAGE = WBYTES + ABYTES;
+    static constexpr int WLOADS = BN / 16 / NW, ALOADS = BM / 16 / NW, LOADS = WLOADS + ALOADS;  // 1 KiB loads a wave
     static constexpr int CPITCH = BN * 2 + 16;  // output tile rows in LDS
     static constexpr int SMEM = NST * STAGE > BM * CPITCH ? NST * STAGE : BM * CPITCH;
     static_assert(SMEM <= 160 * 1024, "LDS");
-    static_assert(WLOADS * NW * 8 == BN && ALOADS * NW * 8 == BM, "loads split evenly");
-    static_assert((NST - 2) * LOADS < 64, "vmcnt");
+    static_assert(WLOADS * NW * 16 == BN && ALOADS * NW * 16 == BM, "loads split evenly");
+    static_assert(NST >= 4 && NST <= 5 && TN % 2 == 0, "stages; a ring of W fragments whose places are constants");
 };
 template <int V>
 struct Const {
     static constexpr int value = V;
 };
+// f(Const<0>) ... f(Const<N - 1>)
+template <class F, int... I>
+__device__ __forceinline__ void each(F &&f, std::integer_sequence<int, I...>) {
+    (f(Const<I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F &&f) {
+    each(f, std::make_integer_sequence<int, N>{});
+}
 }  // namespace
 
 template <class T>
@@ -79,6 +93,7 @@ __global__ __launch_bounds__(T::THREADS, 1) void k_gemm_i8_tiled(I8Args p) {
     const int mt = min(TM, max(0, (rows - wm * TM * 16 + 15) >> 4));  // the wave's row tiles that hold rows
     const int ks = blockIdx.y;
     const int cb = (int)((int64_t)ks * C / p.ksplit), ce = (int)((int64_t)(ks + 1) * C / p.ksplit);
+    const int n = 2 * (ce - cb);  // stages
 
     // column tile i of wave column w; those past the last repeat it and are not stored
     auto col_tile = [&](int w, int i) {
@@ -95,31 +110,27 @@ __global__ __launch_bounds__(T::THREADS, 1) void k_gemm_i8_tiled(I8Args p) {
     };
 
     // this wave's share of a stage's loads: W instructions WLOADS wave + u, one half of a
-    // column tile's block each, and A instructions ALOADS wave + u, eight rows each
+    // column tile's block each, and A instructions ALOADS wave + u, sixteen rows each
     const int8_t *wsrc[T::WLOADS], *asrc[T::ALOADS];
 #pragma unroll
     for (int u = 0; u < T::WLOADS; ++u) {
-        const int idx = T::WLOADS * wave + u, t = idx >> 1;
-        wsrc[u] = p.wp + (((int64_t)e * tiles + col_tile(t / TN, t % TN)) * C + cb) * 2048 + (idx & 1) * 1024;
+        const int t = T::WLOADS * wave + u;
+        wsrc[u] = p.wp + (((int64_t)e * tiles + col_tile(t / TN, t % TN)) * C + cb) * 2048 + 16 * lane;
     }
 #pragma unroll
     for (int u = 0; u < T::ALOADS; ++u) {
-        const int row = 8 * (T::ALOADS * wave + u) + (lane >> 3), piece = (lane & 7) ^ ((row >> 1) & 7);
+        const int row = 16 * (T::ALOADS * wave + u) + (lane >> 2), piece = (lane & 3) ^ ((row >> 2) & 3);
         asrc[u] = p.aq + source_row(r0 + row) * p.K + cb * 128 + 16 * piece;
     }
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(w4_lds_addr(lds));
-    auto issue = [&](int st) {
-        const uint32_t sw = lds0 + st * T::STAGE + T::WLOADS * wave * 1024;
-        const uint32_t sa = lds0 + st * T::STAGE + T::WBYTES + T::ALOADS * wave * 1024;
-#pragma unroll
-        for (int u = 0; u < T::WLOADS; ++u) {
-            w4_load16(wsrc[u], 16u * lane, sw + u * 1024);
-            wsrc[u] += 2048;
-        }
-#pragma unroll
-        for (int u = 0; u < T::ALOADS; ++u) {
-            w4_load16(asrc[u], sa + u * 1024);
-            asrc[u] += 128;
+    auto issue = [&](int st, auto load) {  // the wave's load instruction `load` of a stage
+        constexpr int u = decltype(load)::value, v = u - T::WLOADS;
+        if constexpr (u < T::WLOADS) {
+            w4_load16(wsrc[u], lds0 + st * T::STAGE + (T::WLOADS * wave + u) * 1024);
+            wsrc[u] += 1024;
+        } else if constexpr (u < T::LOADS) {
+            w4_load16(asrc[v], lds0 + st * T::STAGE + T::WBYTES + (T::ALOADS * wave + v) * 1024);
+            asrc[v] += 64;
         }
     };
 
@@ -128,53 +139,90 @@ __global__ __launch_bounds__(T::THREADS, 1) void k_gemm_i8_tiled(I8Args p) {
     for (int i = 0; i < TN; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+    // the scales of the wave's columns and rows, on their way before the first stage
+    float4 ws[TN];
+    float as[TM];
+    if (p.ksplit == 1) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i) ws[i] = *(const float4 *)(p.ws + (int64_t)e * p.N + 16 * col_tile(wn, i) + 4 * q);
+#pragma unroll
+        for (int j = 0; j < TM; ++j) as[j] = p.as[source_row(r0 + wm * TM * 16 + l16 + 16 * j)];
+    }
 
-    // fragment addresses inside a stage: column tile i, half h at wfo + 2048 i + 1024 h; row
-    // tile j, half h at (afo ^ 64 h) + 2048 j (rows 16 apart keep their order of pieces)
-    const int wfo = wn * TN * 2048 + 16 * lane;
+    // fragment addresses inside a stage: column tile i at wfo + 1024 i, row tile j at afo + 1024 j
+    const int wfo = wn * TN * 1024 + 16 * lane;
     const int arow = wm * TM * 16 + l16;
-    const int afo = T::WBYTES + arow * 128 + ((q ^ ((arow >> 1) & 7)) << 4);
+    const int afo = T::WBYTES + arow * 64 + ((q ^ ((arow >> 2) & 3)) << 4);
 
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // from here on only the stages' loads are counted
 #pragma unroll
     for (int k = 0; k < NST - 1; ++k)
-        if (cb + k < ce) issue(k);
-    auto chunk = [&](auto row_tiles, int c, auto stage) {
-        constexpr int MT = decltype(row_tiles)::value, st = decltype(stage)::value;
-        // this chunk's stage has landed: the wave's loads issued after it are those of the NST - 2 chunks behind it
-        // (fewer at the end: then wait for all)
-        if (c + NST - 2 < ce) w4_wait_vm<(NST - 2) * T::LOADS>();
+        if (k < n) each<T::LOADS>([&](auto u) { issue(k, u); });
+    // W fragments in a ring of four, two steps ahead; A fragments of this stage and the next
+    v4i wf[4], af[2][TM];
+    // at most `stages` stages' loads of the wave are in flight
+    auto wait = [&](int stages) {
+        if (NST > 4 && stages >= 3) w4_wait_vm<3 * T::LOADS>();
+        else if (stages >= 2) w4_wait_vm<2 * T::LOADS>();
+        else if (stages == 1) w4_wait_vm<T::LOADS>();
         else w4_wait_vm<0>();
-        __syncthreads();
-        if (c + NST - 1 < ce) issue((st + NST - 1) % NST);
-        const uint8_t *sb = lds + st * T::STAGE;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            v4i af[MT ? MT : 1];
-#pragma unroll
-            for (int j = 0; j < MT; ++j) af[j] = *(const v4i *)(sb + (afo ^ (64 * h)) + 2048 * j);
-            if (MT == 0) continue;
-#pragma unroll
-            for (int i = 0; i < TN; ++i) {
-                const v4i wf = *(const v4i *)(sb + wfo + 2048 * i + 1024 * h);
-#pragma unroll
-                for (int j = 0; j < MT; ++j) acc[i][j] = i8_mfma(wf, af[j], acc[i][j]);
-            }
-        }
     };
-    auto chunks = [&](auto row_tiles) {
-        for (int c = cb; c < ce; c += NST) {
-            chunk(row_tiles, c, Const<0>{});
-            if (c + 1 < ce) chunk(row_tiles, c + 1, Const<1>{});
-            if constexpr (NST == 3)
-                if (c + 2 < ce) chunk(row_tiles, c + 2, Const<2>{});
+    wait(min(NST - 2, n - 1));
+    __syncthreads();
+    int at = 0;  // the stage's place: c % NST
+    auto steps = [&](auto row_tiles, int c, auto parity, auto more) {
+        constexpr int MT = decltype(row_tiles)::value, odd = decltype(parity)::value, ahead = decltype(more)::value;
+        // the next stage has landed: the wave's loads issued after it are those of the NST - 3 stages behind it, fewer at
+        // the end
+        if (ahead) w4_wait_vm<(NST - 3) * T::LOADS>();
+        else wait(min(NST - 3, n - 2 - c));
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        const int next = at + 1 == NST ? 0 : at + 1, last = at == 0 ? NST - 1 : at - 1;
+        const uint8_t *sb = lds + at * T::STAGE, *sx = lds + next * T::STAGE;
+        each<TN>([&](auto step) {
+            constexpr int i = decltype(step)::value, PER = (T::LOADS + TN - 1) / TN;
+            if (ahead)  // the loads of the stage NST - 1 behind, spread over the steps
+                each<PER>([&](auto u) { issue(last, Const<PER * i + decltype(u)::value>{}); });
+            if constexpr (MT > 0) {
+                wf[(TN * odd + i + 2) & 3] = *(const v4i *)((i + 2 < TN ? sb + 1024 * (i + 2) : sx + 1024 * (i + 2 - TN)) + wfo);
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+                    if (j * TN / MT == i) af[odd ^ 1][j] = *(const v4i *)(sx + afo + 1024 * j);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < MT; ++j) acc[i][j] = i8_mfma(wf[(TN * odd + i) & 3], af[odd][j], acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        });
+        at = next;
+    };
+    auto run = [&](auto row_tiles) {
+        constexpr int MT = decltype(row_tiles)::value;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) af[0][j] = *(const v4i *)(lds + afo + 1024 * j);
+        wf[0] = *(const v4i *)(lds + wfo);
+        wf[1] = *(const v4i *)(lds + wfo + 1024);
+        int c = 0;
+        for (; c + NST < n; c += 2) {
+            steps(row_tiles, c, Const<0>{}, Const<1>{});
+            steps(row_tiles, c + 1, Const<1>{}, Const<1>{});
+        }
+        if (c + NST - 1 < n) {  // one more stage to ask for
+            steps(row_tiles, c, Const<0>{}, Const<1>{});
+            steps(row_tiles, c + 1, Const<1>{}, Const<0>{});
+            c += 2;
+        }
+        for (; c < n; c += 2) {
+            steps(row_tiles, c, Const<0>{}, Const<0>{});
+            steps(row_tiles, c + 1, Const<1>{}, Const<0>{});
         }
     };
     switch (mt) {  // only the row tiles that hold rows are computed
-        case 0: chunks(Const<0>{}); break;
-        case 1: chunks(Const<1>{}); break;
-        case 2: chunks(Const<(TM < 2 ? TM : 2)>{}); break;
-        default: chunks(Const<TM>{});
+        case 0: run(Const<0>{}); break;
+        case 1: run(Const<1>{}); break;
+        case 2: run(Const<(TM < 2 ? TM : 2)>{}); break;
+        default: run(Const<TM>{});
     }
 #pragma unroll
     for (int i = 0; i < TN; ++i)
@@ -195,24 +243,18 @@ __global__ __launch_bounds__(T::THREADS, 1) void k_gemm_i8_tiled(I8Args p) {
         }
         return;
     }
-    float as[TM];
-#pragma unroll
-    for (int j = 0; j < TM; ++j) as[j] = p.as[source_row(r0 + arow + 16 * j)];
     // through LDS, so that every store instruction writes whole pieces of rows
     __syncthreads();
     const int nt = p.silu ? TN / 2 : TN, wcols = nt * 16, cols = WN * wcols;
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
         if (16 * i >= wcols) continue;
-        const float *ws = p.ws + (int64_t)e * p.N + 16 * col_tile(wn, i) + 4 * q;
-        const float4 s = *(const float4 *)ws;
-        const float4 s2 = p.silu ? *(const float4 *)(ws + p.N / 2) : s;
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
-            v4f y = i8_scale(acc[i][j], as[j], s);
+            v4f y = i8_scale(acc[i][j], as[j], ws[i]);
             if constexpr (TN > 1) {
                 if (p.silu) {
-                    const v4f u = i8_scale(acc[(i + TN / 2) % TN][j], as[j], s2);
+                    const v4f u = i8_scale(acc[(i + TN / 2) % TN][j], as[j], ws[(i + TN / 2) % TN]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) y[r] = w4_silu_mul(y[r], u[r]);
                 }
@@ -259,12 +301,11 @@ static hipError_t launch_tile(I8Args a, const I8TiledCfg &c, hipStream_t s) {
 hipError_t launch_gemm_i8_tiled(const I8Args &a, const I8TiledCfg &c, hipStream_t s) {
     hipError_t err;
     switch (c.shape) {
-        case I8_256X256: err = launch_tile<I8Tile<2, 4, 8, 4, 2>>(a, c, s); break;
-        case I8_256X128: err = launch_tile<I8Tile<4, 2, 4, 4, 3>>(a, c, s); break;
-        case I8_256X64: err = launch_tile<I8Tile<4, 1, 4, 4, 3>>(a, c, s); break;
-        case I8_128X64: err = launch_tile<I8Tile<4, 1, 2, 4, 3>>(a, c, s); break;
-        case I8_128X128: err = launch_tile<I8Tile<4, 2, 2, 4, 3>>(a, c, s); break;
-        default: err = launch_tile<I8Tile<4, 1, 2, 2, 3>>(a, c, s); break;
+        case I8_256X256: err = launch_tile<I8Tile<2, 4, 8, 4, 5>>(a, c, s); break;
+        case I8_256X128: err = launch_tile<I8Tile<4, 2, 4, 4, 4>>(a, c, s); break;
+        case I8_256X64: err = launch_tile<I8Tile<4, 1, 4, 4, 4>>(a, c, s); break;
+        case I8_128X64: err = launch_tile<I8Tile<4, 1, 2, 4, 4>>(a, c, s); break;
+        default: err = launch_tile<I8Tile<4, 2, 2, 4, 4>>(a, c, s); break;
     }
     if (err != hipSuccess || c.ksplit == 1) return err;
     return launch_i8_reduce(a, c.ksplit, s);
