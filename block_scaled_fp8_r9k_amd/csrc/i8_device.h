@@ -62,6 +62,41 @@ __device__ __forceinline__ uint2 i8_quant8(uint4 v, const I8Scale &r) {
     return r.bad ? make_uint2(0, 0) : o;
 }
 
+// The experts' row blocks for a CTA that looks for several: up to 256 experts stay in the wave's registers, four a
+// lane, and only the first search goes to memory; with more, each does (w4_find_block, whose blocks these are).
+struct I8Blocks {
+    int o[5], incl;
+    __device__ __forceinline__ void load(const int32_t *offsets, int E, int R, int RB) {
+        const int e = 4 * (threadIdx.x & 63), sh = __builtin_ctz(RB);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) o[i] = offsets[min(e + i, E)];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) o[i] = min(max(o[i], 0), R);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n += (max(o[i + 1], o[i]) - o[i] + RB - 1) >> sh;
+        incl = w4_wave_scan(n);
+    }
+    __device__ __forceinline__ bool find(int item, int RB, int &e, int &r0, int &r1) const {
+        if (item >= __builtin_amdgcn_readlane(incl, 63)) return false;
+        const int sh = __builtin_ctz(RB), l = __builtin_ctzll(__ballot(incl > item));
+        if (l > 0) item -= __builtin_amdgcn_readlane(incl, l - 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int a = __builtin_amdgcn_readlane(o[i], l), z = __builtin_amdgcn_readlane(o[i + 1], l);
+            const int b = (max(z, a) - a + RB - 1) >> sh;
+            if (item < b) {
+                e = 4 * l + i;
+                r0 = a + (item << sh);
+                r1 = z;
+                return true;
+            }
+            item -= b;
+        }
+        return false;
+    }
+};
+
 // Maximum over the wave, the same in every lane.  Every lane must be active.
 __device__ __forceinline__ uint32_t max64(uint32_t v) {
     v = max16_dpp(v);

@@ -46,8 +46,8 @@ struct I8Plan {
     int ksplit() const { return tile ? tiled.ksplit : cfg.ksplit; }
 };
 // columns x rows of a CTA
-enum { I8_256X256, I8_256X128, I8_256X64, I8_128X128, I8_128X64, I8_SHAPES };
-inline constexpr int I8_TILES[I8_SHAPES][2] = {{256, 256}, {256, 128}, {256, 64}, {128, 128}, {128, 64}};
+enum { I8_256X256, I8_256X128, I8_128X128, I8_128X64, I8_SHAPES };
+inline constexpr int I8_TILES[I8_SHAPES][2] = {{256, 256}, {256, 128}, {128, 128}, {128, 64}};
 // r9k_set_i8_plan's choice: kernel 0 (the planner's), R9K_I8_STREAM or R9K_I8_TILED, the shape (0: the planner's), the split
 struct I8Tuning {
     int kernel, a, b, c, d, ksplit;

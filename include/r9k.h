@@ -654,7 +654,7 @@ int r9k_i8_plan(int64_t M, int64_t K, int64_t N, int64_t E, int act, int *plan);
  * wave (1, 2; with silu always 2), `b` waves along the columns, `c` along K (powers of two, at most 8
  * together, 16 for one tile of each kind) and `rows` row tiles a CTA (1, 2, 4), all four or none;
  * a split only with them.  R9K_I8_TILED: `a` columns and `b` rows of a CTA (256 x 256, 256 x 128,
- * 256 x 64, 128 x 128, 128 x 64, or 0 0).  ksplit: CTAs along K of dense products, clamped to
+ * 128 x 128, 128 x 64, or 0 0).  ksplit: CTAs along K of dense products, clamped to
  * K / 128; 0 for the planner's.  No choice changes a bit of any output.  The setting is process-wide,
  * changes the workspace a shape needs (query again after a change), and must change only
  * while no 8-bit product is being issued.

@@ -13,7 +13,7 @@ from tests.gpu_util import say
 from tests.test_gpu_i8 import acts, routing, weight
 
 pytestmark = pytest.mark.gpu
-TILES = [(256, 256), (256, 128), (256, 64), (128, 128), (128, 64)]
+TILES = [(256, 256), (256, 128), (128, 128), (128, 64)]
 STREAM = [(nt, wn, wk, mt) for nt, wn, wk, mt in itertools.product((1, 2), (1, 2, 4, 8), (1, 2, 4, 8, 16), (1, 2, 4))
           if wn * wk <= (16 if nt * mt == 1 else 8)]
 
