@@ -104,7 +104,7 @@ def lib() -> ctypes.CDLL:
         L.r9k_gemm_i8_qa.argtypes = L.r9k_gemm_fp8_block_qa.argtypes
         L.r9k_moe_gemm_i8.argtypes = [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64,
                                       c_void_p, c_void_p, c_int64, c_int, c_void_p, c_void_p]
-        L.r9k_i8_plan.argtypes = [c_int64] * 4 + [c_int, POINTER(c_int)]
+        L.r9k_i8_plan.argtypes = [c_int64] * 4 + [c_int, c_int, POINTER(c_int)]
         L.r9k_set_i8_plan.argtypes = [c_int] * 6
         L.r9k_moe_balance_loss_workspace.argtypes = [c_int64, c_int64, c_int64, POINTER(c_size_t)]
         L.r9k_moe_balance_loss.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int64] + [c_void_p] * 5 + [
@@ -889,12 +889,12 @@ def moe_gemm_i8(xq, xs, offsets, wp, ws, src=None, topk: int = 1, act: str = "no
 I8_AUTO, I8_STREAM, I8_TILED = 0, 1, 2
 
 
-def i8_plan(M: int, K: int, N: int, E: int = 0, act: str = "none") -> tuple:
+def i8_plan(M: int, K: int, N: int, E: int = 0, act: str = "none", quant: bool = False) -> tuple:
     """The launch of an 8-bit product (r9k_i8_plan): (I8_STREAM, column tiles a wave, waves along the columns, waves along
-    K, CTAs along K, row tiles a CTA, whether gemm_i8_qa quantises inside) or (I8_TILED, columns, rows, 0, CTAs along K, 0,
-    0).  E = 0: gemm_i8; else moe_gemm_i8 of M rows."""
+    K, CTAs along K, row tiles a CTA, whether the activations are quantised inside) or (I8_TILED, columns, rows, 0, CTAs
+    along K, 0, 0).  E = 0: gemm_i8, with quant gemm_i8_qa; else moe_gemm_i8 of M rows."""
     plan = (c_int * 7)()
-    _check(lib().r9k_i8_plan(M, K, N, E, _ACTS[act], plan), "r9k_i8_plan")
+    _check(lib().r9k_i8_plan(M, K, N, E, _ACTS[act], int(quant), plan), "r9k_i8_plan")
     return tuple(plan)
 
 

@@ -16,6 +16,28 @@ I8Tuning &i8_tuning() {
 }
 }  // namespace r9k
 
+static std::atomic<int> g_i8_setting{0};  // counts the changes of the plan control
+
+// The plan of a shape under the present setting, kept for each thread's last shapes:
+// planning takes longer than a launch.
+static const I8Plan &i8_plan(int64_t M, int64_t K, int64_t N, int64_t E, bool silu, bool quant, bool wide = false) {
+    struct Entry {
+        int64_t M = -1, K, N, E;
+        int setting, kind;
+        I8Plan plan;
+    };
+    static thread_local Entry table[64];
+    const int kind = silu + 2 * quant + 4 * wide, setting = g_i8_setting.load(std::memory_order_relaxed);
+    const uint64_t h = ((uint64_t)M * 0x9E3779B97F4A7C15u) ^ ((uint64_t)K * 0xC2B2AE3D27D4EB4Fu) ^
+                       ((uint64_t)N * 0x165667B19E3779F9u) ^ ((uint64_t)(8 * E + kind) * 0x27D4EB2F165667C5u);
+    Entry &t = table[h >> 58];
+    if (t.M != M || t.K != K || t.N != N || t.E != E || t.kind != kind || t.setting != setting) {
+        t.plan = i8_plan_new(M, K, N, E, silu, quant, wide);
+        t.M = M, t.K = K, t.N = N, t.E = E, t.kind = kind, t.setting = setting;
+    }
+    return t.plan;
+}
+
 extern "C" {
 
 // ---- products -------------------------------------------------------------------
@@ -46,9 +68,9 @@ int r9k_pack_weight_i8(const int8_t *wq, int64_t N, int64_t K, int8_t *wp, void 
 struct I8Layout {
     size_t scales, part, total;
 };
-static I8Layout i8_layout(int64_t M, int64_t K, int64_t N, const I8Plan &p) {
+static I8Layout i8_layout(int64_t M, int64_t K, int64_t N, const I8Plan &p, bool quant) {
     I8Layout l{};
-    if (!p.fused) {
+    if (quant && !p.fused) {
         l.scales = align_up((size_t)(M * K), 256);
         l.part = l.scales + align_up((size_t)M * 4, 256);
     }
@@ -62,7 +84,9 @@ static hipError_t launch_i8(const I8Args &a, const I8Plan &p, hipStream_t s) {
 int r9k_gemm_i8_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes) {
     if (!bytes) return R9K_ERR_NULLPTR;
     if (M < 0 || M > MAX_DIM || !i8_shape(N, K, 16)) return R9K_ERR_SHAPE;
-    *bytes = M ? i8_layout(M, K, N, i8_plan(M, K, N, 0, false)).total : 0;
+    *bytes = 0;
+    for (const bool quant : {false, true})
+        if (M) *bytes = std::max(*bytes, i8_layout(M, K, N, i8_plan(M, K, N, 0, false, quant), quant).total);
     return R9K_OK;
 }
 
@@ -74,12 +98,12 @@ static int run_gemm_i8(const uint16_t *a, const int8_t *aq, const float *as, int
         !aligned16(workspace))
         return R9K_ERR_ALIGN;
     if (M == 0) return R9K_OK;
-    const I8Plan plan = i8_plan(M, K, N, 0, false);
-    const I8Layout l = i8_layout(M, K, N, plan);
-    const bool quant = a && !plan.fused, need = quant || plan.ksplit() > 1;
-    if (need && !workspace) return R9K_ERR_NULLPTR;
-    if (need && ws_bytes < l.total) return R9K_ERR_WORKSPACE;
-    if (clash({{c, 2 * M * N}, {need ? workspace : nullptr, (int64_t)l.total}},
+    const I8Plan &plan = i8_plan(M, K, N, 0, false, a != nullptr);
+    const I8Layout l = i8_layout(M, K, N, plan, a != nullptr);
+    const bool quant = a && !plan.fused;
+    if (l.total && !workspace) return R9K_ERR_NULLPTR;
+    if (ws_bytes < l.total) return R9K_ERR_WORKSPACE;
+    if (clash({{c, 2 * M * N}, {workspace, (int64_t)l.total}},
               {{a, 2 * M * K}, {aq, M * K}, {as, 4 * M}, {wp, N * K}, {ws, 4 * N}}))
         return R9K_ERR_ARG;
     if (int rc = check_device()) return rc;
@@ -90,7 +114,7 @@ static int run_gemm_i8(const uint16_t *a, const int8_t *aq, const float *as, int
         const hipError_t err = launch_quant_i8(a, M, K, (int8_t *)w, (float *)(w + l.scales), s);
         if (err != hipSuccess) return launch_result(err);
     }
-    I8Args g{aq, as, wp, ws, c, M, K, N, nullptr, nullptr, 1, 1, M, 0, need ? (int32_t *)(w + l.part) : nullptr,
+    I8Args g{aq, as, wp, ws, c, M, K, N, nullptr, nullptr, 1, 1, M, 0, plan.ksplit() > 1 ? (int32_t *)(w + l.part) : nullptr,
              quant ? nullptr : a};
     return launch_result(launch_i8(g, plan, s));
 }
@@ -125,18 +149,18 @@ int r9k_moe_gemm_i8(const int8_t *aq, const float *as, int64_t arows, const int3
     if (R == 0) return R9K_OK;
     if (int rc = check_device()) return rc;
     I8Args g{aq, as, wp, ws, c, R, K, N, offsets, src, E, topk, arows, silu ? 1 : 0, nullptr, nullptr};
-    return launch_result(launch_i8(g, i8_plan(R, K, N, E, silu), (hipStream_t)stream));
+    return launch_result(launch_i8(g, i8_plan(R, K, N, E, silu, false, src && arows * K >= int64_t(1) << 32), (hipStream_t)stream));
 }
 
-int r9k_i8_plan(int64_t M, int64_t K, int64_t N, int64_t E, int act, int *plan) {
+int r9k_i8_plan(int64_t M, int64_t K, int64_t N, int64_t E, int act, int quant, int *plan) {
     if (!plan) return R9K_ERR_NULLPTR;
     const bool silu = act == R9K_ACT_SILU_MUL;
     if (M < 0 || E < 0 || E > MOE_MAX_E || M > (E ? 128 * MAX_DIM - 1 : MAX_DIM) || !i8_shape(N, K, silu ? 32 : 16))
         return R9K_ERR_SHAPE;
-    if (act != R9K_ACT_NONE && !(silu && E)) return R9K_ERR_ARG;
+    if ((act != R9K_ACT_NONE && !(silu && E)) || (quant != 0 && !(quant == 1 && E == 0))) return R9K_ERR_ARG;
     std::fill(plan, plan + R9K_I8_PLAN_INTS, 0);
     if (M == 0) return R9K_OK;
-    const I8Plan p = i8_plan(M, K, N, E, silu);
+    const I8Plan &p = i8_plan(M, K, N, E, silu, quant != 0);
     const int *tile = I8_TILES[p.tiled.shape];
     const int tiled[] = {R9K_I8_TILED, tile[0], tile[1], 0, p.tiled.ksplit, 0, 0};
     const int stream[] = {R9K_I8_STREAM, p.cfg.nt, p.cfg.wn, p.cfg.wk, p.cfg.ksplit, p.cfg.mt, p.fused};
@@ -148,7 +172,9 @@ int r9k_set_i8_plan(int kernel, int a, int b, int c, int ksplit, int rows) {
     if (ksplit < 0) return R9K_ERR_ARG;
     const bool shape = a || b || c || rows;
     if (kernel == R9K_I8_STREAM) {
-        if (shape ? !i8_stream_shape(rows, a, b, c) : ksplit != 0) return R9K_ERR_ARG;
+        bool known = !shape && ksplit == 0;
+        for (const auto &t : I8_STREAMS) known |= t[0] == rows && t[1] == a && t[2] == b && t[3] == c;
+        if (!known) return R9K_ERR_ARG;
     } else if (kernel == R9K_I8_TILED) {
         bool known = !shape;
         for (const auto &t : I8_TILES) known |= t[0] == a && t[1] == b && !c && !rows;
@@ -157,6 +183,7 @@ int r9k_set_i8_plan(int kernel, int a, int b, int c, int ksplit, int rows) {
         return R9K_ERR_ARG;
     }
     i8_tuning() = I8Tuning{kernel, a, b, c, rows, ksplit};
+    ++g_i8_setting;
     return R9K_OK;
 }
 

@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "r9k.h"
+#include "w4_internal.h"
 #include "i8_device.h"
 #include "i8_internal.h"
 
@@ -228,7 +229,7 @@ __global__ __launch_bounds__(MT * NT == 1 ? 1024 : 512) void k_gemm_i8(I8Args p)
         if (p.silu) {
             const v4f u = i8_scale(total(j + nt), a, *(const float4 *)(ws + p.N / 2));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = w4_silu_mul(y[i], u[i]);
+            for (int i = 0; i < 4; ++i) y[i] = i8_silu_mul(y[i], u[i]);
         }
         __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(w4_v2u, w4_bf16x4(y)), out, 2 * at, 0, 0);
     }
@@ -251,46 +252,112 @@ hipError_t launch_i8_reduce(const I8Args &a, int ksplit, hipStream_t s) {
     return hipGetLastError();
 }
 
-bool i8_stream_shape(int mt, int nt, int wn, int wk) {
-    const auto pow2 = [](int x, int most) { return x >= 1 && x <= most && (x & (x - 1)) == 0; };
-    return pow2(mt, 4) && pow2(nt, 2) && pow2(wn, 8) && pow2(wk, 16) && wn * wk <= (mt * nt == 1 ? 16 : 8);
+// ---- the launch of the least estimated time ------------------------------------
+//
+// Times in us, fitted (least squares of the logarithm) to every launch of 1563 dense shapes (1 to 1200 rows, K and N
+// from 256 to 14336) and 6036 of experts (4 to 256 of them, up to 4096 tokens, 128 to 4096 wide), in graphs, weights from
+// memory.  The launch picked is 3.6% behind the fastest of all on average (dense; 11% at the 90th percentile, at most
+// 41%), 3.3% with experts (10%, at most 42%).
+//
+// Streaming: a compute unit's busiest CTAs move W (weight blocks of 2 KiB) and A (activation blocks as large), and each of
+// its turns is as long as a wave's slice.  A split adds its sums and the reduce launch.  E.g. one row of 4096 x 14336: 11.9 us
+// in eight slices, 12.6 in four; of 4096 x 4096 5.5 and 6.1; 16 rows of 14336 x 4096 14.0 whole, 14.1 split.
+static double stream_us(const I8Cfg &c, int64_t M, int64_t K, int64_t N, int64_t E, bool silu, double blocks) {
+    const int64_t C = K / 128, span = (C + c.ksplit - 1) / c.ksplit, cps = (span + c.wk - 1) / c.wk, tiles = N / 16;
+    const int waves = c.wn * c.wk, per = (int)cps * (c.nt + c.mt);
+    const int vgprs = c.mt == 1 ? (c.nt == 1 ? 80 : 120) : c.mt == 2 ? (c.nt == 1 ? 120 : 160) : 248;
+    const double fit = std::max(1, std::min(8, 512 / vgprs * 4 / waves));  // CTAs that share a compute unit
+    const int64_t cols = (tiles + c.nt * c.wn - 1) / (c.nt * c.wn);
+    const double W = (double)(c.nt * c.wn * span), A = (double)(c.wn * c.mt * span), ctas = (double)(cols * c.ksplit) * blocks;
+    if (E) {
+        const int64_t RB = 16 * c.mt, grid = cols * ((M + std::min(E, M) * (RB - 1)) / RB);
+        const double rounds = std::max(1.0, ctas / 256.0), turns = std::max(1.0, ctas / 256.0 / fit);
+        const double us = 3.63 + 0.0097 * waves + rounds * (0.0581 * W + 0.0059 * A + 0.0421 * waves) + turns * (0.0947 * per + 0.386) +
+                          0.159 * std::max(0.0, (double)grid - ctas) / 256.0;
+        return std::max(us, 3.63 + 0.000304 * blocks * (double)(tiles * C));
+    }
+    const double rounds = std::ceil(ctas / 256.0), turns = std::ceil(ctas / 256.0 / fit);
+    double us = 2.535 + 0.0107 * waves + rounds * (W * (c.mt == 1 ? 0.0374 : c.mt == 2 ? 0.0589 : 0.086) + 0.0271 * A + 0.253) +
+                turns * 0.0357 * per;
+    if (c.ksplit > 1) us += 2.8 + 3.25e-6 * (double)(c.ksplit * M * N);
+    return us;
 }
 
-I8Plan i8_plan(int64_t M, int64_t K, int64_t N, int64_t E, bool silu) {
-    const I8Tuning &f = i8_tuning();
+// Tiled: a stage takes `alone` where its CTA has the compute unit to itself and `shared` for each of those that share it,
+// less where rows are missing; each tile its start and its outputs (2.4 times as long with silu).  E.g. 4096 x 4096 x 12288:
+// 178 us in tiles of 256 x 256, 220 in 256 x 128, 243 in 128 x 128; 1024 x 4096 x 14336 57, 75, 84; down of 128 experts,
+// 2048 tokens 69, 82, 86, and 85 in 128 x 64.  Streaming, 100 rows of 4096 x 4096 take 12.6 us, tiled 15.3.
+static double tiled_us(const I8TiledCfg &c, int64_t M, int64_t K, int64_t N, int64_t E, bool silu, double blocks) {
+    static constexpr double dense[][3] = {{0.596, 0.065, 4.22}, {0.419, 0.428, 2.12}, {0.264, 0.279, 1.03}, {0.303, 0.240, 0.0}};
+    static constexpr double moe[][3] = {{0.385, 0.689, 4.07}, {0.279, 0.375, 2.47}, {0.165, 0.262, 1.49}, {0.279, 0.197, 0.73}};
+    const int *t = I8_TILES[c.shape];
+    const double *u = E ? moe[c.shape] : dense[c.shape], fit = t[2];
+    const int64_t C = K / 128, stages = 2 * ((C + c.ksplit - 1) / c.ksplit);
+    const double load = (double)((N + t[0] - 1) / t[0] * c.ksplit) * blocks / 256.0;
+    const double fill = std::min(1.0, (double)M / blocks / t[1]), least = E ? 0.375 : 0.727;
+    const double busy = std::min(fit, E ? std::max(1.0, load) : std::ceil(load));
+    const double seq = load <= 2.0 * fit ? std::max(1.0, std::ceil(load / fit)) : load / fit + 0.5;
+    const double stage = std::max(u[0], u[1] * busy) * (least + (1.0 - least) * fill);
+    const double us = seq * ((double)stages * stage + u[2] * (silu ? 2.4 : 1.0));
+    if (E) return 4.28 + std::max(us, 2.0e-7 * (blocks * (double)(N * K) + (double)(M * (silu ? N : 2 * N))));
+    return 2.9 + us + (c.ksplit > 1 ? 3.25 + 2.0e-6 * (double)(c.ksplit * M * N) : 0.0);
+}
+
+// 512-value units of the rows that the streaming kernel quantises itself: as many as its waves hold
+static bool quant_fits(const I8Cfg &c, int64_t M, int64_t K) {
+    return c.mt == 1 && c.ksplit == 1 && M <= 16 && M * ((K + 511) / 512) <= I8_QA_UNITS * c.wn * c.wk;
+}
+
+I8Plan i8_plan_new(int64_t M, int64_t K, int64_t N, int64_t E, bool silu, bool quant, bool wide) {
+    const I8Tuning f = i8_tuning();
     const int64_t C = K / 128;
-    I8Plan p{};
-    const double per = E ? (double)M / (double)E : (double)M;  // rows a weight
-    p.cfg = I8Cfg{per <= (E ? 12 : 16) ? 1 : per <= 32 ? 2 : 4, silu || per > 16 ? 2 : 1, 1, 8, 1};
-    if (p.cfg.mt > 1) p.cfg.wk = 4;
-    while (p.cfg.wk > 1 && C < 2 * p.cfg.wk) p.cfg.wk /= 2;
-    p.cfg.wn = std::max(1, 4 / p.cfg.wk);
-    p.tile = per > (E ? 32 : 128);
-    p.tiled = I8TiledCfg{I8_256X256, 1};
-    if (!E) {
-        const auto ctas = [&](int s) { return ((N + I8_TILES[s][0] - 1) / I8_TILES[s][0]) * ((M + I8_TILES[s][1] - 1) / I8_TILES[s][1]); };
-        if (ctas(I8_256X256) < 200) p.tiled.shape = ctas(I8_256X128) >= 200 ? I8_256X128 : I8_128X64;
-        if (p.tiled.shape == I8_128X64 && ctas(I8_128X64) < 256)
-            p.tiled.ksplit = (int)std::max<int64_t>(1, std::min<int64_t>(256 / ctas(I8_128X64), C / 4));
-    } else if (per < 192) {
-        p.tiled.shape = per > 64 ? I8_256X128 : I8_128X64;
-    }
-    if (f.kernel == R9K_I8_STREAM && f.a) {
-        p.cfg.nt = std::max(f.a, silu ? 2 : 1), p.cfg.wn = f.b, p.cfg.wk = f.c, p.cfg.mt = f.d;
-        p.tile = false;
-    }
-    if (f.kernel == R9K_I8_TILED && f.a)
-        for (int s = 0; s < I8_SHAPES; ++s)
-            if (I8_TILES[s][0] == f.a && I8_TILES[s][1] == f.b) p.tiled.shape = s;
-    if (f.kernel) p.tile = f.kernel == R9K_I8_TILED;
-    if (f.ksplit && !E && N < 1 << 22) (p.tile ? p.tiled.ksplit : p.cfg.ksplit) = (int)std::min<int64_t>(f.ksplit, C);
-    if (!p.tile) {  // no split without chunks
-        const int64_t span = (C + p.cfg.ksplit - 1) / p.cfg.ksplit;
-        p.cfg.ksplit = (int)((C + span - 1) / span);
-    }
-    const int64_t units = M * ((K + 511) / 512);
-    p.fused = !E && !p.tile && p.cfg.mt == 1 && M <= 16 && p.cfg.ksplit == 1 && units <= I8_QA_UNITS * p.cfg.wn * p.cfg.wk;
-    return p;
+    I8Plan best{};
+    double least = 0.0;
+    auto blocks = [&](int64_t RB) { return E ? w4_expert_blocks(M, E, RB) : (double)((M + RB - 1) / RB); };
+    auto offer = [&](const I8Plan &p, double us) {
+        if (least == 0.0 || us < least) {
+            best = p;
+            least = us;
+        }
+    };
+    // a split's sums stay below 2^32 bytes a row block
+    const int64_t splits = E || N >= int64_t(1) << 22 ? 1 : std::min<int64_t>(C, 8);
+    const bool forced = f.kernel && f.a;
+    if (f.kernel != R9K_I8_TILED && !wide)
+        for (const auto &s : I8_STREAMS) {
+            const int nt = forced && silu ? std::max(f.a, 2) : f.a;
+            if (forced && (s[0] != f.rows || s[1] != nt || s[2] != f.b || s[3] != f.c)) continue;
+            // dense: one row tile up to 16 rows, two up to 64 and four above; up to 256 rows
+            if (!forced && (E ? s[0] == 4 : s[2] != 1 || (s[0] == 1) != (M <= 16) || (s[0] == 4 && M <= 32) || (s[0] == 2 && M > 256))) continue;
+            if (!forced && !f.kernel && M > (E ? 100 * E : 256)) continue;
+            if (silu && s[1] == 1) continue;
+            if (((M + 16 * s[0] - 1) / (16 * s[0]) + (E ? std::min(E, M) : 0)) > 65535) continue;  // the grid's
+            const double items = blocks(16 * s[0]);
+            for (int64_t ks = 1; ks <= std::min<int64_t>(splits, 4); ks *= 2) {
+                I8Plan p{};
+                int64_t want = f.kernel && f.ksplit && !E ? std::min<int64_t>(f.ksplit, N >= int64_t(1) << 22 ? 1 : C) : ks;
+                const int64_t span = (C + want - 1) / want;
+                p.cfg = I8Cfg{s[0], s[1], s[2], s[3], (int)((C + span - 1) / span)};  // no split without chunks
+                // a split where one CTA a compute unit is not reached without it
+                if (ks > 1 && !(f.kernel && f.ksplit) && (double)((N / 16 + s[1] * s[2] - 1) / (s[1] * s[2])) * items * (double)ks >= 512.0) break;
+                p.fused = quant && !E && quant_fits(p.cfg, M, K);
+                offer(p, stream_us(p.cfg, M, K, N, E, silu, items) + (quant && !p.fused ? 2.5 : 0.0));
+            }
+        }
+    if (f.kernel != R9K_I8_STREAM || least == 0.0)
+        for (int sh = 0; sh < I8_SHAPES; ++sh) {
+            const int *t = I8_TILES[sh];
+            if (f.kernel == R9K_I8_TILED && f.a ? t[0] != f.a || t[1] != f.b : !f.kernel && !E && M <= 16 && least != 0.0) continue;
+            const double items = blocks(t[1]);
+            for (int64_t ks = 1; ks <= splits; ks *= 2) {
+                I8Plan p{};
+                p.tile = true;
+                p.tiled = I8TiledCfg{sh, (int)(f.kernel == R9K_I8_TILED && f.ksplit && !E ? std::min<int64_t>(f.ksplit, splits == 1 ? 1 : C) : ks)};
+                if (ks > 1 && (double)((N + t[0] - 1) / t[0] * ks) * items > 600.0) break;
+                offer(p, tiled_us(p.tiled, M, K, N, E, silu, items) + (quant ? 2.5 : 0.0));
+            }
+        }
+    return best;
 }
 
 template <int MT, int NT, bool LONG, bool QA>
@@ -328,7 +395,7 @@ static hipError_t launch_mt(const I8Args &a, const I8Cfg &c, hipStream_t s) {
 }
 
 hipError_t launch_gemm_i8(const I8Args &a, const I8Cfg &c, hipStream_t s) {
-    const hipError_t err = c.mt == 1 ? launch_mt<1>(a, c, s) : c.mt == 2 ? launch_mt<2>(a, c, s) : launch_mt<4>(a, c, s);
+    const hipError_t err = c.mt == 1 ? launch_mt<1>(a, c, s) : c.mt == 2 ? launch_mt<2>(a, c, s) : launch_nt<4, 2>(a, c, s);
     if (err != hipSuccess || c.ksplit == 1) return err;
     return launch_i8_reduce(a, c.ksplit, s);
 }

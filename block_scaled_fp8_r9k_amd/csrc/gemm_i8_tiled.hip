@@ -345,7 +345,7 @@ __global__ __launch_bounds__(T::THREADS, T::CTAS * T::NW / 4) void k_gemm_i8_til
                     if constexpr (SILU) {
                         const v4f u = i8_scale(acc[i + NT][j], as[j], ws[i + NT]);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) y[r] = w4_silu_mul(y[r], u[r]);
+                        for (int r = 0; r < 4; ++r) y[r] = i8_silu_mul(y[r], u[r]);
                     }
                     const int piece = (2 * i + (q >> 1)) ^ ((l16 * PR >> 4) & (PR - 1));
                     *(uint2 *)(mine + (l16 * PR + piece) * 16 + 8 * (q & 1)) = w4_bf16x4(y);

@@ -45,16 +45,20 @@ struct I8Plan {
     I8TiledCfg tiled;
     int ksplit() const { return tile ? tiled.ksplit : cfg.ksplit; }
 };
-// columns x rows of a CTA
+// the streaming kernel's shapes: row tiles, column tiles a wave, waves along the columns and along K
+inline constexpr int I8_STREAMS[][4] = {{1, 1, 1, 4}, {1, 1, 1, 8}, {1, 1, 1, 16}, {1, 2, 1, 4}, {1, 2, 1, 8}, {1, 2, 2, 2}, {2, 1, 1, 4},
+                                        {2, 1, 1, 8}, {2, 2, 1, 4}, {2, 2, 1, 8}, {2, 2, 2, 2}, {4, 2, 1, 4}, {4, 2, 1, 8}};
+// the tiled kernel's: columns x rows of a CTA, CTAs that share a compute unit
 enum { I8_256X256, I8_256X128, I8_128X128, I8_128X64, I8_SHAPES };
-inline constexpr int I8_TILES[I8_SHAPES][2] = {{256, 256}, {256, 128}, {128, 128}, {128, 64}};
+inline constexpr int I8_TILES[I8_SHAPES][3] = {{256, 256, 1}, {256, 128, 1}, {128, 128, 2}, {128, 64, 3}};
 // r9k_set_i8_plan's choice: kernel 0 (the planner's), R9K_I8_STREAM or R9K_I8_TILED, the shape (0: the planner's), the split
 struct I8Tuning {
-    int kernel, a, b, c, d, ksplit;
+    int kernel, a, b, c, rows, ksplit;
 };
 I8Tuning &i8_tuning();
-bool i8_stream_shape(int mt, int nt, int wn, int wk);  // one that the streaming kernel has
-I8Plan i8_plan(int64_t M, int64_t K, int64_t N, int64_t E, bool silu);
+// quant: from bf16 activations; wide: activations read through an index, 4 GiB of them or more, which the streaming
+// kernel's 32-bit offsets do not reach
+I8Plan i8_plan_new(int64_t M, int64_t K, int64_t N, int64_t E, bool silu, bool quant, bool wide);
 hipError_t launch_gemm_i8(const I8Args &a, const I8Cfg &c, hipStream_t s);
 hipError_t launch_gemm_i8_tiled(const I8Args &a, const I8TiledCfg &c, hipStream_t s);
 hipError_t launch_i8_reduce(const I8Args &a, int ksplit, hipStream_t s);  // a split's sums, added and scaled

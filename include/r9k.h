@@ -634,28 +634,29 @@ int r9k_moe_gemm_i8(const int8_t *aq, const float *as, int64_t arows, const int3
                     const int32_t *offsets, int64_t E, int64_t R, int64_t K, const int8_t *wp, const float *ws,
                     int64_t N, int act, uint16_t *c, void *stream);
 
-/* Which launch an 8-bit product takes (host only).  E = 0: r9k_gemm_i8 of M rows; E >= 1:
- * r9k_moe_gemm_i8 of R = M rows.  plan holds R9K_I8_PLAN_INTS values:
+/* Which launch an 8-bit product takes (host only).  E = 0: r9k_gemm_i8 of M rows, with quant = 1
+ * r9k_gemm_i8_qa; E >= 1 (quant = 0): r9k_moe_gemm_i8 of R = M rows.  plan holds R9K_I8_PLAN_INTS values:
  *   [0] the kernel: R9K_I8_STREAM (weights streamed into registers) or R9K_I8_TILED
  *       (tiles staged through LDS); 0 for M = 0, and the rest too;
  *   streaming: [1] column tiles of 16 a wave, [2] waves along the columns, [3] waves along K,
- *       [5] row tiles of 16 a CTA, [6] whether r9k_gemm_i8_qa quantises inside it;
+ *       [5] row tiles of 16 a CTA, [6] whether the activations are quantised inside it;
  *   tiled: [1] columns and [2] rows of a CTA;
  *   [4] CTAs along K (above 1: sums in the workspace, and a second launch).
- * Errors: NULLPTR; SHAPE as for the call; ARG for an unknown act, or an act with E = 0. */
+ * Errors: NULLPTR; SHAPE as for the call; ARG for an unknown act or quant, or an act with E = 0. */
 #define R9K_I8_AUTO 0
 #define R9K_I8_STREAM 1
 #define R9K_I8_TILED 2
 #define R9K_I8_PLAN_INTS 7
-int r9k_i8_plan(int64_t M, int64_t K, int64_t N, int64_t E, int act, int *plan);
+int r9k_i8_plan(int64_t M, int64_t K, int64_t N, int64_t E, int act, int quant, int *plan);
 
 /* Plan control of the 8-bit products, for tuning and tests: later calls take this
  * kernel (R9K_I8_AUTO with all else 0: the planner's choice).  R9K_I8_STREAM: `a` column tiles a
- * wave (1, 2; with silu always 2), `b` waves along the columns, `c` along K (powers of two, at most 8
- * together, 16 for one tile of each kind) and `rows` row tiles a CTA (1, 2, 4), all four or none;
- * a split only with them.  R9K_I8_TILED: `a` columns and `b` rows of a CTA (256 x 256, 256 x 128,
- * 128 x 128, 128 x 64, or 0 0).  ksplit: CTAs along K of dense products, clamped to
- * K / 128; 0 for the planner's.  No choice changes a bit of any output.  The setting is process-wide,
+ * wave (with silu always 2), `b` waves along the columns, `c` along K and `rows` row tiles a CTA, all four or none, one
+ * of (a b c rows) 1 1 4 1, 1 1 8 1, 1 1 16 1, 2 1 4 1, 2 1 8 1, 2 2 2 1, 1 1 4 2, 1 1 8 2, 2 1 4 2, 2 1 8 2, 2 2 2 2, 2 1
+ * 4 4, 2 1 8 4; a split only with them.  R9K_I8_TILED: `a` columns and `b` rows of a CTA (256 x 256, 256 x
+ * 128, 128 x 128, 128 x 64, or 0 0).  ksplit: CTAs along K of dense products, clamped to
+ * K / 128; 0 for the planner's.  Shapes that the streaming kernel cannot take (65535 row blocks, activations read
+ * through an index from 4 GiB on) run tiled.  No choice changes a bit of any output.  The setting is process-wide,
  * changes the workspace a shape needs (query again after a change), and must change only
  * while no 8-bit product is being issued.
  * Errors: ARG for an unknown kernel or a shape that it does not have. */
