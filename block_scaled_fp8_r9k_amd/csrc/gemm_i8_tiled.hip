@@ -28,13 +28,14 @@ namespace {
 template <int WN_, int WM_, int TN_, int TM_, int NST_, int CTAS_>
 struct I8Tile {
     static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, NST = NST_, CTAS = CTAS_;  // CTAs a compute unit
+    static constexpr int AHEAD = NST - 1;  // stages asked for before they are computed
     static constexpr int NW = WN * WM, THREADS = 64 * NW;
     static constexpr int BN = WN * TN * 16, BM = WM * TM * 16;  // output columns and rows of a CTA
     static constexpr int WBYTES = BN * 64, ABYTES = BM * 64, STAGE = WBYTES + ABYTES, SMEM = NST * STAGE;
     static constexpr int WLOADS = BN / 16 / NW, ALOADS = BM / 16 / NW, LOADS = WLOADS + ALOADS;  // 1 KiB loads a wave
     static_assert(CTAS * SMEM <= 160 * 1024, "LDS");
     static_assert(WLOADS * NW * 16 == BN && ALOADS * NW * 16 == BM, "loads split evenly");
-    static_assert((NST == 4 || NST == 5) && TN % 2 == 0, "stages; a ring of W fragments whose places are constants");
+    static_assert(NST >= 4 && TN % 2 == 0, "stages; a ring of W fragments whose places are constants");
     static_assert(TM == 4 && NW * 512 * TN <= STAGE, "the outputs' way through one stage's LDS");
     static_assert((NST - 2) * LOADS + TN * TM < 64, "vmcnt");
 };
@@ -42,6 +43,13 @@ template <int V>
 struct Const {
     static constexpr int value = V;
 };
+// at most min(stages, MOST) * LOADS + MORE of the wave's vector-memory instructions are in flight
+template <int MOST, int LOADS, int MORE>
+__device__ __forceinline__ void wait_stages(int stages) {
+    if constexpr (MOST == 0) w4_wait_vm<MORE>();
+    else if (stages >= MOST) w4_wait_vm<MOST * LOADS + MORE>();
+    else wait_stages<MOST - 1, LOADS, MORE>(stages);
+}
 // f(Const<0>) ... f(Const<N - 1>)
 template <class F, int... I>
 __device__ __forceinline__ void each(F &&f, std::integer_sequence<int, I...>) {
@@ -54,8 +62,8 @@ __device__ __forceinline__ void each(F &&f) {
 }  // namespace
 
 template <class T, bool SILU>
-__global__ __launch_bounds__(T::THREADS, T::CTAS * T::NW / 4) void k_gemm_i8_tiled(I8Args p) {
-    constexpr int WN = T::WN, TN = T::TN, TM = T::TM, NST = T::NST, BM = T::BM;
+__global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW + 3) / 4) void k_gemm_i8_tiled(I8Args p) {
+    constexpr int WN = T::WN, TN = T::TN, TM = T::TM, NST = T::NST, BM = T::BM, AHEAD = T::AHEAD;
     constexpr int NT = SILU ? TN / 2 : TN;                    // output tiles a wave and row tile
     constexpr int PR = 2 * NT, READS = PR < 4 ? 1 : PR / 4;   // 16-byte pieces of an output row; stores a row tile
     extern __shared__ __align__(16) uint8_t lds[];
@@ -169,7 +177,7 @@ __global__ __launch_bounds__(T::THREADS, T::CTAS * T::NW / 4) void k_gemm_i8_til
     int at = 0;  // place of the stage that is next to be computed
     auto start = [&](int n) {  // the first stages
 #pragma unroll
-        for (int k = 0; k < NST - 1; ++k)
+        for (int k = 0; k < AHEAD; ++k)
             if (k < n) each<T::LOADS>([&](auto u) { issue(at + k >= NST ? at + k - NST : at + k, u); });
     };
 
@@ -189,26 +197,14 @@ __global__ __launch_bounds__(T::THREADS, T::CTAS * T::NW / 4) void k_gemm_i8_til
     bool stored = false;  // the last tile's stores were issued behind this tile's first stages
 
     for (;;) {
-        // at most the loads of `stages` stages (0 to 3) and, behind the first stages, the last tile's stores are in
+        // at most the loads of `stages` stages and, behind the first stages, the last tile's stores are in
         // flight; other memory instructions of the wave only make the wait longer
         auto wait = [&](int stages, bool behind) {
-            constexpr int S = TM * READS;
-            if (stored && behind) {
-                if (p.ksplit > 1) {
-                    if (stages >= 3 && NST > 4) w4_wait_vm<3 * T::LOADS + TN * TM>();
-                    else if (stages >= 2) w4_wait_vm<2 * T::LOADS + TN * TM>();
-                    else if (stages == 1) w4_wait_vm<T::LOADS + TN * TM>();
-                    else w4_wait_vm<TN * TM>();
-                } else if (stages >= 3 && NST > 4) w4_wait_vm<3 * T::LOADS + S>();
-                else if (stages >= 2) w4_wait_vm<2 * T::LOADS + S>();
-                else if (stages == 1) w4_wait_vm<T::LOADS + S>();
-                else w4_wait_vm<S>();
-            } else if (stages >= 3 && NST > 4) w4_wait_vm<3 * T::LOADS>();
-            else if (stages >= 2) w4_wait_vm<2 * T::LOADS>();
-            else if (stages == 1) w4_wait_vm<T::LOADS>();
-            else w4_wait_vm<0>();
+            if (!stored || !behind) wait_stages<AHEAD - 1, T::LOADS, 0>(stages);
+            else if (p.ksplit > 1) wait_stages<AHEAD - 1, T::LOADS, TN * TM>(stages);
+            else wait_stages<AHEAD - 1, T::LOADS, TM * READS>(stages);
         };
-        wait(min(NST - 2, n - 1), true);
+        wait(min(AHEAD - 1, n - 1), true);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
 
@@ -231,9 +227,9 @@ __global__ __launch_bounds__(T::THREADS, T::CTAS * T::NW / 4) void k_gemm_i8_til
         int scale_at = 0;
         auto steps = [&](auto row_tiles, int c, auto parity, auto behind) {
             constexpr int MT = decltype(row_tiles)::value, odd = decltype(parity)::value, ahead = decltype(behind)::value;
-            // the next stage has landed: the wave's loads issued after it are those of the NST - 3 stages behind it, fewer
-            // at the end
-            wait(ahead ? NST - 3 : min(NST - 3, n - 2 - c), c < NST - 2);
+            // The next stage has landed: the wave's loads issued after it are those of the stages behind, fewer at the end, and
+            // behind the first ones the last tile's stores.
+            wait(ahead ? AHEAD - 2 : min(AHEAD - 2, n - 2 - c), c + 1 < AHEAD);
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
             const int next = at + 1 == NST ? 0 : at + 1, last = at == 0 ? NST - 1 : at - 1;
@@ -251,7 +247,7 @@ __global__ __launch_bounds__(T::THREADS, T::CTAS * T::NW / 4) void k_gemm_i8_til
             const uint8_t *sb = lds + at * T::STAGE, *sx = lds + next * T::STAGE;
             each<TN>([&](auto step) {
                 constexpr int i = decltype(step)::value, PER = (T::LOADS + TN - 1) / TN;
-                if (ahead)  // the loads of the stage NST - 1 behind, spread over the steps
+                if (ahead)  // the loads of the stage AHEAD behind, spread over the steps
                     each<PER>([&](auto u) { issue(last, Const<PER * i + decltype(u)::value>{}); });
                 if constexpr (MT > 0) {
                     wf[(TN * odd + i + 2) & 3] = *(const v4i *)((i + 2 < TN ? sb + 1024 * (i + 2) : sx + 1024 * (i + 2 - TN)) + wfo);
@@ -274,11 +270,11 @@ __global__ __launch_bounds__(T::THREADS, T::CTAS * T::NW / 4) void k_gemm_i8_til
             wf[0] = *(const v4i *)(sb + wfo);
             wf[1] = *(const v4i *)(sb + wfo + 1024);
             int c = 0;
-            for (; c + NST < n; c += 2) {
+            for (; c + 1 + AHEAD < n; c += 2) {
                 steps(row_tiles, c, Const<0>{}, Const<1>{});
                 steps(row_tiles, c + 1, Const<1>{}, Const<1>{});
             }
-            if (c + NST - 1 < n) {  // one more stage to ask for
+            if (c + AHEAD < n) {  // one more stage to ask for (with AHEAD even there is none)
                 steps(row_tiles, c, Const<0>{}, Const<1>{});
                 steps(row_tiles, c + 1, Const<1>{}, Const<0>{});
                 c += 2;
@@ -403,6 +399,8 @@ hipError_t launch_gemm_i8_tiled(const I8Args &a, const I8TiledCfg &c, hipStream_
         case I8_256X256: err = launch_tile<I8Tile<2, 4, 8, 4, 5, 1>>(a, c, s); break;
         case I8_256X128: err = launch_tile<I8Tile<4, 2, 4, 4, 5, 1>>(a, c, s); break;
         case I8_128X128: err = launch_tile<I8Tile<4, 2, 2, 4, 5, 2>>(a, c, s); break;
+        case I8_64X128: err = launch_tile<I8Tile<2, 2, 2, 4, 8, 1>>(a, c, s); break;
+        case I8_64X64: err = launch_tile<I8Tile<2, 1, 2, 4, 8, 2>>(a, c, s); break;
         default: err = launch_tile<I8Tile<4, 1, 2, 4, 4, 3>>(a, c, s); break;
     }
     if (err != hipSuccess || c.ksplit == 1) return err;

@@ -654,7 +654,7 @@ int r9k_i8_plan(int64_t M, int64_t K, int64_t N, int64_t E, int act, int quant, 
  * wave (with silu always 2), `b` waves along the columns, `c` along K and `rows` row tiles a CTA, all four or none, one
  * of (a b c rows) 1 1 4 1, 1 1 8 1, 1 1 16 1, 2 1 4 1, 2 1 8 1, 2 2 2 1, 1 1 4 2, 1 1 8 2, 2 1 4 2, 2 1 8 2, 2 2 2 2, 2 1
  * 4 4, 2 1 8 4; a split only with them.  R9K_I8_TILED: `a` columns and `b` rows of a CTA (256 x 256, 256 x
- * 128, 128 x 128, 128 x 64, or 0 0).  ksplit: CTAs along K of dense products, clamped to
+ * 128, 128 x 128, 128 x 64, 64 x 128, 64 x 64, or 0 0).  ksplit: CTAs along K of dense products, clamped to
  * K / 128; 0 for the planner's.  Shapes that the streaming kernel cannot take (65535 row blocks, activations read
  * through an index from 4 GiB on) run tiled.  No choice changes a bit of any output.  The setting is process-wide,
  * changes the workspace a shape needs (query again after a change), and must change only

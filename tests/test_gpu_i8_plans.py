@@ -10,7 +10,7 @@ from tests.gpu_util import say
 from tests.test_gpu_i8 import acts, routing, weight
 
 pytestmark = pytest.mark.gpu
-TILES = [(256, 256), (256, 128), (128, 128), (128, 64)]
+TILES = [(256, 256), (256, 128), (128, 128), (128, 64), (64, 128), (64, 64)]
 # column tiles a wave, waves along the columns and along K, row tiles a CTA
 STREAM = [(1, 1, 4, 1), (1, 1, 8, 1), (1, 1, 16, 1), (2, 1, 4, 1), (2, 1, 8, 1), (2, 2, 2, 1), (1, 1, 4, 2), (1, 1, 8, 2), (2, 1, 4, 2),
           (2, 1, 8, 2), (2, 2, 2, 2), (2, 1, 4, 4), (2, 1, 8, 4)]
