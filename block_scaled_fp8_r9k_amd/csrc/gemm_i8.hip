@@ -254,10 +254,10 @@ hipError_t launch_i8_reduce(const I8Args &a, int ksplit, hipStream_t s) {
 
 // ---- the launch of the least estimated time ------------------------------------
 //
-// Times in us, fitted to every launch of 3739 dense shapes (1 to 1200 rows, K and N from 256 to 14336) and 16806 of
+// Times in us, fitted to every launch of 2492 dense shapes (1 to 1200 rows, K and N from 256 to 14336) and 10354 of
 // experts (4 to 256 of them, up to 4096 tokens, 128 to 4096 wide), in graphs, weights from memory, so that the launch
-// picked is as little as possible behind the fastest of all: on 1209 and 5689 other shapes 1.8% on average dense (9% at
-// the 90th percentile, at most 31%), 1.3% with experts (8%, at most 58%).
+// picked is as little as possible behind the fastest of all: on 738 and 3101 other shapes 1.7% on average dense (10% at
+// the 90th percentile, at most 44%), 1.3% with experts (8%, at most 50%).
 //
 // Streaming: a compute unit's busiest CTAs move W (weight blocks of 2 KiB) and A (activation blocks as large), and each of
 // its turns is as long as a wave's slice.  A split adds its sums and the reduce launch.  E.g. one row of 4096 x 14336: 11.9 us
@@ -272,37 +272,36 @@ static double stream_us(const I8Cfg &c, int64_t M, int64_t K, int64_t N, int64_t
     if (E) {
         const int64_t RB = 16 * c.mt, grid = cols * ((M + std::min(E, M) * (RB - 1)) / RB);
         const double rounds = std::max(1.0, ctas / 256.0), turns = std::max(1.0, ctas / 256.0 / fit);
-        const double us = 3.65 + 0.115 * waves + rounds * (W * (c.mt == 1 ? 0.0319 : 0.0864) + 0.0004 * A + 0.0277 * waves) +
-                          turns * (0.192 * per + 0.083) + 0.07 * std::max(0.0, (double)grid - ctas) / 256.0;
-        return std::max(us, 3.65 + 0.000385 * blocks * (double)(tiles * C)) + 0.1 * us;
+        const double us = 3.65 + 0.113 * waves + rounds * (W * (c.mt == 1 ? 0.0234 : 0.0738) + 0.0004 * A + 0.0283 * waves) +
+                          turns * (0.192 * per + 0.148) + 0.05 * std::max(0.0, (double)grid - ctas) / 256.0;
+        return std::max(us, 3.65 + 0.000389 * blocks * (double)(tiles * C)) + 0.1 * us;
     }
     const double rounds = std::ceil(ctas / 256.0), turns = std::ceil(ctas / 256.0 / fit);
-    double us = 2.12 + 0.0071 * waves + turns * 0.0499 * per +
-                rounds * (W * (c.mt == 1 ? 0.0402 : c.mt == 2 ? 0.0543 : 0.1234) + 0.0245 * A + 0.24);
-    if (c.mt == 4 && c.wk == 8) us += 0.058;
-    if (c.ksplit > 1) us += 3.13 + 0.3e-6 * (double)(c.ksplit * M * N);
+    double us = 2.11 + 0.0046 * waves + turns * 0.0516 * per +
+                rounds * (W * (c.mt == 1 ? 0.0346 : c.mt == 2 ? 0.0572 : 0.1345) + 0.0245 * A + 0.19);
+    if (c.mt == 4 && c.wk == 8) us += 0.069;
+    if (c.ksplit > 1) us += 2.96 + 0.43e-6 * (double)(c.ksplit * M * N);
     return us;
 }
 
-// Tiled: a stage takes `alone` where its CTA has the compute unit to itself and `shared` for each of those that share it,
-// less where rows are missing; each tile its start and its outputs (longer with silu).  E.g. 4096 x 4096 x 12288:
-// 178 us in tiles of 256 x 256, 220 in 256 x 128, 243 in 128 x 128; 1024 x 4096 x 14336 57, 75, 84; down of 128 experts,
-// 2048 tokens 69, 82, 86, and 85 in 128 x 64.  100 x
-// 4096 x 4096 13.0 in 64 x 64, streaming 12.8, 15.4 in 128 x 64; 256 x 4096 x 4096 14.5, 19.5 in 64 x 128, 19.8 in 128 x 128.
+// Tiled: a stage takes `alone` where its CTA has the compute unit to itself and `shared` for each of those that share
+// it, each tile its start and its outputs.  E.g. 4096 x 4096 x 12288: 178 us in tiles of 256 x 256, 220 in 256 x 128,
+// 243 in 128 x 128; 2048 x 4096 x 4096 51, 37, 42; 256 x 4096 x 4096 12.5 in 64 x 64, 19.2 in 64 x 128, 19.8 in 128 x 128;
+// 100 x 4096 x 4096 11.6 in 64 x 64, streaming 12.8; gate_up of 64 tokens, eight of 128 experts, 70 in 128 x 64, 74 in 64 x 64.
 static double tiled_us(const I8TiledCfg &c, int64_t M, int64_t K, int64_t N, int64_t E, bool silu, double blocks) {
-    static constexpr double dense[][3] = {{0.341, 0.0334, 2.81}, {0.301, 0.326, 1.78}, {0.168, 0.237, 0.924}, {0.288, 0.22, 0.138}, {0.212, 0.105, 1.24}, {0.127, 0.129, 0.606}};
-    static constexpr double moe[][3] = {{0.172, 0.698, 5.48}, {0.216, 0.564, 3.18}, {0.0325, 0.151, 2.84}, {0.178, 0.128, 0.444}, {0.286, 0.157, 1.4}, {0.12, 0.16, 0.69}};
+    static constexpr double dense[][3] = {{0.341, 0.0385, 3.3}, {0.243, 0.349, 1.27}, {0.238, 0.201, 1.05},
+                                     {0.281, 0.244, 0.148}, {0.211, 0.15, 1.14}, {0.0993, 0.122, 0.746}};
+    static constexpr double moe[][3] = {{0.154, 0.785, 5.89}, {0.3, 0.338, 3.03}, {0.0466, 0.18, 2.24},
+                                   {0.149, 0.0774, 0.582}, {0.46, 0.322, 1.59}, {0.0694, 0.133, 0.64}};
     const int *t = I8_TILES[c.shape];
     const double *u = E ? moe[c.shape] : dense[c.shape], fit = t[2];
     const int64_t C = K / 128, stages = 2 * ((C + c.ksplit - 1) / c.ksplit);
     const double load = (double)((N + t[0] - 1) / t[0] * c.ksplit) * blocks / 256.0;
-    const double fill = std::min(1.0, (double)M / blocks / t[1]), least = E ? 0.901 : 1.0;
     const double busy = std::min(fit, E ? std::max(1.0, load) : std::ceil(load));
     const double seq = load <= 2.0 * fit ? std::max(1.0, std::ceil(load / fit)) : load / fit + 0.5;
-    const double stage = std::max(u[0], u[1] * busy) * (least + (1.0 - least) * fill);
-    const double us = seq * ((double)stages * stage + u[2] * (silu ? 1.26 : 1.0));
-    if (E) return 4.87 + 0.148 * seq + 0.1 * us + std::max(us, 2.03e-7 * (blocks * (double)(N * K) + (double)(M * (silu ? N : 2 * N))));
-    return 3.34 + us + (c.ksplit > 1 ? 3.2 + 1.9e-6 * (double)(c.ksplit * M * N) : 0.0);
+    const double us = seq * ((double)stages * std::max(u[0], u[1] * busy) + u[2]);
+    if (E) return 4.96 + 0.141 * seq + 0.1 * us + std::max(us, 2.05e-7 * (blocks * (double)(N * K) + (double)(M * (silu ? N : 2 * N))));
+    return 2.76 + us + (c.ksplit > 1 ? 3.08 + 2.88e-6 * (double)(c.ksplit * M * N) : 0.0);
 }
 
 // 512-value units of the rows that the streaming kernel quantises itself: as many as its waves hold

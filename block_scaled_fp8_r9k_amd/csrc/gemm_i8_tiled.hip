@@ -14,7 +14,15 @@
 // rows of a fragment read fall on distinct banks.
 // A CTA computes one output tile after another: the first stages of the next are asked for before the
 // outputs of the last are scaled and stored, and the waits of its first stages let those stores
-// be in flight.  FIGURE
+// be in flight (at 4096 x 4096 x 12288 175 -> 168 us).
+//
+// Measured: 4096 x 4096 x 12288 in 168 us, 2.45e15 operations a second.  The matrix instructions alone reach 4.0e15 on
+// such values, at the 2.0 GHz that the card's power leaves them; the kernel's clock is the same, its MFMA cycles 61% of all.
+// Without the loads it takes 146 us, without LDS reads 143: neither alone is what is left.  32 x 32 x 32 instructions
+// reach 3.5e15; one barrier for two stages changes nothing.
+// Few rows are bound by what a compute unit takes in from L2 and by the way from the first load to the last store:
+// 64 x 64 with two groups of waves, two CTAs of five stages each, 12.5 us at 256 x 4096 x 4096 (one group 14.5;
+// eight stages, one CTA 13.2; four stages, two CTAs 14.0); 128 x 64 in six stages, two CTAs 19.0 (four, three CTAs 21.7).
 #include <algorithm>
 #include <mutex>
 #include <utility>
@@ -25,18 +33,20 @@
 namespace r9k {
 
 namespace {
-template <int WN_, int WM_, int TN_, int TM_, int NST_, int CTAS_>
+template <int WN_, int WM_, int TN_, int TM_, int NST_, int CTAS_, int KG_ = 1>
 struct I8Tile {
     static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, NST = NST_, CTAS = CTAS_;  // CTAs a compute unit
     static constexpr int AHEAD = NST - 1;  // stages asked for before they are computed
-    static constexpr int NW = WN * WM, THREADS = 64 * NW;
+    static constexpr int KG = KG_;         // groups of waves: with two each computes the whole tile over half of every chunk
+    static constexpr int NW = WN * WM, THREADS = 64 * NW * KG;  // waves of a group
     static constexpr int BN = WN * TN * 16, BM = WM * TM * 16;  // output columns and rows of a CTA
-    static constexpr int WBYTES = BN * 64, ABYTES = BM * 64, STAGE = WBYTES + ABYTES, SMEM = NST * STAGE;
+    static constexpr int WBYTES = BN * 64, ABYTES = BM * 64, STAGE = WBYTES + ABYTES, RING = NST * STAGE, SMEM = KG * RING;
     static constexpr int WLOADS = BN / 16 / NW, ALOADS = BM / 16 / NW, LOADS = WLOADS + ALOADS;  // 1 KiB loads a wave
     static_assert(CTAS * SMEM <= 160 * 1024, "LDS");
     static_assert(WLOADS * NW * 16 == BN && ALOADS * NW * 16 == BM, "loads split evenly");
     static_assert(NST >= 4 && TN % 2 == 0, "stages; a ring of W fragments whose places are constants");
     static_assert(TM == 4 && NW * 512 * TN <= STAGE, "the outputs' way through one stage's LDS");
+    static_assert(KG == 1 || (KG == 2 && NW * TN * TM * 512 <= RING), "half of a group's sums, on their way to the other");
     static_assert((NST - 2) * LOADS + TN * TM < 64, "vmcnt");
 };
 template <int V>
@@ -62,13 +72,16 @@ __device__ __forceinline__ void each(F &&f) {
 }  // namespace
 
 template <class T, bool SILU>
-__global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW + 3) / 4) void k_gemm_i8_tiled(I8Args p) {
+__global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW * T::KG + 3) / 4) void k_gemm_i8_tiled(I8Args p) {
     constexpr int WN = T::WN, TN = T::TN, TM = T::TM, NST = T::NST, BM = T::BM, AHEAD = T::AHEAD;
     constexpr int NT = SILU ? TN / 2 : TN;                    // output tiles a wave and row tile
     constexpr int PR = 2 * NT, READS = PR < 4 ? 1 : PR / 4;   // 16-byte pieces of an output row; stores a row tile
-    extern __shared__ __align__(16) uint8_t lds[];
+    constexpr int KG = T::KG, TMG = TM / KG;                  // row tiles that a wave scales and stores
+    extern __shared__ __align__(16) uint8_t lds_all[];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave % WN, wm = wave / WN;
+    const int wid = __builtin_amdgcn_readfirstlane(tid >> 6), group = KG == 1 ? 0 : wid / T::NW;
+    const int wave = wid - group * T::NW, wn = wave % WN, wm = wave / WN;
+    uint8_t *const lds = lds_all + group * T::RING;  // the group's stages
     const int C = (int)(p.K / 128), tiles = (int)(p.N / 16);
     const int64_t ldc = SILU ? p.N / 2 : p.N;
     const int blocks = p.nblk * p.nrow, total = blocks * p.ksplit;
@@ -134,7 +147,7 @@ __global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW + 3) / 4) void k_gemm_
         asm volatile("" : "+v"(l));
         return l;
     };
-    // this wave's share of a stage's loads: W instructions WLOADS wave + u, one half of a
+    // this wave's share of its group's loads of a stage: W instructions WLOADS wave + u, one half of a
     // column tile's block each, and A instructions ALOADS wave + u, sixteen rows each
     const int8_t *wsrc[T::WLOADS], *asrc[T::ALOADS];
     uint32_t arow[T::ALOADS], srow;  // what look_up found for those, and for the wave's row `lane`
@@ -155,12 +168,12 @@ __global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW + 3) / 4) void k_gemm_
 #pragma unroll
         for (int u = 0; u < T::WLOADS; ++u) {
             const int t = T::WLOADS * wave + u;
-            wsrc[u] = p.wp + (((int64_t)w.e * tiles + col_tile(w.bx, t / TN, t % TN)) * C + cb) * 2048 + 16 * l;
+            wsrc[u] = p.wp + (((int64_t)w.e * tiles + col_tile(w.bx, t / TN, t % TN)) * C + cb) * 2048 + 1024 * group + 16 * l;
         }
 #pragma unroll
         for (int u = 0; u < T::ALOADS; ++u) {
             const int row = 16 * (T::ALOADS * wave + u) + (l >> 2), piece = (l & 3) ^ ((row >> 2) & 3);
-            asrc[u] = p.aq + (int64_t)source_row(arow[u]) * p.K + cb * 128 + 16 * piece;
+            asrc[u] = p.aq + (int64_t)source_row(arow[u]) * p.K + cb * 128 + 64 * group + 16 * piece;
         }
     };
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(w4_lds_addr(lds));
@@ -168,10 +181,10 @@ __global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW + 3) / 4) void k_gemm_
         constexpr int u = decltype(load)::value, v = u - T::WLOADS;
         if constexpr (u < T::WLOADS) {
             w4_load16(wsrc[u], lds0 + st * T::STAGE + (T::WLOADS * wave + u) * 1024);
-            wsrc[u] += 1024;
+            wsrc[u] += 1024 * KG;
         } else if constexpr (u < T::LOADS) {
             w4_load16(asrc[v], lds0 + st * T::STAGE + T::WBYTES + (T::ALOADS * wave + v) * 1024);
-            asrc[v] += 64;
+            asrc[v] += 64 * KG;
         }
     };
     int at = 0;  // place of the stage that is next to be computed
@@ -192,7 +205,7 @@ __global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW + 3) / 4) void k_gemm_
     rows_of(cur);
     pointers(cur);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    int cb, n = 2 * chunks(cur, cb);  // stages
+    int cb, n = 2 / KG * chunks(cur, cb);  // stages
     start(n);
     bool stored = false;  // the last tile's stores were issued behind this tile's first stages
 
@@ -201,8 +214,8 @@ __global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW + 3) / 4) void k_gemm_
         // flight; other memory instructions of the wave only make the wait longer
         auto wait = [&](int stages, bool behind) {
             if (!stored || !behind) wait_stages<AHEAD - 1, T::LOADS, 0>(stages);
-            else if (p.ksplit > 1) wait_stages<AHEAD - 1, T::LOADS, TN * TM>(stages);
-            else wait_stages<AHEAD - 1, T::LOADS, TM * READS>(stages);
+            else if (p.ksplit > 1) wait_stages<AHEAD - 1, T::LOADS, TN * TMG>(stages);
+            else wait_stages<AHEAD - 1, T::LOADS, TMG * READS>(stages);
         };
         wait(min(AHEAD - 1, n - 1), true);
         __builtin_amdgcn_s_barrier();
@@ -280,10 +293,11 @@ __global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW + 3) / 4) void k_gemm_
                 c += 2;
             }
             if (more) pointers(nxt);
-            for (; c < n; c += 2) {
+            for (; c + 1 < n; c += 2) {
                 steps(row_tiles, c, Const<0>{}, Const<0>{});
                 steps(row_tiles, c + 1, Const<1>{}, Const<0>{});
             }
+            if (KG > 1 && c < n) steps(row_tiles, c, Const<0>{}, Const<0>{});
         };
         switch (mt) {  // only the row tiles that hold rows are computed
             case 0: run(Const<0>{}); break;
@@ -296,19 +310,35 @@ __global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW + 3) / 4) void k_gemm_
 #pragma unroll
             for (int j = 0; j < TM; ++j) i8_pin(acc[i][j]);
         float4 ws[TN];
-        float as[TM];
+        float as[TMG];
         w4_wait_vm<0>();  // the scales (waited for already, but in tiles of few stages)
 #pragma unroll
         for (int i = 0; i < TN; ++i) ws[i] = *(const float4 *)(lds + scale_at + 64 * i + 16 * q);
 #pragma unroll
-        for (int j = 0; j < TM; ++j) as[j] = *(const float *)(lds + scale_at + AS + 64 * j + 4 * l16);
+        for (int j = 0; j < TMG; ++j) as[j] = *(const float *)(lds + scale_at + AS + 64 * (group * TMG + j) + 4 * l16);
         __syncthreads();  // every wave is done with this tile's stages
+        if constexpr (KG == 2) {  // each group gives the other the sums of half of its row tiles, and adds up the other half
+            uint8_t *to = lds + wave * (TN * TMG * 1024), *from = lds_all + (1 - group) * T::RING + wave * (TN * TMG * 1024);
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int j = 0; j < TMG; ++j) {
+                    *(v4i *)(to + (TMG * i + j) * 1024 + 16 * lane) = group ? acc[i][j] : acc[i][TMG + j];
+                    if (group) acc[i][j] = acc[i][TMG + j];
+                }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int j = 0; j < TMG; ++j) acc[i][j] += *(const v4i *)(from + (TMG * i + j) * 1024 + 16 * lane);
+            __syncthreads();
+        }
         if (more) {
-            n = 2 * chunks(nxt, cb);
+            n = 2 / KG * chunks(nxt, cb);
             start(n);
         }
 
-        // lane holds, per tile (i, j), row 16 (wm TM + j) + l16 and columns 4 q .. +3 of tile i.  Stores past the last row
+        // lane holds, per tile (i, j), row 16 (wm TM + group TMG + j) + l16 and columns 4 q .. +3 of tile i.  Stores past the last row
         // or column fall behind their descriptor's end and are dropped, so that every wave issues as many.
         const int l = fresh(), l16 = l & 15, q = l >> 4;
         const int have = max(0, now.rows - wm * TM * 16);  // rows of the wave that exist (at most 64)
@@ -321,8 +351,8 @@ __global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW + 3) / 4) void k_gemm_
             for (int i = 0; i < TN; ++i) {
                 const int t = (now.bx * WN + wn) * TN + i;
 #pragma unroll
-                for (int j = 0; j < TM; ++j) {
-                    const uint32_t off = ((uint32_t)(16 * j + l16) * (uint32_t)p.N + 16 * t + 4 * q) * 4u;
+                for (int j = 0; j < TMG; ++j) {
+                    const uint32_t off = ((uint32_t)(16 * (group * TMG + j) + l16) * (uint32_t)p.N + 16 * t + 4 * q) * 4u;
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), out, t < tiles ? off : 0xC0000000u, 0, 0);
                 }
             }
@@ -334,7 +364,7 @@ __global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW + 3) / 4) void k_gemm_
             uint8_t *mine = lds + (at == 0 ? NST - 1 : at - 1) * T::STAGE + wave * (512 * TN);
             const int64_t n0 = (int64_t)(now.bx * WN + wn) * NT * 16;
 #pragma unroll
-            for (int j = 0; j < TM; ++j) {
+            for (int j = 0; j < TMG; ++j) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     v4f y = i8_scale(acc[i][j], as[j], ws[i]);
@@ -351,7 +381,7 @@ __global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW + 3) / 4) void k_gemm_
                     const int id = 64 * r + l, row = id / PR, piece = id % PR;
                     const uint4 x = *(const uint4 *)(mine + ((row & 15) * PR + (piece ^ ((row * PR >> 4) & (PR - 1)))) * 16);
                     const bool in = row < 16 && n0 + 8 * piece < ldc;
-                    const uint32_t off = (uint32_t)(16 * j + row) * (uint32_t)ldc * 2u + (uint32_t)(n0 + 8 * piece) * 2u;
+                    const uint32_t off = (uint32_t)(16 * (group * TMG + j) + row) * (uint32_t)ldc * 2u + (uint32_t)(n0 + 8 * piece) * 2u;
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), out, in ? off : 0xC0000000u, 0, 0);
                 }
             }
@@ -399,9 +429,9 @@ hipError_t launch_gemm_i8_tiled(const I8Args &a, const I8TiledCfg &c, hipStream_
         case I8_256X256: err = launch_tile<I8Tile<2, 4, 8, 4, 5, 1>>(a, c, s); break;
         case I8_256X128: err = launch_tile<I8Tile<4, 2, 4, 4, 5, 1>>(a, c, s); break;
         case I8_128X128: err = launch_tile<I8Tile<4, 2, 2, 4, 5, 2>>(a, c, s); break;
-        case I8_64X128: err = launch_tile<I8Tile<2, 2, 2, 4, 8, 1>>(a, c, s); break;
-        case I8_64X64: err = launch_tile<I8Tile<2, 1, 2, 4, 8, 2>>(a, c, s); break;
-        default: err = launch_tile<I8Tile<4, 1, 2, 4, 4, 3>>(a, c, s); break;
+        case I8_64X128: err = launch_tile<I8Tile<2, 2, 2, 4, 6, 2>>(a, c, s); break;
+        case I8_64X64: err = launch_tile<I8Tile<2, 1, 2, 4, 5, 2, 2>>(a, c, s); break;
+        default: err = launch_tile<I8Tile<4, 1, 2, 4, 6, 2>>(a, c, s); break;
     }
     if (err != hipSuccess || c.ksplit == 1) return err;
     return launch_i8_reduce(a, c.ksplit, s);

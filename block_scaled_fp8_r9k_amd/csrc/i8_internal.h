@@ -50,7 +50,7 @@ inline constexpr int I8_STREAMS[][4] = {{1, 1, 1, 4}, {1, 1, 1, 8}, {1, 1, 1, 16
                                         {2, 1, 1, 8}, {2, 2, 1, 4}, {2, 2, 1, 8}, {2, 2, 2, 2}, {4, 2, 1, 4}, {4, 2, 1, 8}};
 // the tiled kernel's: columns x rows of a CTA, CTAs that share a compute unit
 enum { I8_256X256, I8_256X128, I8_128X128, I8_128X64, I8_64X128, I8_64X64, I8_SHAPES };
-inline constexpr int I8_TILES[I8_SHAPES][3] = {{256, 256, 1}, {256, 128, 1}, {128, 128, 2}, {128, 64, 3}, {64, 128, 1}, {64, 64, 2}};
+inline constexpr int I8_TILES[I8_SHAPES][3] = {{256, 256, 1}, {256, 128, 1}, {128, 128, 2}, {128, 64, 2}, {64, 128, 2}, {64, 64, 2}};
 // r9k_set_i8_plan's choice: kernel 0 (the planner's), R9K_I8_STREAM or R9K_I8_TILED, the shape (0: the planner's), the split
 struct I8Tuning {
     int kernel, a, b, c, rows, ksplit;
