@@ -17,7 +17,7 @@
 // be in flight (at 4096 x 4096 x 12288 175 -> 168 us).
 //
 // Measured: 4096 x 4096 x 12288 in 168 us, 2.45e15 operations a second.  The matrix instructions alone reach 4.0e15 on
-// such values, at the 2.0 GHz that the card's power leaves them; the kernel's clock is the same, its MFMA cycles 61% of all.
+// such values, at the 2.0 GHz that the card's power leaves them; its clock is the same, with MFMA in 57% of the cycles.
 // Without the loads it takes 146 us, without LDS reads 143: neither alone is what is left.  32 x 32 x 32 instructions
 // reach 3.5e15; one barrier for two stages changes nothing.
 // Few rows are bound by what a compute unit takes in from L2 and by the way from the first load to the last store:

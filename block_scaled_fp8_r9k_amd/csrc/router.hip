@@ -176,7 +176,9 @@ __device__ __forceinline__ void put_loss(const BalanceArgs &p, double dot, int k
 }
 
 // A CTA's tokens, consecutive ones: their probabilities and counts, into its part of the
-// workspace, or with one CTA the outputs.  65536 tokens of 256 experts in bf16: FIGURE.
+// workspace, or with one CTA the outputs.  65536 tokens of 256 experts in bf16: 12 us for 36 MB,
+// 2.9 TB/s; each of the 256 CTAs, one a compute unit, asks for its rows in about eight steps, and its start, the
+// histogram and its waves' sums are not hidden behind them.  1023 tokens of 128 in fp32: 5.2 us.
 template <bool F32, int VEC, int NV, int LPT>
 __global__ __launch_bounds__(64 * balance_waves(NV * VEC)) void k_balance(BalanceArgs p, int64_t per) {
     constexpr int U = NV == 1 ? 4 : 1, L = 1 << LPT, TPW = 64 >> LPT;
@@ -275,7 +277,8 @@ __global__ __launch_bounds__(64 * balance_waves(NV * VEC)) void k_balance(Balanc
 
 // The parts, added up, and the loss.  A CTA takes 32 columns: a thread four of them, every 32nd part.  With more
 // than one CTA each leaves its share of the loss in the workspace, and the last to arrive (the ticket starts at 0
-// in the launch before) adds them in their order, so that the order of arrival does not show.  FIGURE
+// in the launch before) adds them in their order, so that the order of arrival does not show.  256 parts of
+// 256 columns: 5.8 us, 16 of 128: 4.4, the launch, a load of other CTAs' sums and the ticket in turn.
 __global__ __launch_bounds__(256) void k_balance_end(BalanceArgs p, int parts) {
     __shared__ __align__(16) v4f sp[4][8];
     __shared__ __align__(16) v4i sc[4][8];
@@ -349,7 +352,8 @@ __global__ __launch_bounds__(256) void k_balance_end(BalanceArgs p, int parts) {
 // The gradient of the logits: with gloss the balance loss's part, with gw the routing weights'.  The
 // latter goes through the wave's own LDS: the token's row is cleared there, its slots put
 // their terms in, and the lanes take their experts' back.  Slots that share an expert (seen by a tag that each slot
-// leaves and reads again) add theirs one after another, in ascending order.
+// leaves and reads again) add theirs one after another, in ascending order.  Bytes bound it: 65536 tokens of 256 in
+// fp32, both parts, 27.4 us for 140 MB, 5.1 TB/s; 8191 of 128 6.1 us, 512 of 8 2.7, of which a launch is most.
 template <bool F32, int VEC, int NV, int LPT>
 __global__ __launch_bounds__(256) void k_router_bwd(RouterGradArgs p) {
     constexpr int U = NV == 1 ? 2 : 1, L = 1 << LPT, TPW = 64 >> LPT, ROW = L * NV * VEC;
@@ -482,8 +486,10 @@ static hipError_t by_shape(int64_t E, int64_t lanes, bool f32, GO go) {
 }
 
 // CTAs of the loss's first launch, each a part of the workspace (one: the outputs come from it)
+// One launch of one CTA and two launches, in graphs: 512 tokens of 8 experts 5.6 and 6.4 us, of 64 7.5 and 8.0, of 128
+// 12.2 and 8.2, 2048 of 8 11.5 and 7.3; a call of one launch takes the host 3 us less besides.
 static int balance_parts(int64_t T, int64_t E) {
-    if (T * E <= 16384) return 1;
+    if (T <= 512 && T * E <= 32768) return 1;
     return (int)std::max<int64_t>(1, std::min<int64_t>(256, (T + 63) / 64));
 }
 // The parts' sums, their counts, their kept tokens (256), the ticket, the end's CTAs' shares of the loss (64)
