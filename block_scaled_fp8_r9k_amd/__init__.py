@@ -781,6 +781,14 @@ def quant_i8(x: torch.Tensor, q=None, s=None, stream=None):
     """Rows to signed bytes with a scale each (r9k_quant_i8): x [..., K] bf16 -> (codes [..., K] int8, scales [...] fp32).
     Activations per token; a weight [..., N, K] per output channel, at load time."""
     dev = _dev(x, "x")
+    if (q is not None and s is not None and x.dtype in BF16 and q.dtype in I8 and s.dtype in F32 and q.shape == x.shape
+            and len(x.shape) and s.shape == x.shape[:-1] and x.is_contiguous() and q.is_contiguous() and s.is_contiguous()
+            and q.get_device() == s.get_device() == dev):  # as in gemm_i8
+        rows = s.numel()
+        rc = lib().r9k_quant_i8(x.data_ptr(), rows, x.shape[-1], q.data_ptr(), s.data_ptr(), _raw(stream, dev)) if rows else 0
+        if rc:
+            _check(rc, "r9k_quant_i8")
+        return q, s
     px = _addr(x, BF16, "x", dev)
     if x.dim() < 1:
         raise ValueError("x has no rows")
@@ -900,6 +908,20 @@ def moe_gemm_i8(xq, xs, offsets, wp, ws, src=None, topk: int = 1, act: str = "no
         raise ValueError(f"activations {tuple(xq.shape)} need two sizes, the experts' weight {tuple(wp.shape)} three and "
                          "some values")
     (rows, K), (E, N) = xq.shape, wp.shape[:2]
+    if (c is not None and xq.dtype in I8 and xs.dtype in F32 and wp.dtype in I8 and ws.dtype in F32 and offsets.dtype in I32
+            and c.dtype in BF16 and wp.shape[2] == K and xs.shape == (rows,) and ws.shape == (E, N) and offsets.shape == (E + 1,)
+            and xq.is_contiguous() and xs.is_contiguous() and wp.is_contiguous() and ws.is_contiguous()
+            and offsets.is_contiguous() and c.is_contiguous()
+            and xs.get_device() == wp.get_device() == ws.get_device() == offsets.get_device() == c.get_device() == dev
+            and (src is None or (src.dtype in I32 and src.is_contiguous() and src.get_device() == dev))):  # as in gemm_i8
+        R = rows if src is None else src.numel()
+        if R and c.shape == (R, N if act == "none" else N // 2):
+            rc = lib().r9k_moe_gemm_i8(xq.data_ptr(), xs.data_ptr(), rows, None if src is None else src.data_ptr(), topk,
+                                       offsets.data_ptr(), E, R, K, wp.data_ptr(), ws.data_ptr(), N, _ACTS[act], c.data_ptr(),
+                                       _raw(stream, dev))
+            if rc:
+                _check(rc, "r9k_moe_gemm_i8")
+            return c
     px, pxs = _addr(xq, I8, "xq", dev), _addr(xs, F32, "xs", dev, (rows,))
     pw, ps = _addr(wp, I8, "wp", dev, (E, N, K)), _addr(ws, F32, "ws", dev, (E, N))
     po = _addr(offsets, I32, "offsets", dev, (E + 1,))

@@ -244,3 +244,32 @@ def test_refusals_with_every_output_given(r9k):
                       ((gw, ids.cpu(), tw), ValueError), ((gw, ids.long(), tw), TypeError), ((gw, ids, tw.half()), TypeError)):
         with pytest.raises(err):
             r9k.moe_route_backward(*args, 8)
+
+
+def test_refusals_of_quantiser_and_experts_with_outputs_given(r9k):
+    T, K, E, N = 6, 256, 3, 32
+    x = acts(T, K, 1).cuda()
+    q, s = r9k.quant_i8(x)
+    for bad, err in ((dict(q=q[:2]), ValueError), (dict(q=q.t()), ValueError), (dict(q=q.cpu()), ValueError), (dict(q=q.float()), TypeError),
+                     (dict(s=s[:2]), ValueError), (dict(s=s[:, None]), ValueError), (dict(s=s.half()), TypeError), (dict(x=x.t()), ValueError),
+                     (dict(x=x.float()), TypeError)):
+        v = dict(x=x, q=q, s=s) | bad
+        with pytest.raises(err):
+            r9k.quant_i8(v["x"], q=v["q"], s=v["s"])
+    q2, s2 = torch.zeros_like(q), torch.zeros_like(s)
+    assert r9k.quant_i8(x, q=q2, s=s2)[0] is q2 and torch.equal(q2, q) and torch.equal(s2, s)
+    w = weight((E, N), K, 2)
+    p, ws = r9k.pack_weight_i8(w[0].cuda()), w[1].cuda()
+    off, src = torch.tensor([0, 2, 3, 6], dtype=torch.int32).cuda(), torch.tensor([3, 1, 0, 5, 4, 2], dtype=torch.int32).cuda()
+    c = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    ok = dict(xq=q, xs=s, offsets=off, wp=p, ws=ws, src=src, c=c)
+    for bad, err in ((dict(c=c[:2]), ValueError), (dict(c=c[:, :16]), ValueError), (dict(c=c.cpu()), ValueError), (dict(c=c.half()), TypeError),
+                     (dict(xs=s[:2]), ValueError), (dict(xs=s.half()), TypeError), (dict(offsets=off[:3]), ValueError),
+                     (dict(offsets=off.long()), TypeError), (dict(offsets=off.cpu()), ValueError), (dict(ws=ws[:2]), ValueError),
+                     (dict(ws=ws.t()), ValueError), (dict(wp=p[:, :, :128].contiguous()), ValueError), (dict(wp=p[:2]), ValueError),
+                     (dict(src=src.long()), TypeError), (dict(src=src.cpu()), ValueError), (dict(src=src[::2], c=c[:3]), ValueError),
+                     (dict(xq=q.t()), ValueError), (dict(act="silu_mul"), ValueError)):
+        with pytest.raises(err):
+            r9k.moe_gemm_i8(**(ok | bad))
+    assert torch.equal(r9k.moe_gemm_i8(**ok), r9k.moe_gemm_i8(**(ok | dict(c=None))))
+    assert torch.equal(r9k.moe_gemm_i8(**(ok | dict(src=None))), r9k.moe_gemm_i8(**(ok | dict(c=None, src=None))))
