@@ -231,11 +231,7 @@ __global__ __launch_bounds__(MT * NT == 1 ? 1024 : 512) void k_gemm_i8(I8Args p)
         for (int i = 1; i < MT; ++i) a = m == i ? as[i] : a;
         const float *ws = p.ws + (int64_t)e * p.N + 16 * t + 4 * q;
         v4f y = i8_scale(x, a, *(const float4 *)ws);
-        if (p.silu) {
-            const v4f u = i8_scale(total(j + nt), a, *(const float4 *)(ws + p.N / 2));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = i8_silu_mul(y[i], u[i]);
-        }
+        if (p.silu) y = i8_silu_mul(y, i8_scale(total(j + nt), a, *(const float4 *)(ws + p.N / 2)));
         __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(w4_v2u, w4_bf16x4(y)), out, 2 * at, 0, 0);
     }
 }

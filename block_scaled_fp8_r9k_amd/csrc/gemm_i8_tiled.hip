@@ -368,11 +368,7 @@ __global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW * T::KG + 3) / 4) void
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     v4f y = i8_scale(acc[i][j], as[j], ws[i]);
-                    if constexpr (SILU) {
-                        const v4f u = i8_scale(acc[i + NT][j], as[j], ws[i + NT]);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) y[r] = i8_silu_mul(y[r], u[r]);
-                    }
+                    if constexpr (SILU) y = i8_silu_mul(y, i8_scale(acc[i + NT][j], as[j], ws[i + NT]));
                     const int piece = (2 * i + (q >> 1)) ^ ((l16 * PR >> 4) & (PR - 1));
                     *(uint2 *)(mine + (l16 * PR + piece) * 16 + 8 * (q & 1)) = w4_bf16x4(y);
                 }

@@ -33,15 +33,44 @@ __device__ __forceinline__ v4f i8_scale(v4i x, float as, float4 ws) {
 }
 
 // silu(g) * u = g sigma(g) u, sigma from e = exp(-|g|): 1 / (1 + e), or e / (1 + e) where g < 0.  The exponent's
-// product with log2 e is taken in two parts, so that e is v_exp_f32's result to its last place for every g; 1 + e, v_rcp_f32
-// (one unit) and three products round: 8 * 2^-24 in all.  (The division and expf of the fp32 library cost twice as
-// many instructions; with them a tile of 256 x 256 spent 9.8 us on its outputs, without silu 4.1.)
-__device__ __forceinline__ float i8_silu_mul(float g, float u) {
-    const float a = fmaxf(-fabsf(g), -200.0f), hi = a * 1.44269502f;
-    const float lo = __builtin_fmaf(a, 1.92596299e-8f, __builtin_fmaf(a, 1.44269502f, -hi));  // log2 e = 1.44269502f + 1.925963e-8
-    const float e0 = __builtin_amdgcn_exp2f(hi), e = __builtin_fmaf(e0, lo * 0.693147182f, e0);
+// product with log2 e is taken in two parts, so that e is v_exp_f32's result to its last place; 1 + e, v_rcp_f32
+// (one unit) and three products round: 8 * 2^-24 in all.  Below 2^-126, from g = -87.34 on, v_exp_f32 gives 0: such gates
+// are i8_silu_far's.  (The division and expf of the fp32 library cost twice as many instructions; with them a tile of
+// 256 x 256 spent 9.8 us on its outputs, without silu 4.1.)
+struct I8Log2 {  // x log2 e = hi + lo; log2 e = 1.44269502f + 1.92596299e-8f
+    float hi, lo;
+};
+__device__ __forceinline__ I8Log2 i8_log2e(float x) {
+    const float hi = x * 1.44269502f;
+    return {hi, __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, 1.44269502f, -hi))};
+}
+__device__ __forceinline__ float i8_silu_near(float g, float u) {
+    const I8Log2 p = i8_log2e(fmaxf(-fabsf(g), -200.0f));
+    const float e0 = __builtin_amdgcn_exp2f(p.hi), e = __builtin_fmaf(e0, p.lo * 0.693147182f, e0);
     const float s = (g < 0.0f ? e : 1.0f) * __builtin_amdgcn_rcpf(1.0f + e);
     return g * s * u;
+}
+// g < -87.3: 1 + e is 1, and u takes the whole powers of two of e before the rest of it, which is near 1, and g
+// follow.  Where u becomes subnormal it loses at most 2^-150, the output 2^-141 (bf16's smallest step is 2^-133).  At
+// g = -300 the output of the largest u is 0.
+__device__ __forceinline__ float i8_silu_far(float g, float u) {
+    const I8Log2 p = i8_log2e(fmaxf(g, -300.0f));
+    const float n = __builtin_rintf(p.hi), m0 = __builtin_amdgcn_exp2f(p.hi - n), m = __builtin_fmaf(m0, p.lo * 0.693147182f, m0);
+    return __builtin_amdgcn_ldexpf(u, (int)n) * m * g;
+}
+// Four of them.  Far gates are rare: the wave looks once for its 256 whether there is one (the branch is the wave's, no
+// lane is masked, and what it skips lies behind the kernel).  The look costs 0.3 to 1%: gate_up of 2048 tokens 101.5 us, 100.7
+// without; with every gate far-proof by itself it would be seven instructions an output.
+__device__ __forceinline__ v4f i8_silu_mul(v4f g, v4f u) {
+    constexpr float far = -87.3f;
+    v4f y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = i8_silu_near(g[i], u[i]);
+    if (__builtin_expect(__ballot(fminf(fminf(g[0], g[1]), fminf(g[2], g[3])) < far) != 0, 0)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = g[i] < far ? i8_silu_far(g[i], u[i]) : y[i];
+    }
+    return y;
 }
 
 // A row's quantisation: b = max(amax, 1e-10) from the largest bf16 bit pattern; with an infinity
