@@ -24,7 +24,7 @@ from ctypes import POINTER, c_char_p, c_int, c_int64, c_size_t, c_void_p
 
 import torch
 
-ABI_VERSION = 11
+ABI_VERSION = 12
 ENGINE_AUTO, ENGINE_SKINNY, ENGINE_TILED, ENGINE_SPLITK = 0, 1, 2, 3
 TILE_AUTO, TILE_256X256, TILE_256X128, TILE_128X64, TILE_256X64 = 0, 1, 2, 3, 4
 
@@ -100,6 +100,7 @@ def lib() -> ctypes.CDLL:
         L.r9k_quant_i8.argtypes = [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p]
         L.r9k_pack_weight_i8.argtypes = [c_void_p, c_int64, c_int64, c_void_p, c_void_p]
         L.r9k_gemm_i8_workspace.argtypes = [c_int64, c_int64, c_int64, POINTER(c_size_t)]
+        L.r9k_gemm_i8_codes_workspace.argtypes = L.r9k_gemm_i8_workspace.argtypes
         L.r9k_gemm_i8.argtypes = L.r9k_gemm_fp8_block.argtypes
         L.r9k_gemm_i8_qa.argtypes = L.r9k_gemm_fp8_block_qa.argtypes
         L.r9k_moe_gemm_i8.argtypes = [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64,
@@ -818,10 +819,14 @@ def pack_weight_i8(wq: torch.Tensor, stream=None) -> torch.Tensor:
 
 
 @functools.lru_cache(maxsize=4096)
-def gemm_i8_workspace(M: int, K: int, N: int) -> int:
-    """Workspace bytes for gemm_i8 and gemm_i8_qa of this shape (r9k_gemm_i8_workspace)."""
+def gemm_i8_workspace(M: int, K: int, N: int, quant: bool = True) -> int:
+    """Workspace bytes for gemm_i8 and gemm_i8_qa of this shape (r9k_gemm_i8_workspace); with quant=False for gemm_i8
+    alone (r9k_gemm_i8_codes_workspace), which has no codes to keep: 0 unless K is split."""
     b = c_size_t(0)
-    _check(lib().r9k_gemm_i8_workspace(M, K, N, ctypes.byref(b)), "r9k_gemm_i8_workspace")
+    if quant:
+        _check(lib().r9k_gemm_i8_workspace(M, K, N, ctypes.byref(b)), "r9k_gemm_i8_workspace")
+    else:
+        _check(lib().r9k_gemm_i8_codes_workspace(M, K, N, ctypes.byref(b)), "r9k_gemm_i8_codes_workspace")
     return b.value
 
 
@@ -848,7 +853,7 @@ def gemm_i8(aq, as_, wp, ws, c=None, workspace=None, stream=None) -> torch.Tenso
                 and aq.is_contiguous() and as_.is_contiguous() and wp.is_contiguous() and ws.is_contiguous()
                 and c.is_contiguous()
                 and as_.get_device() == wp.get_device() == ws.get_device() == c.get_device() == dev):
-            need = gemm_i8_workspace(M, K, N)
+            need = gemm_i8_workspace(M, K, N, False)
             pws, nb, _keep = (None, 0, None) if need == 0 else _scratch(workspace, need, dev, stream)
             rc = lib().r9k_gemm_i8(aq.data_ptr(), as_.data_ptr(), M, K, wp.data_ptr(), ws.data_ptr(), N, c.data_ptr(),
                                    pws, nb, _raw(stream, dev))
@@ -859,7 +864,7 @@ def gemm_i8(aq, as_, wp, ws, c=None, workspace=None, stream=None) -> torch.Tenso
     pa, pas = _addr(aq, I8, "aq", dev), _addr(as_, F32, "as", dev, (M,))
     if M == 0:  # an empty batch: nothing to compute (an empty tensor has no device address to pass)
         return c
-    pws, nb, _keep = _scratch(workspace, gemm_i8_workspace(M, K, N), dev, stream)
+    pws, nb, _keep = _scratch(workspace, gemm_i8_workspace(M, K, N, False), dev, stream)
     rc = lib().r9k_gemm_i8(pa, pas, M, K, pw, ps, N, pc, pws, nb, _raw(stream, dev))
     if rc:
         _check(rc, "r9k_gemm_i8")

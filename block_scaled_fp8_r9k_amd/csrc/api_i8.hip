@@ -81,13 +81,19 @@ static hipError_t launch_i8(const I8Args &a, const I8Plan &p, hipStream_t s) {
     return p.tile ? launch_gemm_i8_tiled(a, p.tiled, s) : launch_gemm_i8(a, p.cfg, s);
 }
 
-int r9k_gemm_i8_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes) {
+static int i8_workspace(int64_t M, int64_t K, int64_t N, std::initializer_list<bool> forms, size_t *bytes) {
     if (!bytes) return R9K_ERR_NULLPTR;
     if (M < 0 || M > MAX_DIM || !i8_shape(N, K, 16)) return R9K_ERR_SHAPE;
     *bytes = 0;
-    for (const bool quant : {false, true})
+    for (const bool quant : forms)
         if (M) *bytes = std::max(*bytes, i8_layout(M, K, N, i8_plan(M, K, N, 0, false, quant), quant).total);
     return R9K_OK;
+}
+int r9k_gemm_i8_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes) {
+    return i8_workspace(M, K, N, {false, true}, bytes);
+}
+int r9k_gemm_i8_codes_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes) {
+    return i8_workspace(M, K, N, {false}, bytes);
 }
 
 static int run_gemm_i8(const uint16_t *a, const int8_t *aq, const float *as, int64_t M, int64_t K, const int8_t *wp,

@@ -60,7 +60,7 @@ extern "C" {
 #pragma GCC visibility push(default)
 #endif
 
-#define R9K_ABI_VERSION 11
+#define R9K_ABI_VERSION 12
 
 /* Return codes: 0 or negative, as the pages' kernels return them (release
  * v0.3.0, its validation record: a test failing "with the kernel's -7").
@@ -78,7 +78,8 @@ extern "C" {
  * routing and the shared-expert fold, 5 the bf16-activation variant, 6 the
  * mid-width kernel in the plan query, 7 the allocation-free GEMM entry point, 8 the tiled-plan
  * control and R9K_ENGINE_SPLITK, 9 the 4-bit weights and the rows sorted by expert, 10 their plan
- * query and control, 11 the 8-bit integer products and the router's training operators).  Callers refuse
+ * query and control, 11 the 8-bit integer products and the router's training operators, 12 the workspace query of products
+ * from codes).  Callers refuse
  * a library whose version differs from the header they were built against:
  * the convention of the pages' plugin, which refuses an older libr9k.so
  * (release v0.2.2, "Upgrading").  Host only; cannot fail. */
@@ -603,6 +604,10 @@ int r9k_pack_weight_i8(const int8_t *wq, int64_t N, int64_t K, int8_t *wp, void 
  * only; 0 for M = 0).  Needs no initialisation; calls sharing one must not overlap in time.
  * Errors: NULLPTR (bytes); SHAPE as for the calls. */
 int r9k_gemm_i8_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes);
+
+/* The same for r9k_gemm_i8 alone, which has no activations to quantise: the sums of a K split, 0 where
+ * the plan has none.  Errors: as r9k_gemm_i8_workspace. */
+int r9k_gemm_i8_codes_workspace(int64_t M, int64_t K, int64_t N, size_t *bytes);
 
 /* The product of codes, any number of rows.
  *   aq [M][K], as [M], wp packed, ws [N] -> c [M][N] bf16.

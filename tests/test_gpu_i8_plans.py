@@ -108,3 +108,19 @@ def test_streaming_experts(r9k, experts, shape):
 def test_tiled_experts(r9k, experts, tile):
     r9k.set_i8_plan(r9k.I8_TILED, *tile)
     run_experts(r9k, experts, f"tiled {tile}")
+
+
+def test_a_product_from_codes_allocates_its_output_alone(r9k):
+    r9k.set_i8_plan()
+    M, K, N = 2048, 4096, 512
+    w = weight((N,), K, 1)
+    p, ws = r9k.pack_weight_i8(w[0].cuda()), w[1].cuda()
+    q, s = r9k.quant_i8(acts(M, K, 2).cuda())
+    want = r9k.gemm_i8(q, s, p, ws)
+    split = r9k.gemm_i8_workspace(M, K, N, quant=False)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    c = r9k.gemm_i8(q, s, p, ws)
+    assert torch.cuda.max_memory_allocated() - before <= c.numel() * 2 + split + 1024 < M * K + split
+    assert torch.equal(c, want)

@@ -1,6 +1,7 @@
 """The 8-bit products' planner on the host (plans are made without a device): every plan is one that the kernels have, the
 workspace covers it, every launch is somebody's; the plan control's refusals; and the wait states before the tiled kernel's
 loads into LDS."""
+import ctypes
 import math
 import os
 import random
@@ -8,6 +9,7 @@ import random
 import pytest
 
 import block_scaled_fp8_r9k_amd as r9k
+from tests.test_abi import _gpu_present
 from tests.test_i8_host import _need
 from tests.test_isa_lds_loads import short_waits
 from tests.test_isa_mfma_exec import CSRC, HIPCC, _device_asm
@@ -90,3 +92,26 @@ def test_tiled_loads_wait_for_their_address(tmp_path):
     with open(_device_asm(os.path.join(CSRC, "gemm_i8_tiled.hip"), str(tmp_path))) as f:
         loads, bad = short_waits(f.read())
     assert loads > 100 and not bad, bad[:3]
+
+
+def test_codes_need_no_room_for_codes():
+    """The workspace of a product from codes holds a split's sums alone, and what the query says is what the call takes."""
+    assert r9k.gemm_i8_workspace(4096, 4096, 12288, quant=False) == 0
+    assert r9k.gemm_i8_workspace(4096, 4096, 12288) >= 4096 * (4096 + 4)
+    rng = random.Random(5)
+    P = [ctypes.c_void_p(i << 40) for i in range(1, 7)]
+    for n in range(600):
+        if n % 3 == 0:
+            r9k.set_i8_plan(r9k.I8_TILED, *rng.choice(TILES), 0, rng.randint(0, 5))
+        M, K, N = sizes(rng, 1, 1 << 14), sizes(rng, 128, 130944, 128), sizes(rng, 16, 1 << 15, 16)
+        need, ks = r9k.gemm_i8_workspace(M, K, N, quant=False), r9k.i8_plan(M, K, N)[4]
+        assert need == (0 if ks == 1 else (ks * M * N * 4 + 255) // 256 * 256), (M, K, N, ks)
+        assert need <= r9k.gemm_i8_workspace(M, K, N)
+        call = lambda room: r9k.lib().r9k_gemm_i8(P[0], P[1], M, K, P[2], P[3], N, P[4], P[5], room, None)
+        if need:
+            assert call(need - 1) == -6, (M, K, N)
+        if not _gpu_present():
+            assert call(need) == -4, (M, K, N)
+    f = r9k.lib().r9k_gemm_i8_codes_workspace
+    b = ctypes.c_size_t(7)
+    assert f(1, 128, 16, None) == -1 and f(1, 100, 16, ctypes.byref(b)) == -2 and f(0, 128, 16, ctypes.byref(b)) == 0 == b.value
