@@ -342,7 +342,7 @@ __global__ __launch_bounds__(T::THREADS, (T::CTAS * T::NW * T::KG + 3) / 4) void
         // or column fall behind their descriptor's end and are dropped, so that every wave issues as many.
         const int l = fresh(), l16 = l & 15, q = l >> 4;
         const int have = max(0, now.rows - wm * TM * 16);  // rows of the wave that exist (at most 64)
-        const int64_t row0 = now.r0 + wm * TM * 16;
+        const int64_t row0 = (int64_t)now.r0 + wm * TM * 16;
         if (p.ksplit > 1) {
             const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
                 (void *)(p.part + ((int64_t)now.ks * p.M + row0) * p.N), (short)0,

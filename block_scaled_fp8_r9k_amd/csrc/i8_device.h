@@ -115,7 +115,7 @@ struct I8Blocks {
 #pragma unroll
         for (int i = 0; i < 5; ++i) o[i] = min(max(o[i], 0), R);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) n += (max(o[i + 1], o[i]) - o[i] + RB - 1) >> sh;
+        for (int i = 0; i < 4; ++i) n += w4_row_blocks(o[i], o[i + 1], sh);
         incl = w4_wave_scan(n);
     }
     __device__ __forceinline__ bool find(int item, int RB, int &e, int &r0, int &r1) const {
@@ -125,7 +125,7 @@ struct I8Blocks {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int a = __builtin_amdgcn_readlane(o[i], l), z = __builtin_amdgcn_readlane(o[i + 1], l);
-            const int b = (max(z, a) - a + RB - 1) >> sh;
+            const int b = w4_row_blocks(a, z, sh);
             if (item < b) {
                 e = 4 * l + i;
                 r0 = a + (item << sh);

@@ -86,6 +86,11 @@ __device__ __forceinline__ int w4_wave_scan(int v) {
     return v;
 }
 
+// Blocks of 2^sh rows that rows [a, z) make; up to 2^31 - 1 rows, which a block's more would carry past int.
+__device__ __forceinline__ int w4_row_blocks(int a, int z, int sh) {
+    return (int)(((uint32_t)(max(z, a) - a) + (1u << sh) - 1) >> sh);
+}
+
 // Row block `item` of the experts' row ranges [offsets[e], offsets[e+1]), RB
 // rows (a power of two) to a block, blocks counted expert by expert: the expert, and
 // its rows from the block's first on; false if there are fewer blocks.  Every wave
@@ -104,7 +109,7 @@ __device__ __forceinline__ bool w4_find_block(const int32_t *offsets, int E, int
         for (int i = 0; i < 5; ++i) o[i] = min(max(o[i], 0), R);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            nb[i] = (max(o[i + 1], o[i]) - o[i] + RB - 1) >> sh;  // none past the last expert
+            nb[i] = w4_row_blocks(o[i], o[i + 1], sh);  // none past the last expert
             n += nb[i];
         }
         const int incl = w4_wave_scan(n), total = __builtin_amdgcn_readlane(incl, 63);

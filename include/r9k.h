@@ -631,7 +631,7 @@ int r9k_gemm_i8_qa(const uint16_t *a, int64_t M, int64_t K, const int8_t *wp, co
  *   at most R); wp: E weights of N rows packed as one, ws [E][N] -> c.
  * offsets and src are device data the host cannot check: offsets are held to
  * [0, R], and an index outside a reads row 0.
- * Errors: NULLPTR (aq, as, offsets, wp, ws, c); SHAPE if R < 0, arows < 1 (with R > 0), E < 1 or
+ * Errors: NULLPTR (aq, as, offsets, wp, ws, c); SHAPE if R < 0 or >= 2^31, arows < 1 (with R > 0) or >= 2^31, E < 1 or
  * > 2048, topk < 1, K as above, N not a positive multiple of 16 (of 32 with silu), R > arows *
  * topk with src, or R > arows without; ARG for an unknown act or an overlap; ALIGN; DEVICE;
  * LAUNCH.  R = 0 launches nothing. */
