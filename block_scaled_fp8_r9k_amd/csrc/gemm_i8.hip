@@ -17,9 +17,9 @@
 // columns that belong to them.
 //
 // Weight bytes bound it, read once: a launch has few rows to meet them, and matrix instructions take 6% of the cycles.
-// From memory: gate_up of 16 tokens, 2048 -> 2 x 768 of 128 experts, 41 us for 250 MB, 6 TB/s; 16 rows of 14336 x 4096
-// 13.8 us for 59 MB, 4.3 TB/s, of which the launch, the first loads' way and the sums' way through LDS are 3 us; one row
-// of 4096 x 14336 with its quantisation 10.9 us, 5.4 TB/s.
+// Kernel trace, weights from memory: gate_up of 16 tokens, 2048 -> 2 x 768 of 128 experts, 41 us for 250 MB, 6 TB/s; 16 rows of
+// 14336 x 4096 14.1 us for 59 MB, 4.2 TB/s, of which the launch, the first loads' way and the sums' way through LDS are 3 us;
+// one row of 4096 x 14336 with its quantisation 11.8 us, 5.0 TB/s.
 #include <algorithm>
 
 #include "r9k.h"
@@ -262,7 +262,7 @@ hipError_t launch_i8_reduce(const I8Args &a, int ksplit, hipStream_t s) {
 //
 // Streaming: a compute unit's busiest CTAs move W (weight blocks of 2 KiB) and A (activation blocks as large), and each of
 // its turns is as long as a wave's slice.  A split adds its sums and the reduce launch.  E.g. one row of 4096 x 14336: 11.9 us
-// in eight slices, 12.6 in four; of 4096 x 4096 5.5 and 6.1; 16 rows of 14336 x 4096 14.0 whole, 14.1 split.
+// in eight slices, 12.7 in four; of 4096 x 4096 5.4 and 6.1; 16 rows of 14336 x 4096 14.4 whole, 17.7 in two.
 static double stream_us(const I8Cfg &c, int64_t M, int64_t K, int64_t N, int64_t E, bool silu, double blocks) {
     const int64_t C = K / 128, span = (C + c.ksplit - 1) / c.ksplit, cps = (span + c.wk - 1) / c.wk, tiles = N / 16;
     const int waves = c.wn * c.wk, per = (int)cps * (c.nt + c.mt);
@@ -286,9 +286,10 @@ static double stream_us(const I8Cfg &c, int64_t M, int64_t K, int64_t N, int64_t
 }
 
 // Tiled: a stage takes `alone` where its CTA has the compute unit to itself and `shared` for each of those that share
-// it, each tile its start and its outputs.  E.g. 4096 x 4096 x 12288: 178 us in tiles of 256 x 256, 220 in 256 x 128,
-// 243 in 128 x 128; 2048 x 4096 x 4096 51, 37, 42; 256 x 4096 x 4096 12.5 in 64 x 64, 19.2 in 64 x 128, 19.8 in 128 x 128;
-// 100 x 4096 x 4096 11.6 in 64 x 64, streaming 12.8; gate_up of 64 tokens, eight of 128 experts, 70 in 128 x 64, 74 in 64 x 64.
+// it, each tile its start and its outputs.  E.g. from codes 4096 x 4096 x 12288: 168 us in tiles of 256 x 256, 219 in 256 x 128,
+// 244 in 128 x 128; 2048 x 4096 x 4096 48, 35, 41; 256 x 4096 x 4096 12.4 in 64 x 64, 18.8 in 64 x 128, 22.9 in 128 x 128;
+// 100 x 4096 x 4096 11.5 in 64 x 64, streaming 14.1, and 64 rows 12.6 and 8.5; gate_up of 64 tokens, eight of 128 experts, 72
+// in 128 x 64, 74 in 64 x 64, of 2048 tokens 108 in 256 x 256, 130 in 256 x 128, 124 in 128 x 128.
 static double tiled_us(const I8TiledCfg &c, int64_t M, int64_t K, int64_t N, int64_t E, bool silu, double blocks) {
     static constexpr double dense[][3] = {{0.341, 0.0385, 3.3}, {0.243, 0.349, 1.27}, {0.238, 0.201, 1.05},
                                      {0.281, 0.244, 0.148}, {0.211, 0.15, 1.14}, {0.0993, 0.122, 0.746}};

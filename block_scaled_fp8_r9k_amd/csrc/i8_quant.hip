@@ -7,7 +7,8 @@
 // multiplication an element; the two rules give the same code except next to a tie.
 // One pass: a row's values stay in registers between its maximum and its codes (rows past
 // 16384 values are read again, from the caches).  Bytes bound it: 16384
-// rows of 768 in 8.7 us for 38 MB, 4.4 TB/s; 100 rows of 4096 2.6 us, most of it the launch.
+// rows of 768 in 8.9 us for 38 MB, 4.2 TB/s, in a kernel trace with the rows from memory; 100 rows of 4096 2.7 us, most of it
+// the launch.
 #include "i8_device.h"
 #include "i8_internal.h"
 
@@ -52,8 +53,8 @@ __global__ __launch_bounds__(256) void k_quant_i8(const uint4 *__restrict__ x, i
 }
 
 hipError_t launch_quant_i8(const uint16_t *x, int64_t rows, int64_t K, int8_t *q, float *s, hipStream_t st) {
-    // A wave a row, else a CTA a row.  16384 x 768: 7.0 and 13.3 us; 4096 x 4096 8.8 and 9.8; 512 x 4096 3.3 and 2.8, few
-    // rows having too few waves.
+    // A wave a row, else a CTA a row.  In graphs, the rows partly from the caches: 16384 x 768 7.1 and 13.3 us; 4096 x 4096 8.8
+    // and 9.8; 512 x 4096 3.3 and 2.9, few rows having too few waves.
     const bool wave = K <= 4096 && rows >= 1024;
     const int64_t blocks = std::min<int64_t>(wave ? (rows + 3) / 4 : rows, 1 << 20);
     auto go = [&](auto kernel) {

@@ -138,8 +138,9 @@ struct Max {
 };
 
 // exp(x - max) in place of the token's logits (experts past E as -inf); returns 1 / their sum, 0 where
-// every logit is -inf.  exp is v_exp_f32 of the difference times log2 e: off by two roundings of the difference and one
-// of its own, and 0 below 2^-126; the reciprocal v_rcp_f32's, one rounding off.
+// every logit is -inf.  exp is v_exp_f32 of the difference d to the maximum times log2 e: d, the product and the constant each
+// round once, which moves the result by up to 2.2 d 2^-24 of itself (7 units of 2^-24 at d = 3, 66 at 30, where the
+// probability is 1e-13), and v_exp_f32 by one unit more; 0 below 2^-126; the reciprocal v_rcp_f32's, one rounding off.
 template <int LPT, int VEC, int NV>
 __device__ __forceinline__ float softmax(float (&x)[NV][VEC]) {
     float mx = -__builtin_inff(), sum = 0.0f;
@@ -176,9 +177,9 @@ __device__ __forceinline__ void put_loss(const BalanceArgs &p, double dot, int k
 }
 
 // A CTA's tokens, consecutive ones: their probabilities and counts, into its part of the
-// workspace, or with one CTA the outputs.  65536 tokens of 256 experts in bf16: 12 us for 36 MB,
-// 2.9 TB/s; each of the 256 CTAs, one a compute unit, asks for its rows in about eight steps, and its start, the
-// histogram and its waves' sums are not hidden behind them.  1023 tokens of 128 in fp32: 5.2 us.
+// workspace, or with one CTA the outputs.  Kernel trace, medians: 65536 tokens of 256 experts in bf16 12.8 us for 36 MB,
+// 2.8 TB/s, in fp32 17.1 us for 69 MB, 4 TB/s; each of the 256 CTAs, one a compute unit, asks for its rows in about eight (16)
+// steps, and its start, the histogram and its waves' sums are not hidden behind them.  1023 tokens of 128 in fp32: 5.2 us.
 template <bool F32, int VEC, int NV, int LPT>
 __global__ __launch_bounds__(64 * balance_waves(NV * VEC)) void k_balance(BalanceArgs p, int64_t per) {
     constexpr int U = NV == 1 ? 4 : 1, L = 1 << LPT, TPW = 64 >> LPT;
@@ -277,8 +278,8 @@ __global__ __launch_bounds__(64 * balance_waves(NV * VEC)) void k_balance(Balanc
 
 // The parts, added up, and the loss.  A CTA takes 32 columns: a thread four of them, every 32nd part.  With more
 // than one CTA each leaves its share of the loss in the workspace, and the last to arrive (the ticket starts at 0
-// in the launch before) adds them in their order, so that the order of arrival does not show.  256 parts of
-// 256 columns: 5.8 us, 16 of 128: 4.4, the launch, a load of other CTAs' sums and the ticket in turn.
+// in the launch before) adds them in their order, so that the order of arrival does not show.  Kernel trace, medians: 256
+// parts of 256 columns 6.3 us, 16 of 128 4.6, the launch, a load of other CTAs' sums and the ticket in turn.
 __global__ __launch_bounds__(256) void k_balance_end(BalanceArgs p, int parts) {
     __shared__ __align__(16) v4f sp[4][8];
     __shared__ __align__(16) v4i sc[4][8];
@@ -352,8 +353,9 @@ __global__ __launch_bounds__(256) void k_balance_end(BalanceArgs p, int parts) {
 // The gradient of the logits: with gloss the balance loss's part, with gw the routing weights'.  The
 // latter goes through the wave's own LDS: the token's row is cleared there, its slots put
 // their terms in, and the lanes take their experts' back.  Slots that share an expert (seen by a tag that each slot
-// leaves and reads again) add theirs one after another, in ascending order.  Bytes bound it: 65536 tokens of 256 in
-// fp32, both parts, 27.4 us for 140 MB, 5.1 TB/s; 8191 of 128 6.1 us, 512 of 8 2.7, of which a launch is most.
+// leaves and reads again) add theirs one after another, in ascending order.  Bytes bound it where tokens are many: kernel trace,
+// medians, 65536 tokens of 256 in fp32, both parts, 30.1 us for 140 MB, 4.7 TB/s; 8191 of 128 6.1 us for 9 MB, the counts'
+// way and one step's, whose second half lies past the last token as long as the grid covers them all; 512 of 8 2.8, a launch.
 template <bool F32, int VEC, int NV, int LPT>
 __global__ __launch_bounds__(256) void k_router_bwd(RouterGradArgs p) {
     constexpr int U = NV == 1 ? 2 : 1, L = 1 << LPT, TPW = 64 >> LPT, ROW = L * NV * VEC;
@@ -468,7 +470,8 @@ __global__ __launch_bounds__(256) void k_route_bwd_wide(RouterGradArgs p) {
 }
 
 // The instance for E experts and at least `lanes` lanes a token: 16-byte pieces where every row begins on
-// 16 bytes.
+// 16 bytes.  Past 64 pieces a row there are two lengths only, so that a row of 65 single experts costs one of 512: loss and both
+// gradients of 65536 tokens in fp32, in graphs, 13.9 and 13.8 us at 64 experts, 17.1 and 18.6 at 100, 27.1 and 40.6 at 65.
 template <class GO>
 static hipError_t by_shape(int64_t E, int64_t lanes, bool f32, GO go) {
     auto sized = [&](auto F, auto V) {
